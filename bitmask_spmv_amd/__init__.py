@@ -29,7 +29,9 @@ __all__ = [
     "nm_obs_inverse_factor_workspace_bytes", "nm_sparsegpt_prune_pack", "nm_sparsegpt_workspace_bytes",
     "nm_stream_read", "nm_stream_read_sink_words", "nm_spmv_plan", "nm_spmv_multi_plan", "NM_EPI_NONE",
     "NM_EPI_SWIGLU", "NM_KERNEL_WORD", "NM_KERNEL_TILE", "NM_KERNEL_WORD_HALF_ROWS", "NM_KERNEL_WORD_STRIPS",
-    "nm_spmv_noalloc",
+    "nm_spmv_noalloc", "nm_kv4_page_bytes", "nm_kv4_append", "nm_kv4_unpack", "nm_kv4_attention",
+    "nm_kv4_attention_workspace_bytes", "nm_kv_pages_workspace_bytes", "nm_kv_resize", "nm_kv_fork",
+    "nm_kv_compact", "nm_kv_copy_pages",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnmspmv.so")
@@ -111,6 +113,23 @@ def _load() -> ctypes.CDLL:
     L.nm_stream_read.argtypes, L.nm_stream_read.restype = [p, sz, p, sz, p], i32
     L.nm_spmv_plan.argtypes, L.nm_spmv_plan.restype = [i64, i64, i32, i32, p], i32
     L.nm_spmv_multi_plan.argtypes, L.nm_spmv_multi_plan.restype = [p, i32, i64, i32, p], i32
+    f32 = ctypes.c_float
+    L.nm_kv4_page_bytes.argtypes, L.nm_kv4_page_bytes.restype = [i32, i32, i32], i64
+    batch = [i64, i32, i32, i32, p, i64, i32, p, p, i64]  # num_pages .. S
+    L.nm_kv4_append.argtypes = [p, i64, i64, p, i64, i64, i64, p, *batch, p]
+    L.nm_kv4_unpack.argtypes = [p, *batch, i64, p, i64, i64, p, i64, i64, p]
+    L.nm_kv4_attention_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i64]
+    L.nm_kv4_attention_workspace_bytes.restype = sz
+    L.nm_kv4_attention.argtypes = [p, i64, i64, i64, i32, p, *batch, i64, f32, i64, p, i64, i64, p, i64, p, sz, p]
+    L.nm_kv_pages_workspace_bytes.argtypes, L.nm_kv_pages_workspace_bytes.restype = [i64, i64, i64], sz
+    book = [p, i64, i32, p, i64, p, i64, i32]  # page_table .. page_size
+    L.nm_kv_resize.argtypes = [p, *book, p, p, p, sz, p]
+    L.nm_kv_fork.argtypes = [p, p, i64, *book, p, p, p, sz, p]
+    L.nm_kv_compact.argtypes = [*book, p, i64, p, p, sz, p]
+    L.nm_kv_copy_pages.argtypes = [p, i64, i64, i64, i64, p, i64, p]
+    for f in (L.nm_kv4_append, L.nm_kv4_unpack, L.nm_kv4_attention, L.nm_kv_resize, L.nm_kv_fork, L.nm_kv_compact,
+              L.nm_kv_copy_pages):
+        f.restype = i32
     for f in (L.nm_col_norm, L.nm_prune_pack, L.nm_spmv, L.dense_gemv, L.nm_unpack, L.nm_spmv_multi,
               L.dense_gemv_multi):
         f.restype = i32
@@ -601,3 +620,179 @@ def nm_spmv_multi_plan(rows, K: int, B: int) -> dict:
     pl = _LaunchPlan()
     _check(lib.nm_spmv_multi_plan(arr, len(rows), int(K), int(B), ctypes.byref(pl)))
     return _plan_dict(pl)
+
+
+# ---- the 4-bit key/value cache (format, places and rules: include/nm_spmv.h) ----
+
+def nm_kv4_page_bytes(page_size: int, n_kv: int, head_dim: int) -> int:
+    """Bytes of one page of page_size tokens (64, 128, 256 or 512) of n_kv heads of 64 or 128 channels."""
+    return int(lib.nm_kv4_page_bytes(int(page_size), int(n_kv), int(head_dim)))
+
+
+def _call(ref: torch.Tensor, fn, *args):
+    """One entry point on ref's device, on the stream that is current there."""
+    dev = ref.device
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, stream))
+
+
+def _i32(t: torch.Tensor, name: str, ref: torch.Tensor, shape) -> int:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != ref.device:
+        raise TypeError(f"{name} must be an int32 tensor on {ref.device}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of shape {list(shape)} (got {list(t.shape)})")
+    return t.data_ptr()
+
+
+def _table(page_table: torch.Tensor, ref: torch.Tensor):
+    if not isinstance(page_table, torch.Tensor) or page_table.dtype != torch.int32 or page_table.device != ref.device:
+        raise TypeError(f"page_table must be an int32 tensor on {ref.device}")
+    if page_table.dim() != 2 or page_table.stride(1) != 1:
+        raise ValueError("page_table must be [S, columns], contiguous in its last dimension")
+    S, cols = page_table.shape
+    return page_table.data_ptr(), page_table.stride(0) if S > 1 else cols, cols, S
+
+
+def _kv_rows(t: torch.Tensor, name: str, ref: torch.Tensor | None = None):
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or (ref is not None and t.device != ref.device):
+        raise ValueError(f"{name} must be a tensor on {'a HIP device' if ref is None else ref.device}")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16} (got {t.dtype})")
+    if t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [T, heads, head_dim], contiguous in its last dimension")
+    T, H, D = t.shape
+    return t.data_ptr(), t.stride(0) if T > 1 else H * D, t.stride(1) if H > 1 else D
+
+
+def _kv_batch(ref: torch.Tensor, cache: torch.Tensor, page_table, kv_len, q_start, page_size: int, n_kv: int, D: int):
+    """(cache pointer, num_pages .. S) of a ragged batch, checked."""
+    if not isinstance(cache, torch.Tensor) or cache.dtype != torch.uint8 or cache.device != ref.device:
+        raise TypeError(f"cache must be a uint8 tensor on {ref.device}")
+    if cache.dim() != 2 or not cache.is_contiguous():
+        raise ValueError("cache must be contiguous, [num_pages, page_bytes]")
+    want = lib.nm_kv4_page_bytes(page_size, n_kv, D)
+    if want and cache.shape[1] != want:
+        raise ValueError(f"cache pages must be of {want} bytes (got {cache.shape[1]})")
+    tp, ld, cols, S = _table(page_table, ref)
+    return (cache.data_ptr(), cache.shape[0], page_size, n_kv, D, tp, ld, cols, _i32(kv_len, "kv_len", ref, (S,)),
+            _i32(q_start, "q_start", ref, (S + 1,)), S)
+
+
+def nm_kv4_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
+                  kv_len: torch.Tensor, q_start: torch.Tensor, page_size: int) -> None:
+    """Rows k, v bf16 [T, n_kv, D] -> cache uint8 [num_pages, page_bytes], at the last places of the
+    sequences: page_table int32 [S, columns], kv_len int32 [S] (new rows included), q_start int32 [S + 1]."""
+    kr = _kv_rows(k, "k")
+    vr = _kv_rows(v, "v", k)
+    if k.shape != v.shape:
+        raise ValueError("k and v must have the same shape")
+    T, H, D = k.shape
+    _call(k, lib.nm_kv4_append, *kr, *vr, T, *_kv_batch(k, cache, page_table, kv_len, q_start, page_size, H, D))
+
+
+def nm_kv4_unpack(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, q_start: torch.Tensor,
+                  page_size: int, k_out: torch.Tensor, v_out: torch.Tensor):
+    """The rows that nm_kv4_append with the same arguments stores, as the cache holds them -> k_out, v_out bf16
+    [T, n_kv, D]."""
+    kr = _kv_rows(k_out, "k_out")
+    vr = _kv_rows(v_out, "v_out", k_out)
+    if k_out.shape != v_out.shape:
+        raise ValueError("k_out and v_out must have the same shape")
+    T, H, D = k_out.shape
+    _call(k_out, lib.nm_kv4_unpack, *_kv_batch(k_out, cache, page_table, kv_len, q_start, page_size, H, D), T, *kr, *vr)
+    return k_out, v_out
+
+
+def nm_kv4_attention_workspace_bytes(T: int, S: int, n_heads: int, n_kv: int, head_dim: int, max_q_len: int) -> int:
+    return int(lib.nm_kv4_attention_workspace_bytes(T, S, n_heads, n_kv, head_dim, max_q_len))
+
+
+def nm_kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
+                     q_start: torch.Tensor, n_kv: int, page_size: int, max_q_len: int, scale: float | None = None,
+                     window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None):
+    """Causal attention of rows q bf16 [T, heads, D] over the cached keys and values of their sequences ->
+    (out bf16 [T, heads, D], lse fp32 [T, heads]).  scale: 1 / sqrt(D) unless given.  window: keys a row looks
+    back over, itself among them (0: all).  max_q_len: a hint, the most rows of one sequence."""
+    qr = _kv_rows(q, "q")
+    T, Hq, D = q.shape
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    o = _kv_rows(out, "out", q)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    if lse.dtype != torch.float32 or lse.device != q.device or lse.shape != (T, Hq) or lse.stride(1) != 1:
+        raise ValueError("lse must be fp32 [T, heads], contiguous in its last dimension, on q's device")
+    b = _kv_batch(q, cache, page_table, kv_len, q_start, page_size, n_kv, D)
+    ws, ws_bytes = _workspace(lib.nm_kv4_attention_workspace_bytes(T, b[-1], Hq, n_kv, D, max_q_len), q, workspace)
+    _call(q, lib.nm_kv4_attention, *qr, T, Hq, *b, max_q_len, D ** -0.5 if scale is None else scale, window, *o,
+          lse.data_ptr(), lse.stride(0) if T > 1 else Hq, None if ws is None else ws.data_ptr(), ws_bytes)
+    return out, lse
+
+
+def nm_kv_pages_workspace_bytes(S: int, n_pairs: int, num_pages: int) -> int:
+    return int(lib.nm_kv_pages_workspace_bytes(S, n_pairs, num_pages))
+
+
+def _kv_book(page_table, kv_len, refcount, page_size, n_pairs, workspace):
+    if not isinstance(page_table, torch.Tensor) or page_table.device.type != "cuda":
+        raise ValueError("page_table must be a tensor on a HIP device")
+    tp, ld, cols, S = _table(page_table, page_table)
+    N = refcount.numel()
+    ws, ws_bytes = _workspace(lib.nm_kv_pages_workspace_bytes(S, n_pairs, N), page_table, workspace)
+    return (tp, ld, cols, _i32(kv_len, "kv_len", page_table, (S,)), S, _i32(refcount, "refcount", page_table, (N,)), N,
+            page_size), ws, ws_bytes
+
+
+def nm_kv_resize(new_len: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, refcount: torch.Tensor,
+                 page_size: int, moves: torch.Tensor, missing: torch.Tensor,
+                 workspace: torch.Tensor | None = None) -> None:
+    """Sequences to new_len int32 [S] tokens: pages given back or handed out, in page_table int32 [S, columns],
+    kv_len int32 [S] and refcount int32 [num_pages].  moves int32 [S, 2] for nm_kv_copy_pages; missing int32 [1]."""
+    b, ws, ws_bytes = _kv_book(page_table, kv_len, refcount, page_size, 0, workspace)
+    S = b[4]
+    _call(page_table, lib.nm_kv_resize, _i32(new_len, "new_len", page_table, (S,)), *b,
+          _i32(moves, "moves", page_table, (S, 2)), _i32(missing, "missing", page_table, (1,)),
+          None if ws is None else ws.data_ptr(), ws_bytes)
+
+
+def nm_kv_fork(parent: torch.Tensor, child: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
+               refcount: torch.Tensor, page_size: int, moves: torch.Tensor, missing: torch.Tensor,
+               workspace: torch.Tensor | None = None) -> None:
+    """Slots child int32 [n] become copies of slots parent int32 [n]; full pages are shared.  moves int32 [n, 2]
+    for nm_kv_copy_pages; missing int32 [1]."""
+    n = parent.numel()
+    if n == 0:
+        return
+    b, ws, ws_bytes = _kv_book(page_table, kv_len, refcount, page_size, n, workspace)
+    _call(page_table, lib.nm_kv_fork, _i32(parent, "parent", page_table, (n,)), _i32(child, "child", page_table, (n,)),
+          n, *b, _i32(moves, "moves", page_table, (n, 2)), _i32(missing, "missing", page_table, (1,)),
+          None if ws is None else ws.data_ptr(), ws_bytes)
+
+
+def nm_kv_compact(page_table: torch.Tensor, kv_len: torch.Tensor, refcount: torch.Tensor, page_size: int,
+                  moves: torch.Tensor, used: torch.Tensor, workspace: torch.Tensor | None = None) -> None:
+    """Used pages into the lowest numbers.  moves int32 [max_moves, 2] for nm_kv_copy_pages; used int32 [1]."""
+    b, ws, ws_bytes = _kv_book(page_table, kv_len, refcount, page_size, 0, workspace)
+    n = moves.shape[0]
+    _call(page_table, lib.nm_kv_compact, *b, _i32(moves, "moves", page_table, (n, 2)), n,
+          _i32(used, "used", page_table, (1,)), None if ws is None else ws.data_ptr(), ws_bytes)
+
+
+def nm_kv_copy_pages(cache: torch.Tensor, moves: torch.Tensor) -> None:
+    """Copies page moves[i, 0] to page moves[i, 1] (int32 [n, 2]) of cache uint8 [num_pages, page_bytes], or in
+    each layer of [layers, num_pages, page_bytes]."""
+    if not isinstance(cache, torch.Tensor) or cache.dtype != torch.uint8 or cache.device.type != "cuda":
+        raise TypeError("cache must be a uint8 tensor on a HIP device")
+    if cache.dim() not in (2, 3) or not cache[0].is_contiguous() or not (cache.dim() == 3 or cache.is_contiguous()):
+        raise ValueError("cache must be [num_pages, page_bytes] or [layers, num_pages, page_bytes], layers contiguous")
+    N, nbytes = cache.shape[-2:]
+    layers = cache.shape[0] if cache.dim() == 3 else 1
+    _call(cache, lib.nm_kv_copy_pages, cache.data_ptr(), N, nbytes, layers, cache.stride(0) if layers > 1 else N * nbytes,
+          _i32(moves, "moves", cache, (moves.shape[0], 2)), moves.shape[0])

@@ -1,0 +1,148 @@
+// nm_kv4.hip -- tokens into the 4-bit key/value cache and back.
+//
+// A block of 32 channels of one token is stored as E2M1 numbers times a power of two:
+//     byte = clamp(E(amax) - 2 + (significand(amax) > 1.75), 16, 252),  x ~ e2m1 * 2^(byte - 127),
+// E the biased exponent of the largest magnitude: that magnitude lands in (3.5, 7], where
+// rounding to nearest (6 the largest) is off by at most one unit of the scale.  The ends
+// 16 and 252 keep every stored value a normal, finite bf16.
+#include "nm_device.h"
+#include "nm_kv.h"
+
+namespace nmk {
+namespace {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Sequence that row t belongs to: the last s with q_start[s] <= t.  Called by a whole wave
+// with one t: 64 lanes look at 64 places at once, so 4096 sequences take two looks.
+__device__ __forceinline__ int find_seq(const int32_t *q_start, int S, int t, int lane) {
+    int lo = 0, n = S;  // the answer is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 63) >> 6;
+        const int at = lo + lane * step;
+        const bool yes = lane * step < n && q_start[at] <= t;
+        const uint64_t m = __ballot(yes);
+        const int last = m ? 63 - __clzll((long long)m) : 0;
+        lo += last * step;
+        n = min(step, S - lo);
+    }
+    return lo;
+}
+
+// Where row t is kept: the head-0 block of its page and its token within the page; null
+// where the sequence has no place or no valid page for it.
+__device__ __forceinline__ uint8_t *place_of(const Kv4Batch &b, int s, int t, int &tok) {
+    const int q0 = b.q_start[s], q1 = b.q_start[s + 1];
+    const int64_t pos = (int64_t)b.kv_len[s] - q1 + t;
+    if (t < q0 || t >= q1 || pos < 0) return nullptr;
+    const int64_t col = pos / b.f.page;
+    tok = (int)(pos - col * b.f.page);
+    if (col >= b.cols) return nullptr;
+    const int page = b.table[(int64_t)s * b.ld_table + col];
+    if (page < 0 || page >= b.num_pages) return nullptr;
+    return b.cache + (int64_t)page * b.f.page_bytes();
+}
+
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+__device__ __forceinline__ bf16x2 as_bf16x2(uint32_t u) {
+    union { uint32_t u; bf16x2 h; } c;
+    c.u = u;
+    return c.h;
+}
+
+// Eight channels of a lane -> eight E2M1 codes; the block's scale byte in every lane of it.
+__device__ __forceinline__ uint32_t quantize8(u32x4 x, uint32_t &byte) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, max(x[i] & 0x7FFFu, (x[i] >> 16) & 0x7FFFu));
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false));  // lanes of 4
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false));
+    const int e = (int)(m >> 7) - 2 + ((m & 127u) > 96u ? 1 : 0);
+    byte = (uint32_t)min(max(e, 16), 252);
+    const float s = scale_of(byte);
+    uint32_t r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(0, as_bf16x2(x[0]), s, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, as_bf16x2(x[1]), s, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, as_bf16x2(x[2]), s, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, as_bf16x2(x[3]), s, 3);
+}
+
+__device__ __forceinline__ u32x4 dequantize8(uint32_t w, float s) {
+    union { bf16x2 h[4]; u32x4 u; } c;
+    c.h[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
+    c.h[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
+    c.h[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
+    c.h[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
+    return c.u;
+}
+
+constexpr int kThreads = 256;
+
+// A lane takes 8 channels of one token and head, K and V.  The lanes of a wave cover one
+// head of 4 (dim 128) or 8 (dim 64) consecutive tokens: four tokens of a sequence fill the
+// 16-byte units of V.  Memory-bound: 4 bytes read and 1.06 written per channel.
+template <int D, bool WRITE>
+__global__ __launch_bounds__(kThreads) void kv4_rows_kernel(Kv4Batch b, Kv4Rows k, Kv4Rows v) {
+    constexpr int C8 = D / 8, ROWS = kWave / C8;
+    b.f.dim = D;
+    const int lane = threadIdx.x & 63;
+    const int64_t wave = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 6;
+    const int64_t h64 = wave % b.f.n_kv, t0 = wave / b.f.n_kv * ROWS;
+    const int h = (int)h64;
+    if (t0 >= b.T) return;
+    int s = find_seq(b.q_start, b.S, (int)t0, lane);
+    const int t = (int)t0 + lane / C8, c8 = lane % C8;
+    if (t >= b.T || t >= b.q_start[b.S]) return;
+    while (s + 1 < b.S && b.q_start[s + 1] <= t) ++s;
+    int tok = 0;
+    uint8_t *p = place_of(b, s, t, tok);
+    u32x4 *kp = reinterpret_cast<u32x4 *>(k.p + t * k.ld + h * k.hd + c8 * 8);
+    u32x4 *vp = reinterpret_cast<u32x4 *>(v.p + t * v.ld + h * v.hd + c8 * 8);
+    if (p) p += (int64_t)h * b.f.head_bytes();
+    if constexpr (WRITE) {
+        if (!p) return;  // all lanes of a row leave together
+        uint32_t kb, vb;
+        const u32x4 kx = *kp, vx = *vp;
+        const uint32_t kw = quantize8(kx, kb), vw = quantize8(vx, vb);
+        *reinterpret_cast<uint32_t *>(p + b.f.k_byte(tok) + c8 * 4) = kw;
+        *reinterpret_cast<uint32_t *>(p + b.f.v_word(tok, c8)) = vw;
+        if ((c8 & 3) == 0) {
+            p[b.f.k_scale(tok, c8 >> 2)] = (uint8_t)kb;
+            p[b.f.v_scale(tok, c8 >> 2)] = (uint8_t)vb;
+        }
+    } else {
+        u32x4 kx = {0, 0, 0, 0}, vx = {0, 0, 0, 0};
+        if (p) {
+            const uint32_t kw = *reinterpret_cast<uint32_t *>(p + b.f.k_byte(tok) + c8 * 4);
+            const uint32_t vw = *reinterpret_cast<uint32_t *>(p + b.f.v_word(tok, c8));
+            kx = dequantize8(kw, scale_of(p[b.f.k_scale(tok, c8 >> 2)]));
+            vx = dequantize8(vw, scale_of(p[b.f.v_scale(tok, c8 >> 2)]));
+        }
+        *kp = kx;
+        *vp = vx;
+    }
+}
+
+template <bool WRITE>
+hipError_t launch_rows(const Kv4Batch &b, const Kv4Rows &k, const Kv4Rows &v, hipStream_t st) {
+    const int rows = kWave * 8 / b.f.dim;
+    const int64_t waves = (((int64_t)b.T + rows - 1) / rows) * b.f.n_kv;
+    const dim3 grid((unsigned)((waves + 3) / 4));
+    if (b.f.dim == 128)
+        kv4_rows_kernel<128, WRITE><<<grid, kThreads, 0, st>>>(b, k, v);
+    else
+        kv4_rows_kernel<64, WRITE><<<grid, kThreads, 0, st>>>(b, k, v);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv4_append(const Kv4Batch &b, const Kv4Rows &k, const Kv4Rows &v, hipStream_t st) {
+    return launch_rows<true>(b, k, v, st);
+}
+
+hipError_t launch_kv4_unpack(const Kv4Batch &b, const Kv4Rows &k, const Kv4Rows &v, hipStream_t st) {
+    return launch_rows<false>(b, k, v, st);
+}
+
+}  // namespace nmk

@@ -391,6 +391,122 @@ nm_status nm_unpack(const uint32_t *masks, const nm_bf16 *values, int64_t R, int
 size_t nm_stream_read_sink_words(size_t bytes);
 nm_status nm_stream_read(const void *buf, size_t bytes, uint32_t *sink, size_t sink_words, void *hip_stream);
 
+/*
+ * The 4-bit key/value cache of the decode step: between the q|k|v and the o projections
+ * a token's key and value join a cache and its query attends over it.  Next to the pruned
+ * weights that cache is what a decode step reads, so it is kept as the weights are: in a
+ * packed format that the kernels read as it lies.
+ *
+ * Format.  A cache of one layer is uint8 [num_pages][page_bytes], page_bytes =
+ * nm_kv4_page_bytes(page_size, n_kv, head_dim) (D = head_dim 64 or 128; page_size 64,
+ * 128, 256 or 512 tokens; 4.25 bits per value).  A page holds n_kv blocks, each
+ *     K values [page_size][D/2]        | V values [page_size/4][D/8][4][4]
+ *     K scales [page_size/64][16][D/32][4] | V scales [page_size/4][D/32][4]
+ * bytes.  Values are OCP E2M1 numbers (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives), two
+ * a byte, the even channel in the low four bits; a scale is an E8M0 byte e for one token
+ * and 32 channels: x = e2m1 * 2^(e - 127).  K value rows are tokens; the 16 V bytes
+ * [g][c] are channels 8c..8c+7 of tokens 4g..4g+3; K scale [G][r][b][j] is block b of
+ * token 64G + 16j + r; V scale [g][b][i] block b of token 4g + i.
+ *
+ * A ragged batch.  page_table int32 [S][ld_table] (table_cols entries used): page of
+ * tokens c*page_size.. of sequence s.  kv_len int32 [S]: tokens of the sequence, new ones
+ * included.  q_start int32 [S + 1], non-decreasing, q_start[0] = 0: sequence s owns rows
+ * q_start[s] .. q_start[s+1] of the token arrays; of its n rows row i is at place
+ * kv_len[s] - n + i.  All are DEVICE arrays and may change between replays of a captured
+ * graph.  Sequences without rows are allowed.  A place below 0, behind the table's last
+ * column or on a page number outside [0, num_pages) holds nothing: it is not written, reads
+ * as zeros (unpack) and is left out (attention).  Rows from q_start[S] to T are not touched.
+ * Token arrays are bf16 [T][heads][D] with element strides ld* (token) and hd* (head), both
+ * multiples of 8, the base 16-byte aligned.  T <= 2^24, S <= 2^20, n_kv <= 256; T = 0 is
+ * allowed.  The cache is 16-byte aligned.
+ *
+ * nm_kv4_append -- stores rows of k and v.  Per block of 32 channels, with E the biased
+ * exponent of the largest magnitude a and m its significand in [1, 2):
+ *     e = min(max(E - 2 + (m > 1.75), 16), 252);
+ * values are rounded to the nearest E2M1 multiple of 2^(e - 127), ties to the even code,
+ * magnitudes above 6 to 6.  Two rows of one call at the same place (a page shared by two
+ * sequences: see nm_kv_resize) leave one of the two there, token by token and head by head.
+ *
+ * nm_kv4_unpack -- the same rows of the cache as bf16 (exact).
+ *
+ * nm_kv4_attention -- for row i (place p) and head h, with key/value head h / (n_heads /
+ * n_kv), over the keys j of its sequence with j <= p, and j > p - window if window > 0:
+ *     s_j = scale * sum_c q_c K_jc,  out = sum_j exp(s_j - lse) V_j,  lse = log sum_j exp(s_j).
+ * A row without keys gives out = 0 and lse = -infinity.  lse (fp32 [T][ld_lse]) may be
+ * NULL.  out must not overlap q.  Scores, maxima, sums and outputs are kept in fp32, the
+ * result is rounded once to bf16.  max_q_len >= 1 is a hint (the largest number of rows of a
+ * sequence) that the choice of kernels goes by; a wrong one costs time only.  Cached values
+ * must be finite in the places that are looked at; what masked places, other pages and the
+ * rest of a page hold does not matter.  Workspace: nm_kv4_attention_workspace_bytes, 16-byte aligned;
+ * calls that may overlap in time need workspaces of their own.
+ */
+int64_t nm_kv4_page_bytes(int page_size, int n_kv, int head_dim); /* 0 for sizes that are refused */
+nm_status nm_kv4_append(const nm_bf16 *k, int64_t ldk, int64_t hdk, const nm_bf16 *v, int64_t ldv, int64_t hdv,
+                        int64_t T, uint8_t *cache, int64_t num_pages, int page_size, int n_kv, int head_dim,
+                        const int32_t *page_table, int64_t ld_table, int table_cols, const int32_t *kv_len,
+                        const int32_t *q_start, int64_t S, void *hip_stream);
+nm_status nm_kv4_unpack(const uint8_t *cache, int64_t num_pages, int page_size, int n_kv, int head_dim,
+                        const int32_t *page_table, int64_t ld_table, int table_cols, const int32_t *kv_len,
+                        const int32_t *q_start, int64_t S, int64_t T, nm_bf16 *k, int64_t ldk, int64_t hdk,
+                        nm_bf16 *v, int64_t ldv, int64_t hdv, void *hip_stream);
+size_t nm_kv4_attention_workspace_bytes(int64_t T, int64_t S, int n_heads, int n_kv, int head_dim, int64_t max_q_len);
+nm_status nm_kv4_attention(const nm_bf16 *q, int64_t ldq, int64_t hdq, int64_t T, int n_heads, const uint8_t *cache,
+                           int64_t num_pages, int page_size, int n_kv, int head_dim, const int32_t *page_table,
+                           int64_t ld_table, int table_cols, const int32_t *kv_len, const int32_t *q_start, int64_t S,
+                           int64_t max_q_len, float scale, int64_t window, nm_bf16 *out, int64_t ldo, int64_t hdo,
+                           float *lse, int64_t ld_lse, void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/*
+ * Keeping the pages of a cache.  The state is the page table (entries behind a sequence's
+ * last page are -1), kv_len and a reference count per page, int32 [num_pages]: how many
+ * sequences hold it, 0 = free.  One table serves the caches of all layers.  Free pages are
+ * handed out lowest number first, in the order of the requests, so a result depends on the
+ * state and the arguments alone.  S * table_cols and num_pages <= 2^30, pairs <= 2^20, moves <= 2^29.  Workspace for all
+ * three: nm_kv_pages_workspace_bytes(S, n_pairs, num_pages), 16-byte aligned (n_pairs 0
+ * where there is no fork).
+ *
+ * moves int32 [..][2] receives pairs (from, to) of pages whose bytes the caller has
+ * nm_kv_copy_pages copy in every cache before the pages are read or written; pairs without
+ * work are (-1, -1).
+ *
+ * nm_kv_resize -- sets every sequence to new_len[s] tokens (negative: leave it).  Pages
+ * behind a shorter length are given back (0 frees the sequence); a longer one gets the
+ * pages it lacks.  A sequence that grows within a page it shares gets a page of its own in
+ * its place, and moves[s] (int32 [S][2]) says what to copy.  Where free pages run out, in the order
+ * of s, a sequence is left at its length (as is one whose new_len is more than table_cols
+ * pages); missing[0] is the number of pages that lacked.
+ *
+ * nm_kv_fork -- for each of n pairs slot child[i] becomes a copy of slot parent[i]: pages
+ * the child held are given back, the parent's full pages are shared, and a last page that
+ * is partly filled is replaced by a fresh one (moves int32 [n][2]).  A child whose page lacks
+ * is left empty; missing[0] counts them.  Pairs with a slot outside [0, S), with parent =
+ * child, with a child that an earlier pair names, or a parent that is a child in the same
+ * call are left out.
+ *
+ * nm_kv_compact -- with U pages used (used[0] = U): the j-th used page at or behind U
+ * moves into the j-th free page before it, for j < max_moves; tables and reference counts
+ * follow, moves (int32 [max_moves][2]) says what to copy.  num_pages / 2 moves are always enough to leave
+ * all used pages in [0, U).
+ *
+ * nm_kv_copy_pages -- copies page moves[i][0] to page moves[i][1], i < n, in each of
+ * `layers` caches at cache + l * layer_stride bytes.  Pairs whose pages are equal or outside
+ * [0, num_pages) are skipped.  A page may be the source of several pairs; one that is the
+ * target of two, or source and target, ends up with unspecified bytes.  page_bytes and
+ * layer_stride are multiples of 16.
+ */
+size_t nm_kv_pages_workspace_bytes(int64_t S, int64_t n_pairs, int64_t num_pages);
+nm_status nm_kv_resize(const int32_t *new_len, int32_t *page_table, int64_t ld_table, int table_cols, int32_t *kv_len,
+                       int64_t S, int32_t *refcount, int64_t num_pages, int page_size, int32_t *moves,
+                       int32_t *missing, void *workspace, size_t workspace_bytes, void *hip_stream);
+nm_status nm_kv_fork(const int32_t *parent, const int32_t *child, int64_t n, int32_t *page_table, int64_t ld_table,
+                     int table_cols, int32_t *kv_len, int64_t S, int32_t *refcount, int64_t num_pages, int page_size,
+                     int32_t *moves, int32_t *missing, void *workspace, size_t workspace_bytes, void *hip_stream);
+nm_status nm_kv_compact(int32_t *page_table, int64_t ld_table, int table_cols, int32_t *kv_len, int64_t S,
+                        int32_t *refcount, int64_t num_pages, int page_size, int32_t *moves, int64_t max_moves,
+                        int32_t *used, void *workspace, size_t workspace_bytes, void *hip_stream);
+nm_status nm_kv_copy_pages(uint8_t *cache, int64_t num_pages, int64_t page_bytes, int64_t layers, int64_t layer_stride,
+                           const int32_t *moves, int64_t n, void *hip_stream);
+
 #ifdef __cplusplus
 }
 #endif
