@@ -4,6 +4,27 @@
 //     s_j = scale * sum_c q_c K_jc,  m = max_j s_j,  l = sum_j exp(s_j - m),
 //     o_c = sum_j exp(s_j - m) V_jc / l,  lse = m + log l,
 // over the keys j <= p, and j > p - window where there is a window.
+//
+// Decode.  The query rows of one key/value head (its query heads times the sequence's new
+// tokens) form tiles of 16.  A wave takes one tile and walks blocks of 64 tokens:
+//   S^T [64 x 16] = K [64 x D] . Q^T: the scaled matrix instruction reads the 4-bit keys and
+//     their scales as they lie in the page (16 tokens x 128 channels an instruction), so
+//     keys cost no conversion at all.  Queries are split into three 6-bit (E2M3) pieces
+//     with a scale per 32 channels: pieces of 4-bit keys and 6-bit queries run at twice the
+//     rate of 4-bit keys and 8-bit queries, and the three of them are within 2^-15 of a
+//     block's largest query channel (the first two hold all 8 bits of the larger ones).
+//   O^T [D x 16] += V^T [D x 64] . P^T: S^T leaves a lane four consecutive tokens of one
+//     query row, which is what the bf16 product over tokens takes; V units of 4 tokens x 8
+//     channels give the same lane its 8 tokens of 8 channels with one conversion and one
+//     byte permute per two values, nothing passes through LDS.
+// Weights are rounded to bf16 for that product (half a step: 2^-9 of each on average
+// cancelling over keys); scores, maxima, sums and O stay in fp32.
+//
+// Work split.  All (sequence, key/value head, row tile, 64-token block) units of a call
+// are laid end to end, in that order, and cut into equal runs, one per wave: lengths need
+// not be alike, nor known to the host.  A wave finishes the rows whose blocks are all its own;
+// pieces of rows cut between waves are joined in LDS, those cut between workgroups in fp32
+// through the workspace by a second kernel, in a fixed order.
 #include "nm_device.h"
 #include "nm_kv.h"
 
@@ -12,96 +33,578 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kBlock = 64;      // tokens a wave takes at a time
+constexpr int kRows = 16;       // query rows of a tile
+constexpr int kWaves = 4;       // waves per workgroup
+constexpr int kGroupsPerCu = 2; // resident workgroups: 8 waves a CU, 8.7 KB of cache in flight each
 
-__device__ __forceinline__ float e2m1(uint32_t code) {
-    const uint32_t e = (code >> 1) & 3u, m = code & 1u;
-    const float a = e ? __uint_as_float(((e + 126u) << 23) | (m << 22)) : 0.5f * (float)m;
-    return (code & 8u) ? -a : a;
-}
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x6 __attribute__((ext_vector_type(6)));
+typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x32 __attribute__((ext_vector_type(32)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x32 __attribute__((ext_vector_type(32)));
 
 __device__ __forceinline__ float pow2_byte(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// One wave per row and head.  Lanes take one key each for the scores, then two channels
-// each (one at dim 64) for the values.
+__device__ __forceinline__ float rows_max(float v) {  // over the four lanes of a column
+    const uint32_t u = __float_as_uint(v);
+    const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const float w = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    const uint32_t x = __float_as_uint(w);
+    const auto q = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    union { bf16x2 h; uint32_t u; } c;
+    c.h = __builtin_convertvector((f32x2){a, b}, bf16x2);
+    return c.u;
+}
+
+__device__ __forceinline__ uint32_t fp4_pair(uint32_t w, float s, int byte) {
+    union { bf16x2 h; uint32_t u; } c;
+    switch (byte) {
+    case 0: c.h = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0); break;
+    case 1: c.h = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1); break;
+    case 2: c.h = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2); break;
+    default: c.h = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3); break;
+    }
+    return c.u;
+}
+
+// Three 6-bit pieces of 32 bf16 query channels with their scale bytes in one dword.
+struct Pieces {
+    u32x6 p[3];
+    uint32_t scales;  // bytes 0..2
+};
+
+__device__ __forceinline__ Pieces split_query(const u32x4 (&x)[4], uint32_t signs) {
+    union { u32x4 u[4]; uint32_t w[16]; bf16x32 h; __bf16 e[32]; } q;
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q.u[i] = x[i];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        top = max(top, max(q.w[i] & 0x7FFFu, (q.w[i] >> 16) & 0x7FFFu));
+        q.w[i] ^= signs;
+    }
+    const uint32_t e = max(top >> 7, 13u);  // biased exponent of the largest magnitude
+    Pieces r;
+    r.scales = (e - 2) | (e - 6) << 8 | (e - 11) << 16;
+    const uint32_t at[3] = {e - 2, e - 6, e - 11};
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const float s = pow2_byte(at[k]);
+        r.p[k] = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(q.h, s);
+        if (k < 2) {  // what is left is a bf16 number: at most the bits the piece did not take
+            const f32x32 d = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(r.p[k], s);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                q.w[i] = pack_bf16((float)q.e[2 * i] - d[2 * i], (float)q.e[2 * i + 1] - d[2 * i + 1]);
+        }
+    }
+    return r;
+}
+
+// Operands of the scaled matrix instruction: 4-bit formats read four registers, 6-bit ones
+// six; the rest of the type is never read.
+__device__ __forceinline__ i32x8 wide(u32x6 v) {
+    return (i32x8)__builtin_shufflevector(v, v, 0, 1, 2, 3, 4, 5, -1, -1);
+}
+__device__ __forceinline__ i32x8 wide(u32x4 v) {
+    return (i32x8)__builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
+}
+
+// What a sequence asks of a call.
+struct Seq {
+    int q0, n, len;      // first row, rows, tokens
+    int tiles;           // row tiles per key/value head
+    int first, blocks;   // first 64-token block and how many (at least one)
+    __device__ int64_t units(int n_kv) const { return (int64_t)tiles * n_kv * blocks; }
+};
+
+__device__ __forceinline__ Seq seq_of(const Kv4Attention &a, int s, int group) {
+    Seq q = {0, 0, 0, 0, 0, 1};
+    if (s >= a.b.S) return q;
+    q.q0 = a.b.q_start[s];
+    q.n = a.b.q_start[s + 1] - q.q0;
+    q.len = a.b.kv_len[s];
+    if (q.n <= 0) {
+        q.n = 0;
+        return q;
+    }
+    q.tiles = (int)(((int64_t)q.n * group + kRows - 1) / kRows);
+    const int64_t cap = (int64_t)a.b.cols * a.b.f.page;
+    const int64_t end = q.len < cap ? q.len : cap;
+    int64_t lo = a.window > 0 ? (int64_t)q.len - q.n - a.window + 1 : 0;
+    if (lo < 0) lo = 0;
+    q.first = (int)(lo / kBlock);
+    const int64_t last = (end + kBlock - 1) / kBlock;
+    q.blocks = last > q.first ? (int)(last - q.first) : 1;
+    return q;
+}
+
+// One tile's running softmax in registers: column c = lane % 16 is query row c, the four
+// lanes of a column share m and hold their own tokens' part of l and D/4 channels of O.
 template <int D>
-__global__ __launch_bounds__(64) void kv4_attention_row_kernel(Kv4Attention a) {
-    __shared__ float sq[D], sp[64];
-    Kv4Batch &b = a.b;
-    b.f.dim = D;
-    const int lane = threadIdx.x, t = blockIdx.x, h = blockIdx.y;
-    if (t >= b.q_start[b.S]) return;
-    int lo = 0, hi = b.S;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (b.q_start[mid] <= t) lo = mid; else hi = mid;
+struct Tile {
+    f32x4 o[D / 16];
+    float m, l;  // m: largest raw score so far
+};
+
+template <int D>
+__device__ __forceinline__ void clear(Tile<D> &t) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) t.o[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    t.m = -INFINITY;
+    t.l = 0.f;
+}
+
+// The cache bytes of 64 tokens of one head that a lane multiplies.
+template <int D>
+struct Bytes {
+    u32x4 k[4], v[4];
+    uint32_t ks, vs[4];
+};
+
+template <int D>
+struct Lane {
+    int col, g;
+    int k_off, ks_off, v_off, vs_off;  // byte places of this lane within a block of 64 tokens
+    __device__ Lane(int lane) {
+        col = lane & 15;
+        g = lane >> 4;
+        const int kb = D == 128 ? g : (g & 1);
+        k_off = col * (D / 2) + kb * 16;
+        ks_off = (col * (D / 32) + kb) * 4;
+        const int c8 = D == 128 ? col : col >> 1;
+        v_off = (g * (D / 8) + c8) * 16;
+        vs_off = (g * (D / 32) + (c8 >> 2)) * 4;
     }
-    const int s = lo;
-    const int q0 = b.q_start[s], q1 = b.q_start[s + 1];
-    if (t < q0 || t >= q1) return;
-    const int64_t pos = (int64_t)b.kv_len[s] - q1 + t;
-    const int64_t first = a.window > 0 && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
-    const int kvh = h / (a.heads / b.f.n_kv);
-    const float c = a.scale * kLog2e;
-    for (int i = lane; i < D; i += 64) sq[i] = bf16_lo(a.q.p[t * a.q.ld + h * a.q.hd + i]) * c;
-    __syncthreads();
-    float m = -INFINITY, l = 0.f, o[D / 64] = {};
-    for (int64_t j0 = first & ~(int64_t)63; j0 <= pos; j0 += 64) {
-        const int64_t col = j0 / b.f.page;
-        if (col >= b.cols) break;
-        const int page = b.table[(int64_t)s * b.ld_table + col];
-        if (page < 0 || page >= b.num_pages) continue;
-        const uint8_t *p = b.cache + (int64_t)page * b.f.page_bytes() + (int64_t)kvh * b.f.head_bytes();
-        const int tok0 = (int)(j0 - col * b.f.page), tok = tok0 + lane;
-        float x = -INFINITY;
-        if (j0 + lane <= pos && j0 + lane >= first) {
-            x = 0.f;
-            for (int g = 0; g < D / 32; ++g) {
-                float y = 0.f;
-                for (int i = 0; i < 16; ++i) {
-                    const uint32_t w = p[b.f.k_byte(tok) + g * 16 + i];
-                    y += e2m1(w & 15u) * sq[g * 32 + 2 * i] + e2m1(w >> 4) * sq[g * 32 + 2 * i + 1];
-                }
-                x += y * pow2_byte(p[b.f.k_scale(tok, g)]);
-            }
-        }
-        float top = x;
-        for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-        const float mn = fmaxf(m, top);
-        if (mn == -INFINITY) continue;
-        const float keep = exp2f(m - mn), pr = exp2f(x - mn);
-        m = mn;
-        l = l * keep + wave_sum(pr);
-        sp[lane] = pr;
-        __syncthreads();
-        for (int i = 0; i < D / 64; ++i) o[i] *= keep;
-        for (int j = 0; j < 64; ++j) {
-            const float w = sp[j];
-            if (w == 0.f) continue;  // masked places hold anything
-            for (int i = 0; i < D / 64; ++i) {
-                const int ch = lane + 64 * i;
-                const uint32_t byte = p[b.f.v_word(tok0 + j, ch >> 3) + ((ch & 7) >> 1)];
-                o[i] += w * e2m1((ch & 1) ? byte >> 4 : byte & 15u) * pow2_byte(p[b.f.v_scale(tok0 + j, ch >> 5)]);
-            }
-        }
-        __syncthreads();
+};
+
+template <int D>
+__device__ __forceinline__ void load_block(Bytes<D> &x, const uint8_t *head, const Kv4Format &f, int tok0,
+                                           const Lane<D> &ln) {
+    const uint8_t *k = head + tok0 * (D / 2), *v = head + f.v_at() + tok0 * (D / 2);
+    const uint8_t *ks = head + f.ks_at() + tok0 * (D / 32), *vs = head + f.vs_at() + tok0 * (D / 32);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x.k[j] = *reinterpret_cast<const u32x4 *>(k + ln.k_off + j * 8 * D);
+    x.ks = *reinterpret_cast<const uint32_t *>(ks + ln.ks_off);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x.v[j] = *reinterpret_cast<const u32x4 *>(v + ln.v_off + j * 8 * D);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x.vs[j] = *reinterpret_cast<const uint32_t *>(vs + ln.vs_off + j * (D / 2));
+}
+
+// Scores of 64 tokens: s[j][i] is token 16 j + 4 g + i of the column's row.
+template <int D>
+__device__ __forceinline__ void scores(const Bytes<D> &x, const Pieces &q, f32x4 (&s)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    const int sc = (int)q.scales, ks = (int)x.ks;
+#define NM_KV4_DOT(J, P) \
+    s[J] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(x.k[J]), wide(q.p[P]), s[J], 4, 2, J, ks, P, sc)
+    if constexpr (D == 128) {
+        NM_KV4_DOT(0, 0); NM_KV4_DOT(1, 0); NM_KV4_DOT(2, 0); NM_KV4_DOT(3, 0);
+        NM_KV4_DOT(0, 1); NM_KV4_DOT(1, 1); NM_KV4_DOT(2, 1); NM_KV4_DOT(3, 1);
+        NM_KV4_DOT(0, 2); NM_KV4_DOT(1, 2); NM_KV4_DOT(2, 2); NM_KV4_DOT(3, 2);
+    } else {  // the upper half of the instruction's channels multiplies the second piece
+        NM_KV4_DOT(0, 0); NM_KV4_DOT(1, 0); NM_KV4_DOT(2, 0); NM_KV4_DOT(3, 0);
+        NM_KV4_DOT(0, 2); NM_KV4_DOT(1, 2); NM_KV4_DOT(2, 2); NM_KV4_DOT(3, 2);
     }
+#undef NM_KV4_DOT
+}
+
+// O += V^T P for 64 tokens.
+template <int D>
+__device__ __forceinline__ void add_values(Tile<D> &t, const Bytes<D> &x, const f32x4 (&p)[4], int col) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        union { uint32_t w[4]; bf16x8 h; } b;
+        b.w[0] = pack_bf16(p[2 * s][0], p[2 * s][1]);
+        b.w[1] = pack_bf16(p[2 * s][2], p[2 * s][3]);
+        b.w[2] = pack_bf16(p[2 * s + 1][0], p[2 * s + 1][1]);
+        b.w[3] = pack_bf16(p[2 * s + 1][2], p[2 * s + 1][3]);
+        uint32_t w[8];
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            w[e] = x.v[2 * s + (e >> 2)][e & 3];
+            if (D == 64) w[e] >>= (col & 1) * 16;
+            f[e] = pow2_byte((x.vs[2 * s + (e >> 2)] >> ((e & 3) * 8)) & 255u);
+        }
+#pragma unroll
+        for (int by = 0; by < D / 32; ++by) {
+            uint32_t c[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) c[e] = fp4_pair(w[e], f[e], by);
+            union { uint32_t w[4]; bf16x8 h; } lo, hi;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                lo.w[e] = __builtin_amdgcn_perm(c[2 * e + 1], c[2 * e], 0x05040100u);
+                hi.w[e] = __builtin_amdgcn_perm(c[2 * e + 1], c[2 * e], 0x07060302u);
+            }
+            t.o[2 * by] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo.h, b.h, t.o[2 * by], 0, 0, 0);
+            t.o[2 * by + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi.h, b.h, t.o[2 * by + 1], 0, 0, 0);
+        }
+    }
+}
+
+// Lane's channel of o[mt][i]: (D/4) g + (D/16) i + mt.
+template <int D>
+__device__ __forceinline__ void store_row(const Kv4Attention &a, int t, int h, int g, const float *o, float m, float l,
+                                          bool with_lse) {
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    for (int i = 0; i < D / 64; ++i)
-        a.out.p[t * a.out.ld + h * a.out.hd + lane + 64 * i] = f32_to_bf16_rne(o[i] * inv);
-    if (a.lse && lane == 0) a.lse[t * a.ld_lse + h] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    uint16_t *p = a.out.p + t * a.out.ld + h * a.out.hd + g * (D / 4);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        u32x4 w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = pack_bf16(o[8 * i + 2 * j] * inv, o[8 * i + 2 * j + 1] * inv);
+        *reinterpret_cast<u32x4 *>(p + 8 * i) = w;
+    }
+    if (with_lse && a.lse) a.lse[t * a.ld_lse + h] = l > 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+}
+
+// Pieces of rows cut between waves (LDS) or workgroups (workspace): unnormalised O by
+// row, the maximum (log2 units, scaled) and the sum.
+template <int D>
+struct Part {
+    float o[kRows][D];
+    float m[kRows], l[kRows];
+};
+
+enum : int { kNone = 0, kEnds = 1, kThrough = 2 };  // the item's last block is in / behind the piece
+
+struct PartTag {
+    int state;        // kNone, kEnds, kThrough
+    int s, head, tile;
+};
+
+template <int D>
+struct Shared {
+    Part<D> part[kWaves][2];
+    PartTag tag[kWaves][2];
+};
+
+template <int D>
+__device__ __forceinline__ void keep_part(Part<D> &p, const Tile<D> &t, float c, const Lane<D> &ln) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < D / 64; ++q) {
+            const f32x4 w = {t.o[4 * q][i], t.o[4 * q + 1][i], t.o[4 * q + 2][i], t.o[4 * q + 3][i]};
+            *reinterpret_cast<f32x4 *>(&p.o[ln.col][(D / 4) * ln.g + (D / 16) * i + 4 * q]) = w;
+        }
+    const float l = cross_rows_sum(t.l);
+    if (ln.g == 0) {
+        p.m[ln.col] = t.m == -INFINITY ? -INFINITY : t.m * c;
+        p.l[ln.col] = l;
+    }
+}
+
+// Threads of a workgroup over a part: 16 rows x 16 threads of D/16 channels.
+template <int D>
+struct Join {
+    float o[D / 16], m, l;
+    __device__ Join() : m(-INFINITY), l(0.f) {
+        for (int i = 0; i < D / 16; ++i) o[i] = 0.f;
+    }
+    __device__ void add(const Part<D> &p, int row, int c) {
+        const float pm = p.m[row], mn = fmaxf(m, pm);
+        const float mine = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
+        const float its = pm == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(pm - mn);
+        l = l * mine + p.l[row] * its;
+        for (int i = 0; i < D / 16; ++i) o[i] = o[i] * mine + p.o[row][c * (D / 16) + i] * its;
+        m = mn;
+    }
+    __device__ void put(Part<D> &p, int row, int c) const {
+        for (int i = 0; i < D / 16; ++i) p.o[row][c * (D / 16) + i] = o[i];
+        if (c == 0) {
+            p.m[row] = m;
+            p.l[row] = l;
+        }
+    }
+    __device__ void finish(const Kv4Attention &a, const PartTag &tag, int group, int row, int c) const {
+        const int q0 = a.b.q_start[tag.s], n = a.b.q_start[tag.s + 1] - q0;
+        const int64_t r = (int64_t)tag.tile * kRows + row;
+        if (r >= (int64_t)n * group) return;
+        const int t = q0 + (int)(r / group), h = tag.head * group + (int)(r % group);
+        if (t >= a.b.T) return;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        uint32_t *p = reinterpret_cast<uint32_t *>(a.out.p + t * a.out.ld + h * a.out.hd + c * (D / 16));
+        for (int i = 0; i < D / 32; ++i) p[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
+        if (c == 0 && a.lse) a.lse[t * a.ld_lse + h] = l > 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    }
+};
+
+__device__ __forceinline__ int64_t wave_sum64(int64_t v) {
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+    return v;
+}
+
+__device__ __forceinline__ int64_t wave_scan64(int64_t v, int lane) {
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t u = __shfl_up(v, d);
+        if (lane >= d) v += u;
+    }
+    return v;
+}
+
+template <int D>
+__global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attention a, Part<D> *parts, PartTag *tags) {
+    __shared__ Shared<D> sh;
+    a.b.f.dim = D;
+    const Kv4Format &f = a.b.f;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int group = a.heads / f.n_kv;
+    const Lane<D> ln(lane);
+    const float scale = fabsf(a.scale);
+    const float c = fmaxf(scale, 1e-37f) * kLog2e;  // a scale of 0 leaves scores of 0
+
+    // my run of units
+    int64_t total = 0;
+    for (int s0 = 0; s0 < a.b.S; s0 += 64) total += wave_sum64(seq_of(a, s0 + lane, group).units(f.n_kv));
+    const int64_t waves = (int64_t)gridDim.x * kWaves;
+    const int64_t run = (total + waves - 1) / waves;
+    int64_t u = ((int64_t)blockIdx.x * kWaves + wave) * run;
+    const int64_t end = u + run < total ? u + run : total;
+    if (lane < 2) sh.tag[wave][lane].state = kNone;
+
+    if (u < end) {
+        // the sequence that unit u is in
+        int s = 0;
+        int64_t base = 0;
+        for (int s0 = 0; s0 < a.b.S; s0 += 64) {
+            const int64_t w = seq_of(a, s0 + lane, group).units(f.n_kv);
+            const int64_t upto = base + wave_scan64(w, lane);
+            const uint64_t behind = __ballot(upto > u);
+            if (behind) {
+                const int at = __builtin_ctzll(behind);
+                s = s0 + at;
+                base = __shfl(upto - w, at);
+                break;
+            }
+            base = __shfl(upto, 63);
+        }
+        s = __builtin_amdgcn_readfirstlane(s);
+        while (u < end) {
+            const Seq sq = seq_of(a, s, group);
+            const int64_t mine = sq.units(f.n_kv);
+            if (u - base >= mine) {
+                base += mine;
+                ++s;
+                continue;
+            }
+            const int64_t in = u - base;
+            const int item = (int)(in / sq.blocks), b0 = (int)(in % sq.blocks);
+            const int64_t room = end - u;
+            const int b1 = (int)(room < sq.blocks - b0 ? b0 + room : sq.blocks);
+            const int head = item / sq.tiles, tile = item % sq.tiles;
+            u += b1 - b0;
+
+            // queries of my column
+            const int64_t r = (int64_t)tile * kRows + ln.col;
+            const int qi = (int)(r / group), t = sq.q0 + qi, h = head * group + (int)(r % group);
+            const bool real = r < (int64_t)sq.n * group && t < a.b.T;
+            Pieces q;
+            {
+                u32x4 x[4];
+                const uint16_t *p = a.q.p + t * a.q.ld + h * a.q.hd + (D == 128 ? ln.g : (ln.g & 1)) * 32;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[i] = real ? reinterpret_cast<const u32x4 *>(p)[i] : (u32x4){0, 0, 0, 0};
+                q = split_query(x, a.scale < 0.f ? 0x80008000u : 0u);
+                if constexpr (D == 64) {  // lanes of the upper half: the second piece first, then nothing
+                    if (ln.g >= 2) {
+                        q.p[0] = q.p[1];
+                        q.scales = (q.scales >> 8 & 255u) | (q.scales & 0xFF0000u);
+                        q.p[2] = (u32x6){0, 0, 0, 0, 0, 0};
+                    }
+                }
+            }
+            // keys that my row sees: [from, upto]
+            const int64_t place = (int64_t)sq.len - sq.n + qi;
+            const int64_t cap = (int64_t)a.b.cols * f.page;
+            const int upto = real ? (int)(place < cap ? place : cap - 1) : -1;
+            const int from = a.window > 0 && place - a.window + 1 > 0 ? (int)(place - a.window + 1) : 0;
+            // blocks in which every row of the sequence sees every token need no mask
+            const int64_t all_from = a.window > 0 ? (int64_t)sq.len - a.window : 0;
+            const int64_t all_upto = (int64_t)sq.len - sq.n < cap - 1 ? (int64_t)sq.len - sq.n : cap - 1;
+            // tokens that any row of the sequence sees
+            const int64_t any_from = a.window > 0 ? (int64_t)sq.len - sq.n - a.window + 1 : 0;
+            const int64_t any_upto = (int64_t)sq.len < cap ? (int64_t)sq.len - 1 : cap - 1;
+
+            Tile<D> tl;
+            clear(tl);
+            const int32_t *row = a.b.table + (int64_t)s * a.b.ld_table;
+            const int per = f.page / kBlock;
+            int have = -64;  // first of the 64 blocks whose pages the lanes hold
+            int pages = -1;
+            auto head_of = [&](int b) -> const uint8_t * {  // block b of the walk, null without a valid page
+                if (b >= have + 64 || have < 0) {
+                    have = b;
+                    const int64_t col = (int64_t)(sq.first + b + lane) / per;
+                    pages = col < a.b.cols && b + lane < b1 ? row[col] : -1;
+                }
+                const int page = __builtin_amdgcn_readlane(pages, b - have);
+                if (page < 0 || page >= a.b.num_pages) return nullptr;
+                return a.b.cache + (int64_t)page * f.page_bytes() + (int64_t)head * f.head_bytes();
+            };
+            const uint8_t *now = head_of(b0);
+            Bytes<D> x;
+            if (now) load_block(x, now, f, (sq.first + b0) % per * kBlock, ln);
+            for (int b = b0; b < b1; ++b) {
+                Bytes<D> nx;
+                const uint8_t *next = b + 1 < b1 ? head_of(b + 1) : nullptr;
+                if (next) load_block(nx, next, f, (sq.first + b + 1) % per * kBlock, ln);
+                if (now) {
+                    const int64_t j0 = (int64_t)(sq.first + b) * kBlock;
+                    f32x4 sc[4];
+                    scores(x, q, sc);
+                    if (j0 < all_from || j0 + kBlock - 1 > all_upto) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int64_t tok = j0 + 16 * j + 4 * ln.g + i;
+                                if (tok > upto || tok < from) sc[j][i] = -INFINITY;
+                                // a weight of 0 times what an unseen place holds must be 0
+                                if (tok > any_upto || tok < any_from) x.vs[j] &= ~(255u << (8 * i));
+                            }
+                    }
+                    float mx = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3]));
+#pragma unroll
+                    for (int j = 1; j < 4; ++j)
+                        mx = fmaxf(mx, fmaxf(fmaxf(sc[j][0], sc[j][1]), fmaxf(sc[j][2], sc[j][3])));
+                    const float mn = fmaxf(tl.m, rows_max(mx));
+                    if (__any(mn > tl.m)) {
+                        const float keep = tl.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((tl.m - mn) * c);
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) tl.o[i] *= keep;
+                        tl.l *= keep;
+                        tl.m = mn;
+                    }
+                    const float mc = mn == -INFINITY ? 0.f : mn * c;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sc[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[j][i], c, -mc));
+                        tl.l += (sc[j][0] + sc[j][1]) + (sc[j][2] + sc[j][3]);
+                    }
+                    add_values(tl, x, sc, ln.col);
+                }
+                now = next;
+                x = nx;
+            }
+
+            const bool begins = b0 == 0, ends = b1 == sq.blocks;
+            if (begins && ends) {
+                float o[D / 4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int m = 0; m < D / 16; ++m) o[(D / 16) * i + m] = tl.o[m][i];
+                const float l = cross_rows_sum(tl.l);
+                if (real) store_row<D>(a, t, h, ln.g, o, tl.m * c, l, ln.g == 0);
+            } else {
+                const int slot = begins ? 1 : 0;
+                keep_part(sh.part[wave][slot], tl, c, ln);
+                if (lane == 0) sh.tag[wave][slot] = {ends ? kEnds : kThrough, s, head, tile};
+            }
+        }
+    }
+    __syncthreads();
+
+    // Join the pieces.  Slot 0 of a wave belongs to a row that began before it, slot 1 to
+    // one that begins in it and goes on behind it.
+    const int row = threadIdx.x >> 4, cc = threadIdx.x & 15;
+    const int64_t me = blockIdx.x;
+    PartTag out0 = {kNone, 0, 0, 0}, out1 = {kNone, 0, 0, 0};
+    for (int first = -1; first < kWaves; ++first) {  // -1: the chain that enters this workgroup
+        if (first >= 0 && sh.tag[first][1].state == kNone) continue;
+        if (first < 0 && sh.tag[0][0].state == kNone) continue;
+        Join<D> j;
+        PartTag tag = first < 0 ? sh.tag[0][0] : sh.tag[first][1];
+        if (first >= 0) j.add(sh.part[first][1], row, cc);
+        int state = kThrough;
+        for (int w = first + 1; w < kWaves && state == kThrough; ++w) {
+            if (sh.tag[w][0].state == kNone) break;
+            j.add(sh.part[w][0], row, cc);
+            state = sh.tag[w][0].state;
+        }
+        tag.state = state;
+        if (first >= 0 && state == kEnds) {
+            j.finish(a, tag, group, row, cc);
+        } else {
+            j.put(parts[me * 2 + (first < 0 ? 0 : 1)], row, cc);
+            if (first < 0) out0 = tag; else out1 = tag;
+        }
+    }
+    if (threadIdx.x == 0) {
+        tags[me * 2] = out0;
+        tags[me * 2 + 1] = out1;
+    }
+}
+
+// Rows cut between workgroups: the workgroup in which a row begins owns it; the pieces
+// follow in the slots 0 of the next ones.
+template <int D>
+__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attention a, const Part<D> *parts, const PartTag *tags) {
+    const int64_t w = blockIdx.x;
+    const PartTag tag = tags[2 * w + 1];
+    if (tag.state != kThrough) return;
+    const int row = threadIdx.x >> 4, cc = threadIdx.x & 15;
+    Join<D> j;
+    j.add(parts[2 * w + 1], row, cc);
+    for (int64_t k = w + 1; k < gridDim.x; ++k) {
+        const int state = tags[2 * k].state;
+        if (state == kNone) break;
+        j.add(parts[2 * k], row, cc);
+        if (state == kEnds) break;
+    }
+    j.finish(a, tag, a.heads / a.b.f.n_kv, row, cc);
+}
+
+int device_cus() {
+    int dev = 0, cu = 0;
+    if (hipGetDevice(&dev) != hipSuccess ||
+        hipDeviceGetAttribute(&cu, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cu <= 0) {
+        (void)hipGetLastError();
+        return 256;
+    }
+    return cu;
+}
+
+template <int D>
+size_t decode_workspace(int groups) {
+    return (size_t)groups * 2 * (sizeof(Part<D>) + sizeof(PartTag));
+}
+
+template <int D>
+hipError_t launch_decode(const Kv4Attention &a, void *ws, hipStream_t st) {
+    const int groups = device_cus() * kGroupsPerCu;
+    Part<D> *parts = (Part<D> *)ws;
+    PartTag *tags = (PartTag *)(parts + 2 * (size_t)groups);
+    kv4_decode_kernel<D><<<groups, kWaves * kWave, 0, st>>>(a, parts, tags);
+    kv4_join_kernel<D><<<groups, 256, 0, st>>>(a, parts, tags);
+    return hipGetLastError();
 }
 
 }  // namespace
 
-size_t kv4_attention_workspace(int64_t, int64_t, int, int, int, int64_t) { return 0; }
+size_t kv4_attention_workspace(int64_t, int64_t, int, int, int dim, int64_t) {
+    const int groups = device_cus() * kGroupsPerCu;
+    return dim == 128 ? decode_workspace<128>(groups) : decode_workspace<64>(groups);
+}
 
-hipError_t launch_kv4_attention(const Kv4Attention &a, int64_t, void *, hipStream_t st) {
-    const dim3 grid((unsigned)a.b.T, (unsigned)a.heads);
-    if (a.b.f.dim == 128)
-        kv4_attention_row_kernel<128><<<grid, 64, 0, st>>>(a);
-    else
-        kv4_attention_row_kernel<64><<<grid, 64, 0, st>>>(a);
-    return hipGetLastError();
+hipError_t launch_kv4_attention(const Kv4Attention &a, int64_t, void *ws, hipStream_t st) {
+    return a.b.f.dim == 128 ? launch_decode<128>(a, ws, st) : launch_decode<64>(a, ws, st);
 }
 
 }  // namespace nmk
