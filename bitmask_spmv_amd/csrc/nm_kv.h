@@ -61,6 +61,7 @@ struct Kv4Attention {
     int heads = 0;
     float scale = 1.f;
     int64_t window = 0;  // keys a query looks back over, itself among them; 0: all
+    bool prompts = false;  // sequences of many rows are taken by the prompt kernel
 };
 
 hipError_t launch_kv4_append(const Kv4Batch &b, const Kv4Rows &k, const Kv4Rows &v, hipStream_t st);

@@ -36,6 +36,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kBlock = 64;      // tokens a wave takes at a time
 constexpr int kRows = 16;       // query rows of a tile
 constexpr int kWaves = 4;       // waves per workgroup
+constexpr int kDecodeRows = 64; // query rows of a head up to which a sequence is walked row tile by row tile
 constexpr int kGroupsPerCu = 2; // resident workgroups: 8 waves a CU, 8.7 KB of cache in flight each
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -119,6 +120,24 @@ __device__ __forceinline__ i32x8 wide(u32x4 v) {
     return (i32x8)__builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
 }
 
+// The pieces as a lane multiplies them.  At dim 64 the matrix instruction's upper 64
+// channels multiply the same keys again: lanes 32.. hold the second piece in the first's
+// place, and nothing in the third's.
+template <int D>
+struct Lane;
+template <int D>
+__device__ __forceinline__ Pieces lane_pieces(const u32x4 (&x)[4], float scale, const Lane<D> &ln) {
+    Pieces q = split_query(x, scale < 0.f ? 0x80008000u : 0u);
+    if constexpr (D == 64) {
+        if (ln.g >= 2) {
+            q.p[0] = q.p[1];
+            q.scales = (q.scales >> 8 & 255u) | (q.scales & 0xFF0000u);
+            q.p[2] = (u32x6){0, 0, 0, 0, 0, 0};
+        }
+    }
+    return q;
+}
+
 // What a sequence asks of a call.
 struct Seq {
     int q0, n, len;      // first row, rows, tokens
@@ -133,7 +152,7 @@ __device__ __forceinline__ Seq seq_of(const Kv4Attention &a, int s, int group) {
     q.q0 = a.b.q_start[s];
     q.n = a.b.q_start[s + 1] - q.q0;
     q.len = a.b.kv_len[s];
-    if (q.n <= 0) {
+    if (q.n <= 0 || (a.prompts && (int64_t)q.n * group > kDecodeRows)) {
         q.n = 0;
         return q;
     }
@@ -218,6 +237,29 @@ __device__ __forceinline__ void scores(const Bytes<D> &x, const Pieces &q, f32x4
         NM_KV4_DOT(0, 2); NM_KV4_DOT(1, 2); NM_KV4_DOT(2, 2); NM_KV4_DOT(3, 2);
     }
 #undef NM_KV4_DOT
+}
+
+// Scores -> weights relative to the new maximum; O and l follow it.
+template <int D>
+__device__ __forceinline__ void weights(Tile<D> &t, f32x4 (&s)[4], float c) {
+    float mx = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3]));
+#pragma unroll
+    for (int j = 1; j < 4; ++j) mx = fmaxf(mx, fmaxf(fmaxf(s[j][0], s[j][1]), fmaxf(s[j][2], s[j][3])));
+    const float mn = fmaxf(t.m, rows_max(mx));
+    if (__any(mn > t.m)) {
+        const float keep = t.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((t.m - mn) * c);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) t.o[i] *= keep;
+        t.l *= keep;
+        t.m = mn;
+    }
+    const float mc = mn == -INFINITY ? 0.f : mn * c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i], c, -mc));
+        t.l += (s[j][0] + s[j][1]) + (s[j][2] + s[j][3]);
+    }
 }
 
 // O += V^T P for 64 tokens.
@@ -419,14 +461,7 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attenti
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     x[i] = real ? reinterpret_cast<const u32x4 *>(p)[i] : (u32x4){0, 0, 0, 0};
-                q = split_query(x, a.scale < 0.f ? 0x80008000u : 0u);
-                if constexpr (D == 64) {  // lanes of the upper half: the second piece first, then nothing
-                    if (ln.g >= 2) {
-                        q.p[0] = q.p[1];
-                        q.scales = (q.scales >> 8 & 255u) | (q.scales & 0xFF0000u);
-                        q.p[2] = (u32x6){0, 0, 0, 0, 0, 0};
-                    }
-                }
+                q = lane_pieces<D>(x, a.scale, ln);
             }
             // keys that my row sees: [from, upto]
             const int64_t place = (int64_t)sq.len - sq.n + qi;
@@ -478,25 +513,7 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attenti
                                 if (tok > any_upto || tok < any_from) x.vs[j] &= ~(255u << (8 * i));
                             }
                     }
-                    float mx = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3]));
-#pragma unroll
-                    for (int j = 1; j < 4; ++j)
-                        mx = fmaxf(mx, fmaxf(fmaxf(sc[j][0], sc[j][1]), fmaxf(sc[j][2], sc[j][3])));
-                    const float mn = fmaxf(tl.m, rows_max(mx));
-                    if (__any(mn > tl.m)) {
-                        const float keep = tl.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((tl.m - mn) * c);
-#pragma unroll
-                        for (int i = 0; i < D / 16; ++i) tl.o[i] *= keep;
-                        tl.l *= keep;
-                        tl.m = mn;
-                    }
-                    const float mc = mn == -INFINITY ? 0.f : mn * c;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) sc[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[j][i], c, -mc));
-                        tl.l += (sc[j][0] + sc[j][1]) + (sc[j][2] + sc[j][3]);
-                    }
+                    weights(tl, sc, c);
                     add_values(tl, x, sc, ln.col);
                 }
                 now = next;
@@ -571,6 +588,228 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attention a, const Par
     j.finish(a, tag, a.heads / a.b.f.n_kv, row, cc);
 }
 
+// ---- prompts ----
+//
+// Many rows of a sequence: a workgroup takes kPromptRows rows of one key/value head, 32 a
+// wave, and walks the blocks of 64 tokens that the last of them sees.  Each wave converts a
+// quarter of the next block's values into the operand order of the product and leaves them
+// in LDS (two buffers, one barrier a block), so a value is converted once for 128 rows and
+// read from LDS without bank conflicts; keys go from the page into the matrix
+// instruction as in decode.
+constexpr int kPromptTiles = 2;                              // 16-row tiles per wave
+constexpr int kPromptRows = kWaves * kPromptTiles * kRows;   // rows of a workgroup
+
+template <int D>
+struct RawValues {  // 32 tokens x half of a lane's channels, converted by one wave
+    u32x4 v[2];
+    uint32_t vs[2];
+};
+
+template <int D>
+__global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attention a, int tiles) {
+    constexpr int MT = D / 16;  // channel tiles
+    __shared__ u32x4 values[2][2][MT][kWave];
+    a.b.f.dim = D;
+    const Kv4Format &f = a.b.f;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int group = a.heads / f.n_kv;
+    const Lane<D> ln(lane);
+
+    // Row tile: sequence s owns the tiles from q_start[s] * group / rows + s on, which are
+    // enough for it.  Later rows, which see more, go first; the heads of a tile go to
+    // neighbouring workgroups, that is to different XCDs, so an XCD reads few heads.
+    const int head = blockIdx.x % f.n_kv;
+    const int vt = tiles - 1 - (int)(blockIdx.x / f.n_kv);
+    int s = 0;
+    for (int n = a.b.S; n > 1;) {  // the last s whose first tile is at or before vt, 64 looks at a time
+        const int step = (n + 63) >> 6, at = s + lane * step;
+        const bool yes = lane * step < n && (int64_t)a.b.q_start[at] * group / kPromptRows + at <= vt;
+        const uint64_t m = __ballot(yes);
+        s += (m ? 63 - __clzll((long long)m) : 0) * step;
+        n = min(step, a.b.S - s);
+    }
+    const int q0 = a.b.q_start[s], n = a.b.q_start[s + 1] - q0, len = a.b.kv_len[s];
+    const int64_t rows = (int64_t)n * group;
+    if (rows <= kDecodeRows) return;
+    const int64_t r0 = (int64_t)(vt - (int)((int64_t)q0 * group / kPromptRows + s)) * kPromptRows;
+    if (r0 < 0 || r0 >= rows) return;
+
+    const float c = fmaxf(fabsf(a.scale), 1e-37f) * kLog2e;
+    const int64_t cap = (int64_t)a.b.cols * f.page;
+    const int64_t place0 = (int64_t)len - n;  // of the sequence's first row
+    const int64_t any_from = a.window > 0 ? place0 - a.window + 1 : 0;
+    const int64_t any_upto = len < cap ? (int64_t)len - 1 : cap - 1;
+
+    Pieces q[kPromptTiles];
+    Tile<D> tl[kPromptTiles];
+    int upto[kPromptTiles], from[kPromptTiles];
+    const int64_t w0 = r0 + wave * (kPromptTiles * kRows);  // the wave's first row
+#pragma unroll
+    for (int k = 0; k < kPromptTiles; ++k) {
+        const int64_t r = w0 + k * kRows + ln.col;
+        const int qi = (int)(r / group), t = q0 + qi, h = head * group + (int)(r % group);
+        const bool real = r < rows && t < a.b.T;
+        u32x4 x[4];
+        const uint16_t *p = a.q.p + t * a.q.ld + h * a.q.hd + (D == 128 ? ln.g : (ln.g & 1)) * 32;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = real ? reinterpret_cast<const u32x4 *>(p)[i] : (u32x4){0, 0, 0, 0};
+        q[k] = lane_pieces<D>(x, a.scale, ln);
+        const int64_t place = place0 + qi;
+        upto[k] = real ? (int)(place < cap ? place : cap - 1) : -1;
+        from[k] = a.window > 0 && place - a.window + 1 > 0 ? (int)(place - a.window + 1) : 0;
+        clear(tl[k]);
+    }
+    // blocks that the workgroup walks, that the wave needs, that need no mask for the wave
+    const int64_t last_row = (r0 + kPromptRows < rows ? r0 + kPromptRows : rows) - 1;
+    const int64_t see_last = place0 + last_row / group < cap ? place0 + last_row / group : cap - 1;
+    const int64_t see_first = a.window > 0 ? place0 + r0 / group - a.window + 1 : 0;
+    const int b_first = (int)((see_first > 0 ? see_first : 0) / kBlock);
+    const int b_end = see_last >= 0 ? (int)(see_last / kBlock) + 1 : 0;
+    const int64_t wl = w0 + kPromptTiles * kRows - 1;
+    const int64_t w_last = place0 + (wl < rows - 1 ? wl : rows - 1) / group;
+    const int64_t w_all = place0 + w0 / group < cap - 1 ? place0 + w0 / group : cap - 1;
+    const int64_t w_all_from = a.window > 0 ? w_last - a.window + 1 : 0;
+    const bool idle = w0 >= rows;
+
+    const int32_t *row = a.b.table + (int64_t)s * a.b.ld_table;
+    const int per = f.page / kBlock;
+    int have = -64, pages = -1;
+    auto head_of = [&](int b) -> const uint8_t * {
+        if (b >= have + 64 || have < 0) {
+            have = b;
+            const int64_t col = (int64_t)(b + lane) / per;
+            pages = col < a.b.cols && b + lane < b_end ? row[col] : -1;
+        }
+        const int page = __builtin_amdgcn_readlane(pages, b - have);
+        if (page < 0 || page >= a.b.num_pages) return nullptr;
+        return a.b.cache + (int64_t)page * f.page_bytes() + (int64_t)head * f.head_bytes() + 0;
+    };
+    // this wave's share of a block's values: tokens 32 vs .. + 31, bytes vb .. of each word
+    const int vstep = wave >> 1, vhalf = wave & 1;
+    auto load_values = [&](RawValues<D> &x, const uint8_t *hd, int b) {
+        const int tok0 = b % per * kBlock;
+        const uint8_t *v = hd + f.v_at() + tok0 * (D / 2), *vs = hd + f.vs_at() + tok0 * (D / 32);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            x.v[i] = *reinterpret_cast<const u32x4 *>(v + ln.v_off + (2 * vstep + i) * 8 * D);
+            x.vs[i] = *reinterpret_cast<const uint32_t *>(vs + ln.vs_off + (2 * vstep + i) * (D / 2));
+        }
+    };
+    auto put_values = [&](RawValues<D> &x, int b, u32x4 (*to)[MT][kWave]) {
+        const int64_t j0 = (int64_t)b * kBlock;
+        if (j0 < any_from || j0 + kBlock - 1 > any_upto) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int64_t tok = j0 + 32 * vstep + 16 * (e >> 2) + 4 * ln.g + (e & 3);
+                if (tok > any_upto || tok < any_from) x.vs[e >> 2] &= ~(255u << (8 * (e & 3)));
+            }
+        }
+        uint32_t w[8];
+        float sc[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            w[e] = x.v[e >> 2][e & 3] >> (D == 128 ? vhalf * 16 : (ln.col & 1) * 16 + vhalf * 8);
+            sc[e] = pow2_byte((x.vs[e >> 2] >> ((e & 3) * 8)) & 255u);
+        }
+#pragma unroll
+        for (int by = 0; by < D / 64; ++by) {
+            uint32_t cv[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) cv[e] = fp4_pair(w[e], sc[e], by);
+            u32x4 lo, hi;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                lo[e] = __builtin_amdgcn_perm(cv[2 * e + 1], cv[2 * e], 0x05040100u);
+                hi[e] = __builtin_amdgcn_perm(cv[2 * e + 1], cv[2 * e], 0x07060302u);
+            }
+            const int mt = 2 * (vhalf * (D / 64) + by);
+            to[vstep][mt][lane] = lo;
+            to[vstep][mt + 1][lane] = hi;
+        }
+    };
+    auto load_keys = [&](u32x4 (&k)[4], uint32_t &ks, const uint8_t *hd, int b) {
+        const int tok0 = b % per * kBlock;
+        const uint8_t *kp = hd + tok0 * (D / 2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const u32x4 *>(kp + ln.k_off + j * 8 * D);
+        ks = *reinterpret_cast<const uint32_t *>(hd + f.ks_at() + tok0 * (D / 32) + ln.ks_off);
+    };
+
+    Bytes<D> x;  // keys of the block in hand
+    RawValues<D> rv;
+    const uint8_t *now = b_first < b_end ? head_of(b_first) : nullptr;
+    if (now) {
+        load_keys(x.k, x.ks, now, b_first);
+        load_values(rv, now, b_first);
+        put_values(rv, b_first, values[b_first & 1]);
+    }
+    const uint8_t *next = b_first + 1 < b_end ? head_of(b_first + 1) : nullptr;
+    if (next) load_values(rv, next, b_first + 1);
+    __syncthreads();
+    for (int b = b_first; b < b_end; ++b) {
+        const uint8_t *after = b + 2 < b_end ? head_of(b + 2) : nullptr;
+        if (next) put_values(rv, b + 1, values[(b + 1) & 1]);
+        if (after) load_values(rv, after, b + 2);
+        const int64_t j0 = (int64_t)b * kBlock;
+        const bool work = now && !idle && j0 <= w_last && j0 + kBlock > w_all_from - (int64_t)(w_last - place0 - w0 / group);
+        f32x4 sc[kPromptTiles][4];
+        if (work) {
+#pragma unroll
+            for (int k = 0; k < kPromptTiles; ++k) scores(x, q[k], sc[k]);
+        }
+        if (next) load_keys(x.k, x.ks, next, b + 1);
+        if (work) {
+            if (j0 < w_all_from || j0 + kBlock - 1 > w_all) {
+#pragma unroll
+                for (int k = 0; k < kPromptTiles; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int tok = (int)j0 + 16 * j + 4 * ln.g + i;
+                            if (tok > upto[k] || tok < from[k]) sc[k][j][i] = -INFINITY;
+                        }
+            }
+#pragma unroll
+            for (int k = 0; k < kPromptTiles; ++k) weights(tl[k], sc[k], c);
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+                union { uint32_t w[4]; bf16x8 h; } p[kPromptTiles];
+#pragma unroll
+                for (int k = 0; k < kPromptTiles; ++k) {
+                    p[k].w[0] = pack_bf16(sc[k][2 * st][0], sc[k][2 * st][1]);
+                    p[k].w[1] = pack_bf16(sc[k][2 * st][2], sc[k][2 * st][3]);
+                    p[k].w[2] = pack_bf16(sc[k][2 * st + 1][0], sc[k][2 * st + 1][1]);
+                    p[k].w[3] = pack_bf16(sc[k][2 * st + 1][2], sc[k][2 * st + 1][3]);
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    union { u32x4 u; bf16x8 h; } v;
+                    v.u = values[b & 1][st][mt][lane];
+#pragma unroll
+                    for (int k = 0; k < kPromptTiles; ++k)
+                        tl[k].o[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v.h, p[k].h, tl[k].o[mt], 0, 0, 0);
+                }
+            }
+        }
+        now = next;
+        next = after;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < kPromptTiles; ++k) {
+        const int64_t r = w0 + k * kRows + ln.col;
+        const int t = q0 + (int)(r / group), h = head * group + (int)(r % group);
+        float o[D / 4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) o[MT * i + m] = tl[k].o[m][i];
+        const float l = cross_rows_sum(tl[k].l);
+        if (r < rows && t < a.b.T) store_row<D>(a, t, h, ln.g, o, tl[k].m * c, l, ln.g == 0);
+    }
+}
+
 int device_cus() {
     int dev = 0, cu = 0;
     if (hipGetDevice(&dev) != hipSuccess ||
@@ -587,7 +826,15 @@ size_t decode_workspace(int groups) {
 }
 
 template <int D>
-hipError_t launch_decode(const Kv4Attention &a, void *ws, hipStream_t st) {
+hipError_t launch(Kv4Attention a, int64_t max_q, void *ws, hipStream_t st) {
+    const int group = a.heads / a.b.f.n_kv;
+    // Where no sequence has many rows every one is walked by row tiles; else each goes to the
+    // kernel that its own rows ask for.
+    a.prompts = max_q * group > kDecodeRows;
+    if (a.prompts) {
+        const int64_t tiles = (int64_t)a.b.T * group / kPromptRows + a.b.S;
+        kv4_prompt_kernel<D><<<(unsigned)(tiles * a.b.f.n_kv), kWaves * kWave, 0, st>>>(a, (int)tiles);
+    }
     const int groups = device_cus() * kGroupsPerCu;
     Part<D> *parts = (Part<D> *)ws;
     PartTag *tags = (PartTag *)(parts + 2 * (size_t)groups);
@@ -603,8 +850,8 @@ size_t kv4_attention_workspace(int64_t, int64_t, int, int, int dim, int64_t) {
     return dim == 128 ? decode_workspace<128>(groups) : decode_workspace<64>(groups);
 }
 
-hipError_t launch_kv4_attention(const Kv4Attention &a, int64_t, void *ws, hipStream_t st) {
-    return a.b.f.dim == 128 ? launch_decode<128>(a, ws, st) : launch_decode<64>(a, ws, st);
+hipError_t launch_kv4_attention(const Kv4Attention &a, int64_t max_q, void *ws, hipStream_t st) {
+    return a.b.f.dim == 128 ? launch<128>(a, max_q, ws, st) : launch<64>(a, max_q, ws, st);
 }
 
 }  // namespace nmk
