@@ -9,10 +9,8 @@
 // tokens) form tiles of 16.  A wave takes one tile and walks blocks of 64 tokens:
 //   S^T [64 x 16] = K [64 x D] . Q^T: the scaled matrix instruction reads the 4-bit keys and
 //     their scales as they lie in the page (16 tokens x 128 channels an instruction), so
-//     keys cost no conversion at all.  Queries are split into three 6-bit (E2M3) pieces
-//     with a scale per 32 channels: pieces of 4-bit keys and 6-bit queries run at twice the
-//     rate of 4-bit keys and 8-bit queries, and the three of them are within 2^-15 of a
-//     block's largest query channel (the first two hold all 8 bits of the larger ones).
+//     keys cost no conversion at all.  Queries are sums of four 6-bit (E2M3) pieces, so
+//     the scores are those of the bf16 queries.
 //   O^T [D x 16] += V^T [D x 64] . P^T: S^T leaves a lane four consecutive tokens of one
 //     query row, which is what the bf16 product over tokens takes; V units of 4 tokens x 8
 //     channels give the same lane its 8 tokens of 8 channels with one conversion and one
@@ -40,14 +38,13 @@ constexpr int kDecodeRows = 64; // query rows of a head up to which a sequence i
 constexpr int kGroupsPerCu = 2; // resident workgroups: 8 waves a CU, 8.7 KB of cache in flight each
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef int i32x6 __attribute__((ext_vector_type(6)));
-typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x32 __attribute__((ext_vector_type(32)));
+typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x32 __attribute__((ext_vector_type(32)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ float pow2_byte(uint32_t byte) { return __uint_as_float(byte << 23); }
 
@@ -77,65 +74,68 @@ __device__ __forceinline__ uint32_t fp4_pair(uint32_t w, float s, int byte) {
     return c.u;
 }
 
-// Three 6-bit pieces of 32 bf16 query channels with their scale bytes in one dword.
-struct Pieces {
-    u32x6 p[3];
-    uint32_t scales;  // bytes 0..2
+// A lane's 32 query channels as four 6-bit (E2M3) pieces with a scale each: 2^-2, 2^-6,
+// 2^-11 and 2^-16 of the power of two at or below the largest of them.  What is left is at
+// most 2^-20 of that, and nothing of numbers within 2^-8 of it.  The instruction aligns the products of 8
+// neighbouring channels to about 13 bits below the largest of them: those of 4-bit and 6-bit
+// numbers always fit, those of 4-bit and 8-bit (E4M3) ones do not (two 8-bit pieces, at the
+// same matrix time, were measured 2^-17 of |q| |k| off).  At dim 64 the instruction's upper
+// 64 channels multiply the same keys again: lanes 32.. hold the second and fourth piece.
+template <int D>
+struct Query {
+    static constexpr int kSteps = D / 32;
+    u32x6 p[kSteps];
+    uint32_t scales;  // a byte for each of p
 };
 
-__device__ __forceinline__ Pieces split_query(const u32x4 (&x)[4], uint32_t signs) {
-    union { u32x4 u[4]; uint32_t w[16]; bf16x32 h; __bf16 e[32]; } q;
+template <int D>
+__device__ __forceinline__ Query<D> load_query(const uint16_t *row, bool real, float scale, int g) {
+    union { u32x4 u[4]; uint32_t w[16]; bf16x32 h; } x;
+    const int block = D == 128 ? g : (g & 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x.u[i] = real ? *reinterpret_cast<const u32x4 *>(row + block * 32 + i * 8) : (u32x4){0, 0, 0, 0};
+    const uint32_t signs = scale < 0.f ? 0x80008000u : 0u;
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q.u[i] = x[i];
-#pragma unroll
     for (int i = 0; i < 16; ++i) {
-        top = max(top, max(q.w[i] & 0x7FFFu, (q.w[i] >> 16) & 0x7FFFu));
-        q.w[i] ^= signs;
+        top = max(top, max(x.w[i] & 0x7FFFu, (x.w[i] >> 16) & 0x7FFFu));
+        x.w[i] ^= signs;
     }
-    const uint32_t e = max(top >> 7, 13u);  // biased exponent of the largest magnitude
-    Pieces r;
-    r.scales = (e - 2) | (e - 6) << 8 | (e - 11) << 16;
-    const uint32_t at[3] = {e - 2, e - 6, e - 11};
+    const uint32_t e = max(top >> 7, 20u);  // biased exponent of the largest magnitude
+    const uint32_t at[4] = {e - 2, e - 6, e - 11, e - 16};
+    u32x6 p[4];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
+    for (int k = 0; k < 4; ++k) {
         const float s = pow2_byte(at[k]);
-        r.p[k] = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(q.h, s);
-        if (k < 2) {  // what is left is a bf16 number: at most the bits the piece did not take
-            const f32x32 d = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(r.p[k], s);
+        p[k] = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(x.h, s);
+        if (k < 3) {  // what is left is a bf16 number: the bits that the piece did not take
+            const f32x32 d = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(p[k], s);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                q.w[i] = pack_bf16((float)q.e[2 * i] - d[2 * i], (float)q.e[2 * i + 1] - d[2 * i + 1]);
+                x.w[i] = pack_bf16(bf16_lo(x.w[i]) - d[2 * i], bf16_hi(x.w[i]) - d[2 * i + 1]);
         }
     }
-    return r;
+    Query<D> q;
+    if constexpr (D == 128) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q.p[k] = p[k];
+        q.scales = at[0] | at[1] << 8 | at[2] << 16 | at[3] << 24;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) q.p[k] = g < 2 ? p[2 * k] : p[2 * k + 1];
+        q.scales = g < 2 ? at[0] | at[2] << 8 : at[1] | at[3] << 8;
+    }
+    return q;
 }
 
-// Operands of the scaled matrix instruction: 4-bit formats read four registers, 6-bit ones
-// six; the rest of the type is never read.
+// Of the scaled matrix instruction's operands 4-bit formats are read from four registers
+// and 6-bit ones from six; the rest of the type is never read.
 __device__ __forceinline__ i32x8 wide(u32x6 v) {
     return (i32x8)__builtin_shufflevector(v, v, 0, 1, 2, 3, 4, 5, -1, -1);
 }
 __device__ __forceinline__ i32x8 wide(u32x4 v) {
     return (i32x8)__builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
-}
-
-// The pieces as a lane multiplies them.  At dim 64 the matrix instruction's upper 64
-// channels multiply the same keys again: lanes 32.. hold the second piece in the first's
-// place, and nothing in the third's.
-template <int D>
-struct Lane;
-template <int D>
-__device__ __forceinline__ Pieces lane_pieces(const u32x4 (&x)[4], float scale, const Lane<D> &ln) {
-    Pieces q = split_query(x, scale < 0.f ? 0x80008000u : 0u);
-    if constexpr (D == 64) {
-        if (ln.g >= 2) {
-            q.p[0] = q.p[1];
-            q.scales = (q.scales >> 8 & 255u) | (q.scales & 0xFF0000u);
-            q.p[2] = (u32x6){0, 0, 0, 0, 0, 0};
-        }
-    }
-    return q;
 }
 
 // What a sequence asks of a call.
@@ -222,19 +222,16 @@ __device__ __forceinline__ void load_block(Bytes<D> &x, const uint8_t *head, con
 
 // Scores of 64 tokens: s[j][i] is token 16 j + 4 g + i of the column's row.
 template <int D>
-__device__ __forceinline__ void scores(const Bytes<D> &x, const Pieces &q, f32x4 (&s)[4]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ void scores(const Bytes<D> &x, const Query<D> &q, f32x4 (&s)[4]) {
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     const int sc = (int)q.scales, ks = (int)x.ks;
-#define NM_KV4_DOT(J, P) \
-    s[J] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(x.k[J]), wide(q.p[P]), s[J], 4, 2, J, ks, P, sc)
+#define NM_KV4_DOT(J, P, C) \
+    s[J] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(x.k[J]), wide(q.p[P]), C, 4, 2, J, ks, P, sc)
+    NM_KV4_DOT(0, 0, zero); NM_KV4_DOT(1, 0, zero); NM_KV4_DOT(2, 0, zero); NM_KV4_DOT(3, 0, zero);
+    NM_KV4_DOT(0, 1, s[0]); NM_KV4_DOT(1, 1, s[1]); NM_KV4_DOT(2, 1, s[2]); NM_KV4_DOT(3, 1, s[3]);
     if constexpr (D == 128) {
-        NM_KV4_DOT(0, 0); NM_KV4_DOT(1, 0); NM_KV4_DOT(2, 0); NM_KV4_DOT(3, 0);
-        NM_KV4_DOT(0, 1); NM_KV4_DOT(1, 1); NM_KV4_DOT(2, 1); NM_KV4_DOT(3, 1);
-        NM_KV4_DOT(0, 2); NM_KV4_DOT(1, 2); NM_KV4_DOT(2, 2); NM_KV4_DOT(3, 2);
-    } else {  // the upper half of the instruction's channels multiplies the second piece
-        NM_KV4_DOT(0, 0); NM_KV4_DOT(1, 0); NM_KV4_DOT(2, 0); NM_KV4_DOT(3, 0);
-        NM_KV4_DOT(0, 2); NM_KV4_DOT(1, 2); NM_KV4_DOT(2, 2); NM_KV4_DOT(3, 2);
+        NM_KV4_DOT(0, 2, s[0]); NM_KV4_DOT(1, 2, s[1]); NM_KV4_DOT(2, 2, s[2]); NM_KV4_DOT(3, 2, s[3]);
+        NM_KV4_DOT(0, 3, s[0]); NM_KV4_DOT(1, 3, s[1]); NM_KV4_DOT(2, 3, s[2]); NM_KV4_DOT(3, 3, s[3]);
     }
 #undef NM_KV4_DOT
 }
@@ -454,15 +451,7 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attenti
             const int64_t r = (int64_t)tile * kRows + ln.col;
             const int qi = (int)(r / group), t = sq.q0 + qi, h = head * group + (int)(r % group);
             const bool real = r < (int64_t)sq.n * group && t < a.b.T;
-            Pieces q;
-            {
-                u32x4 x[4];
-                const uint16_t *p = a.q.p + t * a.q.ld + h * a.q.hd + (D == 128 ? ln.g : (ln.g & 1)) * 32;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[i] = real ? reinterpret_cast<const u32x4 *>(p)[i] : (u32x4){0, 0, 0, 0};
-                q = lane_pieces<D>(x, a.scale, ln);
-            }
+            const Query<D> q = load_query<D>(a.q.p + t * a.q.ld + h * a.q.hd, real, a.scale, ln.g);
             // keys that my row sees: [from, upto]
             const int64_t place = (int64_t)sq.len - sq.n + qi;
             const int64_t cap = (int64_t)a.b.cols * f.page;
@@ -640,7 +629,7 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
     const int64_t any_from = a.window > 0 ? place0 - a.window + 1 : 0;
     const int64_t any_upto = len < cap ? (int64_t)len - 1 : cap - 1;
 
-    Pieces q[kPromptTiles];
+    Query<D> q[kPromptTiles];
     Tile<D> tl[kPromptTiles];
     int upto[kPromptTiles], from[kPromptTiles];
     const int64_t w0 = r0 + wave * (kPromptTiles * kRows);  // the wave's first row
@@ -649,11 +638,7 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
         const int64_t r = w0 + k * kRows + ln.col;
         const int qi = (int)(r / group), t = q0 + qi, h = head * group + (int)(r % group);
         const bool real = r < rows && t < a.b.T;
-        u32x4 x[4];
-        const uint16_t *p = a.q.p + t * a.q.ld + h * a.q.hd + (D == 128 ? ln.g : (ln.g & 1)) * 32;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = real ? reinterpret_cast<const u32x4 *>(p)[i] : (u32x4){0, 0, 0, 0};
-        q[k] = lane_pieces<D>(x, a.scale, ln);
+        q[k] = load_query<D>(a.q.p + t * a.q.ld + h * a.q.hd, real, a.scale, ln.g);
         const int64_t place = place0 + qi;
         upto[k] = real ? (int)(place < cap ? place : cap - 1) : -1;
         from[k] = a.window > 0 && place - a.window + 1 > 0 ? (int)(place - a.window + 1) : 0;

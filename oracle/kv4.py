@@ -111,14 +111,13 @@ def rows_of(cache, table, kv_len, q_start, ps, H, D, T):
 def attention(q, cache, table, kv_len, q_start, ps, n_kv, scale, window):
     """q fp64 [T, Hq, D] -> dict of fp64 arrays over the rows of the sequences (NaN behind them):
     out [T, Hq, D], lse [T, Hq]; absum = sum_j p_j |V_j| [T, Hq, D], and over the seen keys of a row the largest
-    scale * sum |q K| (smax) and scale * sum over 32-channel blocks of max |q| * sum |K| (sblk), the largest |V|
+    scale * sum |q K| (smax) and scale * max |q| * sum |K| (srow), the largest |V|
     (vmax) and their number (keys)."""
     T, Hq, D = q.shape
     K, V = unpack_pages(cache, ps, n_kv, D)
     r = {"out": np.full((T, Hq, D), np.nan), "absum": np.full((T, Hq, D), np.nan)}
-    for n in ("lse", "smax", "sblk", "vmax", "keys"):
+    for n in ("lse", "smax", "srow", "vmax", "keys"):
         r[n] = np.full((T, Hq), np.nan)
-    qb = np.repeat(np.abs(q).reshape(T, Hq, -1, 32).max(-1), 32, -1)
     for s in range(len(kv_len)):
         n = int(q_start[s + 1] - q_start[s])
         end = int(kv_len[s])
@@ -141,7 +140,7 @@ def attention(q, cache, table, kv_len, q_start, ps, n_kv, scale, window):
                     see &= j > p - window
                 r["keys"][t, h] = see.sum()
                 if not see.any():
-                    r["out"][t, h] = r["absum"][t, h] = r["smax"][t, h] = r["sblk"][t, h] = r["vmax"][t, h] = 0.0
+                    r["out"][t, h] = r["absum"][t, h] = r["smax"][t, h] = r["srow"][t, h] = r["vmax"][t, h] = 0.0
                     r["lse"][t, h] = -np.inf
                     continue
                 k, v = Ks[see], Vs[see]
@@ -154,7 +153,7 @@ def attention(q, cache, table, kv_len, q_start, ps, n_kv, scale, window):
                 r["lse"][t, h] = m + np.log(l)
                 r["vmax"][t, h] = np.abs(v).max()
                 r["smax"][t, h] = abs(scale) * (np.abs(k) @ np.abs(q[t, h])).max()
-                r["sblk"][t, h] = abs(scale) * (np.abs(k) @ qb[t, h]).max()
+                r["srow"][t, h] = abs(scale) * np.abs(k).sum(-1).max() * np.abs(q[t, h]).max()
     return r
 
 

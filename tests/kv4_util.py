@@ -57,8 +57,8 @@ def poison(cache, table, kv_len, ps, H, D):
 def attention_bounds(r):
     """Largest differences of (out, lse) from the fp64 results r that the arithmetic allows.
 
-    Scores: a query block is held as three 6-bit pieces, at most 2^-15 of its largest magnitude off
-    (three_pieces goes through every number a block can hold); the products
+    Scores: 32 channels of a query are held as four 6-bit pieces, at most 2^-20 of their largest magnitude off
+    (four_pieces goes through every number they can hold); the products
     are exact and their 128 sums, the scale and log2(e) round in fp32: 136 steps of 2^-24 of sum |q K|; the
     exponent's argument and exp2 itself: 4 steps of the largest score.  exp(x) is off by the score's
     difference, for weight and for sum, hence 2 delta.  Weights are rounded to bf16 for the products, 2^-8 (half
@@ -66,7 +66,7 @@ def attention_bounds(r):
     rounded once to bf16.  Weights below 2^-126 of a row's largest and products below 2^-126 are not normal
     fp32 numbers and may count as 0: each key then lacks at most 2^-126 (|V| + 1)."""
     keys = r["keys"]
-    delta = 2.0**-15 * r["sblk"] + 140 * 2.0**-24 * r["smax"] + 2.0**-22
+    delta = 2.0**-20 * r["srow"] + 140 * 2.0**-24 * r["smax"] + 2.0**-22
     fp32 = 2.0**-24 * (keys + 64)
     lse = delta + fp32 + 2.0**-22 * np.abs(np.where(np.isfinite(r["lse"]), r["lse"], 0.0))
     rel = (2.0**-8 + 2 * delta + 2 * fp32)[..., None]
@@ -78,12 +78,12 @@ def attention_bounds(r):
 E2M3 = np.array([m / 8 for m in range(8)] + [(1 + m / 8) * 2.0**e for e in range(3) for m in range(8)])
 
 
-def three_pieces(q):
-    """What three E2M3 pieces with scales of 2^-2, 2^-6 and 2^-11 leave of numbers of a block whose largest
-    magnitude is in [1, 2): rounding to nearest, 7.5 the largest."""
+def four_pieces(q):
+    """What four E2M3 pieces with scales of 2^-2, 2^-6, 2^-11 and 2^-16 leave of numbers of a block whose
+    largest magnitude is in [1, 2): rounding to nearest, a tie to the even code, 7.5 the largest."""
     rest = np.asarray(q, dtype=np.float64)
-    order = np.concatenate([np.arange(0, 32, 2), np.arange(1, 32, 2)])  # the even code of two equally near ones
-    for s in (2, 6, 11):
+    order = np.concatenate([np.arange(0, 32, 2), np.arange(1, 32, 2)])
+    for s in (2, 6, 11, 16):
         a = np.abs(rest) * 2.0**s
         near = E2M3[order[np.argmin(np.abs(a[..., None] - E2M3[order]), -1)]]
         rest = rest - np.sign(rest) * near * 2.0**-s

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from oracle import kv4
-from tests.kv4_util import bf16, three_pieces
+from tests.kv4_util import bf16, four_pieces
 
 
 def test_every_place_of_a_block_is_used_once():
@@ -94,8 +94,8 @@ def test_a_pool_that_runs_out_serves_the_first():
     assert missing == 2 and list(kv_len) == [64, 0, 0] and list(refs) == [1, 0]
 
 
-def test_three_pieces_hold_every_query_number():
+def test_four_pieces_hold_every_query_number():
     """Every bf16 number of a block whose largest magnitude is in [1, 2), down to where all of it is below the bound."""
-    q = np.concatenate([np.arange(128, 256) / 128.0 * 2.0**-d for d in range(24)])
-    assert np.abs(three_pieces(q)).max() <= 2.0**-15
-    assert (three_pieces(q[: 128 * 4]) == 0).all()  # within 2^-3 of the largest nothing is lost
+    q = np.concatenate([np.arange(128, 256) / 128.0 * 2.0**-d for d in range(40)])
+    assert np.abs(four_pieces(q)).max() <= 2.0**-20
+    assert (four_pieces(q[: 128 * 9]) == 0).all()  # within 2^-8 of the largest nothing is lost
