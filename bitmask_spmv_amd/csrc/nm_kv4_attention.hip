@@ -46,6 +46,12 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x32 __attribute__((ext_vector_type(32)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+// A read with a wave-uniform address of data that no kernel in flight writes: through the
+// scalar cache, so it does not enter the order in which a wave's vector loads return.
+__device__ __forceinline__ int32_t uniform_load(const int32_t *p) {
+    return *(const __attribute__((address_space(4))) int32_t *)(uintptr_t)p;
+}
+
 __device__ __forceinline__ float pow2_byte(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 __device__ __forceinline__ float rows_max(float v) {  // over the four lanes of a column
@@ -146,12 +152,8 @@ struct Seq {
     __device__ int64_t units(int n_kv) const { return (int64_t)tiles * n_kv * blocks; }
 };
 
-__device__ __forceinline__ Seq seq_of(const Kv4Attention &a, int s, int group) {
-    Seq q = {0, 0, 0, 0, 0, 1};
-    if (s >= a.b.S) return q;
-    q.q0 = a.b.q_start[s];
-    q.n = a.b.q_start[s + 1] - q.q0;
-    q.len = a.b.kv_len[s];
+__device__ __forceinline__ Seq seq_from(const Kv4Attention &a, int group, int q0, int q1, int len) {
+    Seq q = {q0, q1 - q0, len, 0, 0, 1};
     if (q.n <= 0 || (a.prompts && (int64_t)q.n * group > kDecodeRows)) {
         q.n = 0;
         return q;
@@ -165,6 +167,64 @@ __device__ __forceinline__ Seq seq_of(const Kv4Attention &a, int s, int group) {
     const int64_t last = (end + kBlock - 1) / kBlock;
     q.blocks = last > q.first ? (int)(last - q.first) : 1;
     return q;
+}
+
+// Sixty-four sequences, one a lane (behind the last one: without rows), and the inclusive
+// prefix sums of their units.
+struct SeqLane {
+    int q0, q1, len;
+    __device__ void load(const Kv4Batch &b, int s) {
+        q0 = q1 = len = 0;
+        if (s < b.S) {
+            q0 = b.q_start[s];
+            q1 = b.q_start[s + 1];
+            len = b.kv_len[s];
+        }
+    }
+};
+
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ uint32_t dpp_scan_add(uint32_t v) {
+    return v + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, kRowMask, 0xF, false);
+}
+
+__device__ __forceinline__ int64_t units_scan(int64_t w, int lane) {
+    if (__builtin_expect(__any(w >> 25) == 0, 1)) {  // 64 of them fit in 31 bits
+        uint32_t v = (uint32_t)w;
+        v = dpp_scan_add<0x111, 0xF>(v);  // shifts within rows of 16 lanes
+        v = dpp_scan_add<0x112, 0xF>(v);
+        v = dpp_scan_add<0x114, 0xF>(v);
+        v = dpp_scan_add<0x118, 0xF>(v);
+        v = dpp_scan_add<0x142, 0xA>(v);  // last lane of rows 0 and 2 to rows 1 and 3
+        v = dpp_scan_add<0x143, 0xC>(v);  // lane 31 to the upper half
+        return v;
+    }
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t u = __shfl_up(w, d);
+        if (lane >= d) w += u;
+    }
+    return w;
+}
+
+// A value that is the same in all lanes, or lane i's, in scalar registers.
+__device__ __forceinline__ int64_t lane64(int64_t v, int i) {
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, i);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)v >> 32), i);
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// The page of 64-token block b of a sequence's table row, -1 where there is none.
+__device__ __forceinline__ int page_of(const Kv4Batch &b, const int32_t *row, int block) {
+    const int col = block / (b.f.page / kBlock);
+    if (block < 0 || col >= b.cols) return -1;
+    const int page = uniform_load(row + col);
+    return page < b.num_pages ? page : -1;
+}
+
+// Head block of a page; that of page 0 for no page, so that loads need no branch (a branch
+// around them would make the wave wait for all it has in flight).
+__device__ __forceinline__ const uint8_t *head_block(const Kv4Batch &b, int page, int head) {
+    return b.cache + (int64_t)(page < 0 ? 0 : page) * b.f.page_bytes() + (int64_t)head * b.f.head_bytes();
 }
 
 // One tile's running softmax in registers: column c = lane % 16 is query row c, the four
@@ -206,18 +266,24 @@ struct Lane {
     }
 };
 
-template <int D>
+// NT: bytes that are read once (one row tile per head) stay out of the caches' way.
+template <bool NT, class T>
+__device__ __forceinline__ T load_cache(const uint8_t *p) {
+    return NT ? __builtin_nontemporal_load(reinterpret_cast<const T *>(p)) : *reinterpret_cast<const T *>(p);
+}
+
+template <int D, bool NT>
 __device__ __forceinline__ void load_block(Bytes<D> &x, const uint8_t *head, const Kv4Format &f, int tok0,
                                            const Lane<D> &ln) {
     const uint8_t *k = head + tok0 * (D / 2), *v = head + f.v_at() + tok0 * (D / 2);
     const uint8_t *ks = head + f.ks_at() + tok0 * (D / 32), *vs = head + f.vs_at() + tok0 * (D / 32);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x.k[j] = *reinterpret_cast<const u32x4 *>(k + ln.k_off + j * 8 * D);
-    x.ks = *reinterpret_cast<const uint32_t *>(ks + ln.ks_off);
+    for (int j = 0; j < 4; ++j) x.k[j] = load_cache<NT, u32x4>(k + ln.k_off + j * 8 * D);
+    x.ks = load_cache<NT, uint32_t>(ks + ln.ks_off);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x.v[j] = *reinterpret_cast<const u32x4 *>(v + ln.v_off + j * 8 * D);
+    for (int j = 0; j < 4; ++j) x.v[j] = load_cache<NT, u32x4>(v + ln.v_off + j * 8 * D);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x.vs[j] = *reinterpret_cast<const uint32_t *>(vs + ln.vs_off + j * (D / 2));
+    for (int j = 0; j < 4; ++j) x.vs[j] = load_cache<NT, uint32_t>(vs + ln.vs_off + j * (D / 2));
 }
 
 // Scores of 64 tokens: s[j][i] is token 16 j + 4 g + i of the column's row.
@@ -311,18 +377,19 @@ __device__ __forceinline__ void store_row(const Kv4Attention &a, int t, int h, i
 }
 
 // Pieces of rows cut between waves (LDS) or workgroups (workspace): unnormalised O by
-// row, the maximum (log2 units, scaled) and the sum.
+// row, the maximum (log2 units, scaled) and the sum.  The rows' stride keeps the 16 columns
+// of a wave on different banks.
 template <int D>
 struct Part {
-    float o[kRows][D];
+    float o[kRows][D + 4];
     float m[kRows], l[kRows];
 };
 
 enum : int { kNone = 0, kEnds = 1, kThrough = 2 };  // the item's last block is in / behind the piece
 
 struct PartTag {
-    int state;        // kNone, kEnds, kThrough
-    int s, head, tile;
+    int state;                  // kNone, kEnds, kThrough
+    int q0, head, tile, rows;   // the sequence's first row, the row tile and its rows
 };
 
 template <int D>
@@ -347,182 +414,175 @@ __device__ __forceinline__ void keep_part(Part<D> &p, const Tile<D> &t, float c,
     }
 }
 
+__device__ __forceinline__ float weight_of(float m, float top) {
+    return m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
+}
+
 // Threads of a workgroup over a part: 16 rows x 16 threads of D/16 channels.
 template <int D>
 struct Join {
-    float o[D / 16], m, l;
+    static constexpr int N = D / 16;
+    float o[N], m, l;
     __device__ Join() : m(-INFINITY), l(0.f) {
-        for (int i = 0; i < D / 16; ++i) o[i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = 0.f;
     }
     __device__ void add(const Part<D> &p, int row, int c) {
         const float pm = p.m[row], mn = fmaxf(m, pm);
-        const float mine = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
-        const float its = pm == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(pm - mn);
+        const float mine = weight_of(m, mn), its = weight_of(pm, mn);
         l = l * mine + p.l[row] * its;
-        for (int i = 0; i < D / 16; ++i) o[i] = o[i] * mine + p.o[row][c * (D / 16) + i] * its;
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = o[i] * mine + p.o[row][c * N + i] * its;
         m = mn;
     }
     __device__ void put(Part<D> &p, int row, int c) const {
-        for (int i = 0; i < D / 16; ++i) p.o[row][c * (D / 16) + i] = o[i];
+#pragma unroll
+        for (int i = 0; i < N; ++i) p.o[row][c * N + i] = o[i];
         if (c == 0) {
             p.m[row] = m;
             p.l[row] = l;
         }
     }
     __device__ void finish(const Kv4Attention &a, const PartTag &tag, int group, int row, int c) const {
-        const int q0 = a.b.q_start[tag.s], n = a.b.q_start[tag.s + 1] - q0;
-        const int64_t r = (int64_t)tag.tile * kRows + row;
-        if (r >= (int64_t)n * group) return;
-        const int t = q0 + (int)(r / group), h = tag.head * group + (int)(r % group);
+        if (row >= tag.rows) return;
+        const int r = tag.tile * kRows + row;
+        const int t = tag.q0 + r / group, h = tag.head * group + r % group;
         if (t >= a.b.T) return;
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        uint32_t *p = reinterpret_cast<uint32_t *>(a.out.p + t * a.out.ld + h * a.out.hd + c * (D / 16));
-        for (int i = 0; i < D / 32; ++i) p[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
+        uint32_t *p = reinterpret_cast<uint32_t *>(a.out.p + t * a.out.ld + h * a.out.hd + c * N);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) p[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
         if (c == 0 && a.lse) a.lse[t * a.ld_lse + h] = l > 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
     }
 };
 
-__device__ __forceinline__ int64_t wave_sum64(int64_t v) {
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-    return v;
-}
-
-__device__ __forceinline__ int64_t wave_scan64(int64_t v, int lane) {
-    for (int d = 1; d < 64; d <<= 1) {
-        const int64_t u = __shfl_up(v, d);
-        if (lane >= d) v += u;
-    }
-    return v;
-}
-
-template <int D>
+template <int D, bool NT>
 __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attention a, Part<D> *parts, PartTag *tags) {
     __shared__ Shared<D> sh;
     a.b.f.dim = D;
     const Kv4Format &f = a.b.f;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int group = a.heads / f.n_kv;
     const Lane<D> ln(lane);
-    const float scale = fabsf(a.scale);
-    const float c = fmaxf(scale, 1e-37f) * kLog2e;  // a scale of 0 leaves scores of 0
+    const float c = fmaxf(fabsf(a.scale), 1e-37f) * kLog2e;  // a scale of 0 leaves scores of 0
+    const int64_t cap = (int64_t)a.b.cols * f.page;
 
     // my run of units
-    int64_t total = 0;
-    for (int s0 = 0; s0 < a.b.S; s0 += 64) total += wave_sum64(seq_of(a, s0 + lane, group).units(f.n_kv));
+    SeqLane sl, behind;
+    sl.load(a.b, lane);
+    int64_t w = seq_from(a, group, sl.q0, sl.q1, sl.len).units(f.n_kv);
+    int64_t upto = units_scan(w, lane);
+    int64_t total = lane64(upto, 63);
+    for (int s0 = 64; s0 < a.b.S; s0 += 64) {
+        if (s0 == 64) behind.load(a.b, s0 + lane);
+        const SeqLane x = behind;
+        behind.load(a.b, s0 + 64 + lane);
+        total += lane64(units_scan(seq_from(a, group, x.q0, x.q1, x.len).units(f.n_kv), lane), 63);
+    }
     const int64_t waves = (int64_t)gridDim.x * kWaves;
-    const int64_t run = (total + waves - 1) / waves;
+    const int64_t run = total < ((int64_t)1 << 31) ? (int64_t)(((uint32_t)total + (uint32_t)waves - 1) / (uint32_t)waves)
+                                                   : (total + waves - 1) / waves;
     int64_t u = ((int64_t)blockIdx.x * kWaves + wave) * run;
     const int64_t end = u + run < total ? u + run : total;
     if (lane < 2) sh.tag[wave][lane].state = kNone;
 
-    if (u < end) {
+    int s0 = 0;        // the 64 sequences that the lanes hold
+    int64_t base = 0;  // units before them
+    while (u < end) {
         // the sequence that unit u is in
-        int s = 0;
-        int64_t base = 0;
-        for (int s0 = 0; s0 < a.b.S; s0 += 64) {
-            const int64_t w = seq_of(a, s0 + lane, group).units(f.n_kv);
-            const int64_t upto = base + wave_scan64(w, lane);
-            const uint64_t behind = __ballot(upto > u);
-            if (behind) {
-                const int at = __builtin_ctzll(behind);
-                s = s0 + at;
-                base = __shfl(upto - w, at);
-                break;
-            }
-            base = __shfl(upto, 63);
+        const uint64_t past = __ballot(base + upto > u);
+        if (!past) {
+            base += lane64(upto, 63);
+            s0 += 64;
+            sl.load(a.b, s0 + lane);
+            w = seq_from(a, group, sl.q0, sl.q1, sl.len).units(f.n_kv);
+            upto = units_scan(w, lane);
+            continue;
         }
-        s = __builtin_amdgcn_readfirstlane(s);
-        while (u < end) {
-            const Seq sq = seq_of(a, s, group);
-            const int64_t mine = sq.units(f.n_kv);
-            if (u - base >= mine) {
-                base += mine;
-                ++s;
-                continue;
-            }
-            const int64_t in = u - base;
-            const int item = (int)(in / sq.blocks), b0 = (int)(in % sq.blocks);
-            const int64_t room = end - u;
-            const int b1 = (int)(room < sq.blocks - b0 ? b0 + room : sq.blocks);
-            const int head = item / sq.tiles, tile = item % sq.tiles;
-            u += b1 - b0;
+        const int at = __builtin_ctzll(past), s = s0 + at;
+        const Seq sq = seq_from(a, group, __builtin_amdgcn_readlane(sl.q0, at), __builtin_amdgcn_readlane(sl.q1, at),
+                                __builtin_amdgcn_readlane(sl.len, at));
+        const int64_t in = u - base - lane64(upto - w, at);
+        const int item = in < ((int64_t)1 << 31) ? (int)((uint32_t)in / (uint32_t)sq.blocks) : (int)(in / sq.blocks);
+        const int b0 = (int)(in - (int64_t)item * sq.blocks);
+        const int64_t room = end - u;
+        const int b1 = (int)(room < sq.blocks - b0 ? b0 + room : sq.blocks);
+        const int head = item / sq.tiles, tile = item - head * sq.tiles;
+        u += b1 - b0;
 
-            // queries of my column
-            const int64_t r = (int64_t)tile * kRows + ln.col;
-            const int qi = (int)(r / group), t = sq.q0 + qi, h = head * group + (int)(r % group);
-            const bool real = r < (int64_t)sq.n * group && t < a.b.T;
-            const Query<D> q = load_query<D>(a.q.p + t * a.q.ld + h * a.q.hd, real, a.scale, ln.g);
-            // keys that my row sees: [from, upto]
-            const int64_t place = (int64_t)sq.len - sq.n + qi;
-            const int64_t cap = (int64_t)a.b.cols * f.page;
-            const int upto = real ? (int)(place < cap ? place : cap - 1) : -1;
-            const int from = a.window > 0 && place - a.window + 1 > 0 ? (int)(place - a.window + 1) : 0;
-            // blocks in which every row of the sequence sees every token need no mask
-            const int64_t all_from = a.window > 0 ? (int64_t)sq.len - a.window : 0;
-            const int64_t all_upto = (int64_t)sq.len - sq.n < cap - 1 ? (int64_t)sq.len - sq.n : cap - 1;
-            // tokens that any row of the sequence sees
-            const int64_t any_from = a.window > 0 ? (int64_t)sq.len - sq.n - a.window + 1 : 0;
-            const int64_t any_upto = (int64_t)sq.len < cap ? (int64_t)sq.len - 1 : cap - 1;
+        // two blocks in flight: the next one's loads are under way while one is multiplied
+        const int32_t *row = a.b.table + (int64_t)s * a.b.ld_table;
+        const int per = f.page / kBlock;
+        auto load = [&](Bytes<D> &x, int page, int b) {
+            load_block<D, NT>(x, head_block(a.b, page, head), f, ((sq.first + b) & (per - 1)) * kBlock, ln);
+        };
+        Bytes<D> x0, x1;
+        int p0 = page_of(a.b, row, sq.first + b0), p1 = page_of(a.b, row, sq.first + b0 + 1);
+        load(x0, p0, b0);
 
-            Tile<D> tl;
-            clear(tl);
-            const int32_t *row = a.b.table + (int64_t)s * a.b.ld_table;
-            const int per = f.page / kBlock;
-            int have = -64;  // first of the 64 blocks whose pages the lanes hold
-            int pages = -1;
-            auto head_of = [&](int b) -> const uint8_t * {  // block b of the walk, null without a valid page
-                if (b >= have + 64 || have < 0) {
-                    have = b;
-                    const int64_t col = (int64_t)(sq.first + b + lane) / per;
-                    pages = col < a.b.cols && b + lane < b1 ? row[col] : -1;
-                }
-                const int page = __builtin_amdgcn_readlane(pages, b - have);
-                if (page < 0 || page >= a.b.num_pages) return nullptr;
-                return a.b.cache + (int64_t)page * f.page_bytes() + (int64_t)head * f.head_bytes();
-            };
-            const uint8_t *now = head_of(b0);
-            Bytes<D> x;
-            if (now) load_block(x, now, f, (sq.first + b0) % per * kBlock, ln);
-            for (int b = b0; b < b1; ++b) {
-                Bytes<D> nx;
-                const uint8_t *next = b + 1 < b1 ? head_of(b + 1) : nullptr;
-                if (next) load_block(nx, next, f, (sq.first + b + 1) % per * kBlock, ln);
-                if (now) {
-                    const int64_t j0 = (int64_t)(sq.first + b) * kBlock;
-                    f32x4 sc[4];
-                    scores(x, q, sc);
-                    if (j0 < all_from || j0 + kBlock - 1 > all_upto) {
+        // queries of my column
+        const int64_t r = (int64_t)tile * kRows + ln.col;
+        const int qi = (int)r / group, t = sq.q0 + qi, h = head * group + ((int)r - qi * group);
+        const bool real = r < (int64_t)sq.n * group && t < a.b.T;
+        const Query<D> q = load_query<D>(a.q.p + t * a.q.ld + h * a.q.hd, real, a.scale, ln.g);
+        // keys that my row sees: [from, upto]
+        const int64_t place = (int64_t)sq.len - sq.n + qi;
+        const int see_last = real ? (int)(place < cap ? place : cap - 1) : -1;
+        const int see_first = a.window > 0 && place - a.window + 1 > 0 ? (int)(place - a.window + 1) : 0;
+        // tokens that every row of the sequence sees (their blocks need no mask), and that any of them sees
+        const int all_first = a.window > 0 && sq.len > a.window ? (int)(sq.len - a.window) : 0;
+        const int all_last = (int)((int64_t)sq.len - sq.n < cap ? (int64_t)sq.len - sq.n : cap - 1);
+        const int64_t some = (int64_t)sq.len - sq.n - a.window + 1;
+        const int any_first = a.window > 0 && some > 0 ? (int)some : 0;
+        const int any_last = (int)((int64_t)sq.len < cap ? (int64_t)sq.len : cap) - 1;
+
+        Tile<D> tl;
+        clear(tl);
+        auto add = [&](Bytes<D> &x, int b) {
+            const int j0 = (sq.first + b) * kBlock;
+            f32x4 sc[4];
+            scores(x, q, sc);
+            if (j0 < all_first || j0 + (kBlock - 1) > all_last) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int64_t tok = j0 + 16 * j + 4 * ln.g + i;
-                                if (tok > upto || tok < from) sc[j][i] = -INFINITY;
-                                // a weight of 0 times what an unseen place holds must be 0
-                                if (tok > any_upto || tok < any_from) x.vs[j] &= ~(255u << (8 * i));
-                            }
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = j0 + 16 * j + 4 * ln.g + i;
+                        if (tok > see_last || tok < see_first) sc[j][i] = -INFINITY;
+                        // a weight of 0 times what an unseen place holds must be 0
+                        if (tok > any_last || tok < any_first) x.vs[j] &= ~(255u << (8 * i));
                     }
-                    weights(tl, sc, c);
-                    add_values(tl, x, sc, ln.col);
-                }
-                now = next;
-                x = nx;
             }
+            weights(tl, sc, c);
+            add_values(tl, x, sc, ln.col);
+        };
+        for (int b = b0; b < b1; b += 2) {
+            const int p2 = page_of(a.b, row, sq.first + b + 2);
+            load(x1, p1, b + 1);
+            if (p0 >= 0) add(x0, b);
+            if (b + 1 >= b1) break;
+            const int p3 = page_of(a.b, row, sq.first + b + 3);
+            load(x0, p2, b + 2);
+            if (p1 >= 0) add(x1, b + 1);
+            p0 = p2;
+            p1 = p3;
+        }
 
-            const bool begins = b0 == 0, ends = b1 == sq.blocks;
-            if (begins && ends) {
-                float o[D / 4];
+        const bool begins = b0 == 0, ends = b1 == sq.blocks;
+        if (begins && ends) {
+            float o[D / 4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int m = 0; m < D / 16; ++m) o[(D / 16) * i + m] = tl.o[m][i];
-                const float l = cross_rows_sum(tl.l);
-                if (real) store_row<D>(a, t, h, ln.g, o, tl.m * c, l, ln.g == 0);
-            } else {
-                const int slot = begins ? 1 : 0;
-                keep_part(sh.part[wave][slot], tl, c, ln);
-                if (lane == 0) sh.tag[wave][slot] = {ends ? kEnds : kThrough, s, head, tile};
-            }
+                for (int m = 0; m < D / 16; ++m) o[(D / 16) * i + m] = tl.o[m][i];
+            const float l = cross_rows_sum(tl.l);
+            if (real) store_row<D>(a, t, h, ln.g, o, tl.m * c, l, ln.g == 0);
+        } else {
+            const int slot = begins ? 1 : 0;
+            keep_part(sh.part[wave][slot], tl, c, ln);
+            const int64_t left = (int64_t)sq.n * group - (int64_t)tile * kRows;
+            if (lane == 0)
+                sh.tag[wave][slot] = {ends ? kEnds : kThrough, sq.q0, head, tile, (int)(left < kRows ? left : kRows)};
         }
     }
     __syncthreads();
@@ -531,12 +591,11 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attenti
     // one that begins in it and goes on behind it.
     const int row = threadIdx.x >> 4, cc = threadIdx.x & 15;
     const int64_t me = blockIdx.x;
-    PartTag out0 = {kNone, 0, 0, 0}, out1 = {kNone, 0, 0, 0};
+    PartTag out0 = {kNone}, out1 = {kNone};
     for (int first = -1; first < kWaves; ++first) {  // -1: the chain that enters this workgroup
-        if (first >= 0 && sh.tag[first][1].state == kNone) continue;
-        if (first < 0 && sh.tag[0][0].state == kNone) continue;
-        Join<D> j;
         PartTag tag = first < 0 ? sh.tag[0][0] : sh.tag[first][1];
+        if (tag.state == kNone) continue;
+        Join<D> j;
         if (first >= 0) j.add(sh.part[first][1], row, cc);
         int state = kThrough;
         for (int w = first + 1; w < kWaves && state == kThrough; ++w) {
@@ -548,7 +607,7 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attenti
         if (first >= 0 && state == kEnds) {
             j.finish(a, tag, group, row, cc);
         } else {
-            j.put(parts[me * 2 + (first < 0 ? 0 : 1)], row, cc);
+            if (row < tag.rows) j.put(parts[me * 2 + (first < 0 ? 0 : 1)], row, cc);
             if (first < 0) out0 = tag; else out1 = tag;
         }
     }
@@ -559,20 +618,36 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attenti
 }
 
 // Rows cut between workgroups: the workgroup in which a row begins owns it; the pieces
-// follow in the slots 0 of the next ones.
+// follow in the slots 0 of the next ones, up to one in which the row ends.
 template <int D>
 __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attention a, const Part<D> *parts, const PartTag *tags) {
-    const int64_t w = blockIdx.x;
+    const int w = blockIdx.x, lane = threadIdx.x & 63;
     const PartTag tag = tags[2 * w + 1];
     if (tag.state != kThrough) return;
+    int n = 0;  // pieces behind the first
+    for (int k = w + 1; k < (int)gridDim.x; k += 64) {
+        const int state = k + lane < (int)gridDim.x ? tags[2 * (k + lane)].state : kNone;
+        const uint64_t stop = __ballot(state != kThrough);
+        if (!stop) {
+            n += 64;
+            continue;
+        }
+        const int at = __builtin_ctzll(stop);
+        n += at + (__shfl(state, at) == kEnds);
+        break;
+    }
     const int row = threadIdx.x >> 4, cc = threadIdx.x & 15;
+    if (row >= tag.rows) return;
     Join<D> j;
-    j.add(parts[2 * w + 1], row, cc);
-    for (int64_t k = w + 1; k < gridDim.x; ++k) {
-        const int state = tags[2 * k].state;
-        if (state == kNone) break;
-        j.add(parts[2 * k], row, cc);
-        if (state == kEnds) break;
+    j.m = parts[2 * w + 1].m[row];
+    for (int k = 1; k <= n; ++k) j.m = fmaxf(j.m, parts[2 * (w + k)].m[row]);
+#pragma unroll 4
+    for (int k = 0; k <= n; ++k) {
+        const Part<D> &p = parts[k ? 2 * (w + k) : 2 * w + 1];
+        const float its = weight_of(p.m[row], j.m);
+        j.l += p.l[row] * its;
+#pragma unroll
+        for (int i = 0; i < Join<D>::N; ++i) j.o[i] += p.o[row][cc * Join<D>::N + i] * its;
     }
     j.finish(a, tag, a.heads / a.b.f.n_kv, row, cc);
 }
@@ -600,7 +675,7 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
     __shared__ u32x4 values[2][2][MT][kWave];
     a.b.f.dim = D;
     const Kv4Format &f = a.b.f;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int group = a.heads / f.n_kv;
     const Lane<D> ln(lane);
 
@@ -617,7 +692,8 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
         s += (m ? 63 - __clzll((long long)m) : 0) * step;
         n = min(step, a.b.S - s);
     }
-    const int q0 = a.b.q_start[s], n = a.b.q_start[s + 1] - q0, len = a.b.kv_len[s];
+    const int q0 = uniform_load(a.b.q_start + s), n = uniform_load(a.b.q_start + s + 1) - q0;
+    const int len = uniform_load(a.b.kv_len + s);
     const int64_t rows = (int64_t)n * group;
     if (rows <= kDecodeRows) return;
     const int64_t r0 = (int64_t)(vt - (int)((int64_t)q0 * group / kPromptRows + s)) * kPromptRows;
@@ -658,17 +734,6 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
 
     const int32_t *row = a.b.table + (int64_t)s * a.b.ld_table;
     const int per = f.page / kBlock;
-    int have = -64, pages = -1;
-    auto head_of = [&](int b) -> const uint8_t * {
-        if (b >= have + 64 || have < 0) {
-            have = b;
-            const int64_t col = (int64_t)(b + lane) / per;
-            pages = col < a.b.cols && b + lane < b_end ? row[col] : -1;
-        }
-        const int page = __builtin_amdgcn_readlane(pages, b - have);
-        if (page < 0 || page >= a.b.num_pages) return nullptr;
-        return a.b.cache + (int64_t)page * f.page_bytes() + (int64_t)head * f.head_bytes() + 0;
-    };
     // this wave's share of a block's values: tokens 32 vs .. + 31, bytes vb .. of each word
     const int vstep = wave >> 1, vhalf = wave & 1;
     auto load_values = [&](RawValues<D> &x, const uint8_t *hd, int b) {
@@ -722,27 +787,26 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
 
     Bytes<D> x;  // keys of the block in hand
     RawValues<D> rv;
-    const uint8_t *now = b_first < b_end ? head_of(b_first) : nullptr;
-    if (now) {
-        load_keys(x.k, x.ks, now, b_first);
-        load_values(rv, now, b_first);
-        put_values(rv, b_first, values[b_first & 1]);
-    }
-    const uint8_t *next = b_first + 1 < b_end ? head_of(b_first + 1) : nullptr;
-    if (next) load_values(rv, next, b_first + 1);
+    int now = b_first < b_end ? page_of(a.b, row, b_first) : -1;
+    int next = b_first + 1 < b_end ? page_of(a.b, row, b_first + 1) : -1;
+    int after = page_of(a.b, row, b_first + 2);
+    load_keys(x.k, x.ks, head_block(a.b, now, head), b_first);
+    load_values(rv, head_block(a.b, now, head), b_first);
+    put_values(rv, b_first, values[b_first & 1]);
+    load_values(rv, head_block(a.b, next, head), b_first + 1);
     __syncthreads();
     for (int b = b_first; b < b_end; ++b) {
-        const uint8_t *after = b + 2 < b_end ? head_of(b + 2) : nullptr;
-        if (next) put_values(rv, b + 1, values[(b + 1) & 1]);
-        if (after) load_values(rv, after, b + 2);
+        const int then = page_of(a.b, row, b + 3);
+        put_values(rv, b + 1, values[(b + 1) & 1]);
+        load_values(rv, head_block(a.b, after, head), b + 2);
         const int64_t j0 = (int64_t)b * kBlock;
-        const bool work = now && !idle && j0 <= w_last && j0 + kBlock > w_all_from - (int64_t)(w_last - place0 - w0 / group);
+        const bool work = now >= 0 && !idle && j0 <= w_last && j0 + kBlock > w_all_from - (int64_t)(w_last - place0 - w0 / group);
         f32x4 sc[kPromptTiles][4];
         if (work) {
 #pragma unroll
             for (int k = 0; k < kPromptTiles; ++k) scores(x, q[k], sc[k]);
         }
-        if (next) load_keys(x.k, x.ks, next, b + 1);
+        load_keys(x.k, x.ks, head_block(a.b, next, head), b + 1);
         if (work) {
             if (j0 < w_all_from || j0 + kBlock - 1 > w_all) {
 #pragma unroll
@@ -779,6 +843,7 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
         }
         now = next;
         next = after;
+        after = then;
         __syncthreads();
     }
 #pragma unroll
@@ -823,7 +888,10 @@ hipError_t launch(Kv4Attention a, int64_t max_q, void *ws, hipStream_t st) {
     const int groups = device_cus() * kGroupsPerCu;
     Part<D> *parts = (Part<D> *)ws;
     PartTag *tags = (PartTag *)(parts + 2 * (size_t)groups);
-    kv4_decode_kernel<D><<<groups, kWaves * kWave, 0, st>>>(a, parts, tags);
+    if (max_q * group <= kRows)
+        kv4_decode_kernel<D, true><<<groups, kWaves * kWave, 0, st>>>(a, parts, tags);
+    else
+        kv4_decode_kernel<D, false><<<groups, kWaves * kWave, 0, st>>>(a, parts, tags);
     kv4_join_kernel<D><<<groups, 256, 0, st>>>(a, parts, tags);
     return hipGetLastError();
 }
