@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -115,17 +116,15 @@ def _load() -> ctypes.CDLL:
     L.nm_spmv_multi_plan.argtypes, L.nm_spmv_multi_plan.restype = [p, i32, i64, i32, p], i32
     f32 = ctypes.c_float
     L.nm_kv4_page_bytes.argtypes, L.nm_kv4_page_bytes.restype = [i32, i32, i32], i64
-    batch = [i64, i32, i32, i32, p, i64, i32, p, p, i64]  # num_pages .. S
-    L.nm_kv4_append.argtypes = [p, i64, i64, p, i64, i64, i64, p, *batch, p]
-    L.nm_kv4_unpack.argtypes = [p, *batch, i64, p, i64, i64, p, i64, i64, p]
+    d = ctypes.c_char_p  # a descriptor struct, packed by the caller
+    L.nm_kv4_append.argtypes = L.nm_kv4_unpack.argtypes = [d, d, d, p]
     L.nm_kv4_attention_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i64]
     L.nm_kv4_attention_workspace_bytes.restype = sz
-    L.nm_kv4_attention.argtypes = [p, i64, i64, i64, i32, p, *batch, i64, f32, i64, p, i64, i64, p, i64, p, sz, p]
+    L.nm_kv4_attention.argtypes = [d, d, i32, i64, f32, i64, d, p, i64, p, sz, p]
     L.nm_kv_pages_workspace_bytes.argtypes, L.nm_kv_pages_workspace_bytes.restype = [i64, i64, i64], sz
-    book = [p, i64, i32, p, i64, p, i64, i32]  # page_table .. page_size
-    L.nm_kv_resize.argtypes = [p, *book, p, p, p, sz, p]
-    L.nm_kv_fork.argtypes = [p, p, i64, *book, p, p, p, sz, p]
-    L.nm_kv_compact.argtypes = [*book, p, i64, p, p, sz, p]
+    L.nm_kv_resize.argtypes = [d, p, p, p, p, sz, p]
+    L.nm_kv_fork.argtypes = [d, p, p, i64, p, p, p, sz, p]
+    L.nm_kv_compact.argtypes = [d, p, i64, p, p, sz, p]
     L.nm_kv_copy_pages.argtypes = [p, i64, i64, i64, i64, p, i64, p]
     for f in (L.nm_kv4_append, L.nm_kv4_unpack, L.nm_kv4_attention, L.nm_kv_resize, L.nm_kv_fork, L.nm_kv_compact,
               L.nm_kv_copy_pages):
@@ -623,87 +622,121 @@ def nm_spmv_multi_plan(rows, K: int, B: int) -> dict:
 
 
 # ---- the 4-bit key/value cache (format, places and rules: include/nm_spmv.h) ----
+#
+# These run once a token and layer, some for a few microseconds: descriptors are packed in one
+# go (native alignment, the C structs' field order), devices compared by number.
+
+_KV4_BATCH = struct.Struct("@PqPqPPqq4i")  # nm_kv4_batch
+_KV4_ROWS = struct.Struct("@Pqq")          # nm_kv4_rows
+_KV_BOOK = struct.Struct("@PqPqPq2i")      # nm_kv_book
+
 
 def nm_kv4_page_bytes(page_size: int, n_kv: int, head_dim: int) -> int:
     """Bytes of one page of page_size tokens (64, 128, 256 or 512) of n_kv heads of 64 or 128 channels."""
     return int(lib.nm_kv4_page_bytes(int(page_size), int(n_kv), int(head_dim)))
 
 
-def _call(ref: torch.Tensor, fn, *args):
-    """One entry point on ref's device, on the stream that is current there."""
-    dev = ref.device
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, stream))
+# The current stream's handle without the Python object around it (2 us of it), where torch has that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _call(dev: int, fn, *args):
+    """One entry point on device `dev`, on the stream that is current there."""
+    stream = _raw_stream(dev)
+    if dev == torch.cuda.current_device():
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, stream))
+            status = fn(*args, stream)
+    if status:
+        _check(status)
 
 
-def _i32(t: torch.Tensor, name: str, ref: torch.Tensor, shape) -> int:
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != ref.device:
-        raise TypeError(f"{name} must be an int32 tensor on {ref.device}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
+def _where(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise ValueError(f"{name} must be a tensor on a HIP device")
+    return t.get_device()
+
+
+def _i32(t: torch.Tensor, name: str, dev: int, *shape) -> int:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.get_device() != dev:
+        raise TypeError(f"{name} must be an int32 tensor on cuda:{dev}")
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, of shape {list(shape)} (got {list(t.shape)})")
     return t.data_ptr()
 
 
-def _table(page_table: torch.Tensor, ref: torch.Tensor):
-    if not isinstance(page_table, torch.Tensor) or page_table.dtype != torch.int32 or page_table.device != ref.device:
-        raise TypeError(f"page_table must be an int32 tensor on {ref.device}")
-    if page_table.dim() != 2 or page_table.stride(1) != 1:
+def _table(t: torch.Tensor, dev: int):
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.get_device() != dev:
+        raise TypeError(f"page_table must be an int32 tensor on cuda:{dev}")
+    if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError("page_table must be [S, columns], contiguous in its last dimension")
-    S, cols = page_table.shape
-    return page_table.data_ptr(), page_table.stride(0) if S > 1 else cols, cols, S
+    S, cols = t.shape
+    return t.data_ptr(), t.stride(0) if S > 1 else cols, cols, S
 
 
-def _kv_rows(t: torch.Tensor, name: str, ref: torch.Tensor | None = None):
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or (ref is not None and t.device != ref.device):
-        raise ValueError(f"{name} must be a tensor on {'a HIP device' if ref is None else ref.device}")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16} (got {t.dtype})")
-    if t.dim() != 3 or t.stride(2) != 1:
-        raise ValueError(f"{name} must be [T, heads, head_dim], contiguous in its last dimension")
-    T, H, D = t.shape
-    return t.data_ptr(), t.stride(0) if T > 1 else H * D, t.stride(1) if H > 1 else D
+def _kv_rows(t: torch.Tensor, name: str, dev: int, shape) -> bytes:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be a {torch.bfloat16} tensor")
+    if t.get_device() != dev or t.shape != shape:
+        raise ValueError(f"{name} must be on cuda:{dev}, of shape {list(shape)} (got {t.device}, {list(t.shape)})")
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [T, heads, head_dim]")
+    ld, hd, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    T, H, D = shape
+    return _KV4_ROWS.pack(t.data_ptr(), ld if T > 1 else H * D, hd if H > 1 else D)
 
 
-def _kv_batch(ref: torch.Tensor, cache: torch.Tensor, page_table, kv_len, q_start, page_size: int, n_kv: int, D: int):
-    """(cache pointer, num_pages .. S) of a ragged batch, checked."""
-    if not isinstance(cache, torch.Tensor) or cache.dtype != torch.uint8 or cache.device != ref.device:
-        raise TypeError(f"cache must be a uint8 tensor on {ref.device}")
+def _kv_batch(dev: int, cache: torch.Tensor, page_table, kv_len, q_start, page_size: int, n_kv: int, T: int, D: int):
+    """(nm_kv4_batch, S), checked."""
+    if not isinstance(cache, torch.Tensor) or cache.dtype is not torch.uint8 or cache.get_device() != dev:
+        raise TypeError(f"cache must be a uint8 tensor on cuda:{dev}")
     if cache.dim() != 2 or not cache.is_contiguous():
         raise ValueError("cache must be contiguous, [num_pages, page_bytes]")
+    N, nbytes = cache.shape
     want = lib.nm_kv4_page_bytes(page_size, n_kv, D)
-    if want and cache.shape[1] != want:
-        raise ValueError(f"cache pages must be of {want} bytes (got {cache.shape[1]})")
-    tp, ld, cols, S = _table(page_table, ref)
-    return (cache.data_ptr(), cache.shape[0], page_size, n_kv, D, tp, ld, cols, _i32(kv_len, "kv_len", ref, (S,)),
-            _i32(q_start, "q_start", ref, (S + 1,)), S)
+    if want and nbytes != want:
+        raise ValueError(f"cache pages must be of {want} bytes (got {nbytes})")
+    tp, ld, cols, S = _table(page_table, dev)
+    return _KV4_BATCH.pack(cache.data_ptr(), N, tp, ld, _i32(kv_len, "kv_len", dev, S),
+                           _i32(q_start, "q_start", dev, S + 1), S, T, cols, page_size, n_kv, D), S
+
+
+def _kv_workspace(nbytes: int, t: torch.Tensor, workspace: torch.Tensor | None):
+    """(tensor to hold on to, pointer, bytes)."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+        return workspace, workspace.data_ptr(), nbytes
+    if workspace.get_device() != t.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the same device")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def nm_kv4_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
                   kv_len: torch.Tensor, q_start: torch.Tensor, page_size: int) -> None:
     """Rows k, v bf16 [T, n_kv, D] -> cache uint8 [num_pages, page_bytes], at the last places of the
     sequences: page_table int32 [S, columns], kv_len int32 [S] (new rows included), q_start int32 [S + 1]."""
-    kr = _kv_rows(k, "k")
-    vr = _kv_rows(v, "v", k)
-    if k.shape != v.shape:
-        raise ValueError("k and v must have the same shape")
-    T, H, D = k.shape
-    _call(k, lib.nm_kv4_append, *kr, *vr, T, *_kv_batch(k, cache, page_table, kv_len, q_start, page_size, H, D))
+    dev, shape = _where(k, "k"), k.shape
+    kr, vr = _kv_rows(k, "k", dev, shape), _kv_rows(v, "v", dev, shape)
+    T, H, D = shape
+    b, _ = _kv_batch(dev, cache, page_table, kv_len, q_start, page_size, H, T, D)
+    _call(dev, lib.nm_kv4_append, b, kr, vr)
 
 
 def nm_kv4_unpack(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, q_start: torch.Tensor,
                   page_size: int, k_out: torch.Tensor, v_out: torch.Tensor):
     """The rows that nm_kv4_append with the same arguments stores, as the cache holds them -> k_out, v_out bf16
     [T, n_kv, D]."""
-    kr = _kv_rows(k_out, "k_out")
-    vr = _kv_rows(v_out, "v_out", k_out)
-    if k_out.shape != v_out.shape:
-        raise ValueError("k_out and v_out must have the same shape")
-    T, H, D = k_out.shape
-    _call(k_out, lib.nm_kv4_unpack, *_kv_batch(k_out, cache, page_table, kv_len, q_start, page_size, H, D), T, *kr, *vr)
+    dev, shape = _where(k_out, "k_out"), k_out.shape
+    kr, vr = _kv_rows(k_out, "k_out", dev, shape), _kv_rows(v_out, "v_out", dev, shape)
+    T, H, D = shape
+    b, _ = _kv_batch(dev, cache, page_table, kv_len, q_start, page_size, H, T, D)
+    _call(dev, lib.nm_kv4_unpack, b, kr, vr)
     return k_out, v_out
 
 
@@ -718,21 +751,19 @@ def nm_kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Ten
     """Causal attention of rows q bf16 [T, heads, D] over the cached keys and values of their sequences ->
     (out bf16 [T, heads, D], lse fp32 [T, heads]).  scale: 1 / sqrt(D) unless given.  window: keys a row looks
     back over, itself among them (0: all).  max_q_len: a hint, the most rows of one sequence."""
-    qr = _kv_rows(q, "q")
-    T, Hq, D = q.shape
+    dev, shape = _where(q, "q"), q.shape
+    qr = _kv_rows(q, "q", dev, shape)
+    T, Hq, D = shape
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    o = _kv_rows(out, "out", q)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
     if lse is None:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    if lse.dtype != torch.float32 or lse.device != q.device or lse.shape != (T, Hq) or lse.stride(1) != 1:
+    elif lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != (T, Hq) or lse.stride(1) != 1:
         raise ValueError("lse must be fp32 [T, heads], contiguous in its last dimension, on q's device")
-    b = _kv_batch(q, cache, page_table, kv_len, q_start, page_size, n_kv, D)
-    ws, ws_bytes = _workspace(lib.nm_kv4_attention_workspace_bytes(T, b[-1], Hq, n_kv, D, max_q_len), q, workspace)
-    _call(q, lib.nm_kv4_attention, *qr, T, Hq, *b, max_q_len, D ** -0.5 if scale is None else scale, window, *o,
-          lse.data_ptr(), lse.stride(0) if T > 1 else Hq, None if ws is None else ws.data_ptr(), ws_bytes)
+    b, S = _kv_batch(dev, cache, page_table, kv_len, q_start, page_size, n_kv, T, D)
+    ws, wp, wn = _kv_workspace(lib.nm_kv4_attention_workspace_bytes(T, S, Hq, n_kv, D, max_q_len), q, workspace)
+    _call(dev, lib.nm_kv4_attention, b, qr, Hq, max_q_len, D ** -0.5 if scale is None else scale, window,
+          _kv_rows(out, "out", dev, shape), lse.data_ptr(), lse.stride(0) if T > 1 else Hq, wp, wn)
     return out, lse
 
 
@@ -740,14 +771,12 @@ def nm_kv_pages_workspace_bytes(S: int, n_pairs: int, num_pages: int) -> int:
     return int(lib.nm_kv_pages_workspace_bytes(S, n_pairs, num_pages))
 
 
-def _kv_book(page_table, kv_len, refcount, page_size, n_pairs, workspace):
-    if not isinstance(page_table, torch.Tensor) or page_table.device.type != "cuda":
-        raise ValueError("page_table must be a tensor on a HIP device")
-    tp, ld, cols, S = _table(page_table, page_table)
+def _kv_book(dev: int, page_table, kv_len, refcount, page_size, n_pairs, workspace):
+    """(nm_kv_book, S, workspace, its pointer and bytes), checked."""
+    tp, ld, cols, S = _table(page_table, dev)
     N = refcount.numel()
-    ws, ws_bytes = _workspace(lib.nm_kv_pages_workspace_bytes(S, n_pairs, N), page_table, workspace)
-    return (tp, ld, cols, _i32(kv_len, "kv_len", page_table, (S,)), S, _i32(refcount, "refcount", page_table, (N,)), N,
-            page_size), ws, ws_bytes
+    b = _KV_BOOK.pack(tp, ld, _i32(kv_len, "kv_len", dev, S), S, _i32(refcount, "refcount", dev, N), N, cols, page_size)
+    return b, S, *_kv_workspace(lib.nm_kv_pages_workspace_bytes(S, n_pairs, N), page_table, workspace)
 
 
 def nm_kv_resize(new_len: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, refcount: torch.Tensor,
@@ -755,11 +784,10 @@ def nm_kv_resize(new_len: torch.Tensor, page_table: torch.Tensor, kv_len: torch.
                  workspace: torch.Tensor | None = None) -> None:
     """Sequences to new_len int32 [S] tokens: pages given back or handed out, in page_table int32 [S, columns],
     kv_len int32 [S] and refcount int32 [num_pages].  moves int32 [S, 2] for nm_kv_copy_pages; missing int32 [1]."""
-    b, ws, ws_bytes = _kv_book(page_table, kv_len, refcount, page_size, 0, workspace)
-    S = b[4]
-    _call(page_table, lib.nm_kv_resize, _i32(new_len, "new_len", page_table, (S,)), *b,
-          _i32(moves, "moves", page_table, (S, 2)), _i32(missing, "missing", page_table, (1,)),
-          None if ws is None else ws.data_ptr(), ws_bytes)
+    dev = _where(page_table, "page_table")
+    b, S, ws, wp, wn = _kv_book(dev, page_table, kv_len, refcount, page_size, 0, workspace)
+    _call(dev, lib.nm_kv_resize, b, _i32(new_len, "new_len", dev, S), _i32(moves, "moves", dev, S, 2),
+          _i32(missing, "missing", dev, 1), wp, wn)
 
 
 def nm_kv_fork(parent: torch.Tensor, child: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
@@ -767,32 +795,29 @@ def nm_kv_fork(parent: torch.Tensor, child: torch.Tensor, page_table: torch.Tens
                workspace: torch.Tensor | None = None) -> None:
     """Slots child int32 [n] become copies of slots parent int32 [n]; full pages are shared.  moves int32 [n, 2]
     for nm_kv_copy_pages; missing int32 [1]."""
-    n = parent.numel()
-    if n == 0:
-        return
-    b, ws, ws_bytes = _kv_book(page_table, kv_len, refcount, page_size, n, workspace)
-    _call(page_table, lib.nm_kv_fork, _i32(parent, "parent", page_table, (n,)), _i32(child, "child", page_table, (n,)),
-          n, *b, _i32(moves, "moves", page_table, (n, 2)), _i32(missing, "missing", page_table, (1,)),
-          None if ws is None else ws.data_ptr(), ws_bytes)
+    dev, n = _where(page_table, "page_table"), parent.numel()
+    b, S, ws, wp, wn = _kv_book(dev, page_table, kv_len, refcount, page_size, n, workspace)
+    _call(dev, lib.nm_kv_fork, b, _i32(parent, "parent", dev, n), _i32(child, "child", dev, n), n,
+          _i32(moves, "moves", dev, n, 2), _i32(missing, "missing", dev, 1), wp, wn)
 
 
 def nm_kv_compact(page_table: torch.Tensor, kv_len: torch.Tensor, refcount: torch.Tensor, page_size: int,
                   moves: torch.Tensor, used: torch.Tensor, workspace: torch.Tensor | None = None) -> None:
     """Used pages into the lowest numbers.  moves int32 [max_moves, 2] for nm_kv_copy_pages; used int32 [1]."""
-    b, ws, ws_bytes = _kv_book(page_table, kv_len, refcount, page_size, 0, workspace)
-    n = moves.shape[0]
-    _call(page_table, lib.nm_kv_compact, *b, _i32(moves, "moves", page_table, (n, 2)), n,
-          _i32(used, "used", page_table, (1,)), None if ws is None else ws.data_ptr(), ws_bytes)
+    dev, n = _where(page_table, "page_table"), moves.shape[0]
+    b, S, ws, wp, wn = _kv_book(dev, page_table, kv_len, refcount, page_size, 0, workspace)
+    _call(dev, lib.nm_kv_compact, b, _i32(moves, "moves", dev, n, 2), n, _i32(used, "used", dev, 1), wp, wn)
 
 
 def nm_kv_copy_pages(cache: torch.Tensor, moves: torch.Tensor) -> None:
     """Copies page moves[i, 0] to page moves[i, 1] (int32 [n, 2]) of cache uint8 [num_pages, page_bytes], or in
     each layer of [layers, num_pages, page_bytes]."""
-    if not isinstance(cache, torch.Tensor) or cache.dtype != torch.uint8 or cache.device.type != "cuda":
-        raise TypeError("cache must be a uint8 tensor on a HIP device")
-    if cache.dim() not in (2, 3) or not cache[0].is_contiguous() or not (cache.dim() == 3 or cache.is_contiguous()):
-        raise ValueError("cache must be [num_pages, page_bytes] or [layers, num_pages, page_bytes], layers contiguous")
+    dev = _where(cache, "cache")
+    if cache.dtype is not torch.uint8 or cache.dim() not in (2, 3):
+        raise TypeError("cache must be uint8 [num_pages, page_bytes] or [layers, num_pages, page_bytes]")
     N, nbytes = cache.shape[-2:]
-    layers = cache.shape[0] if cache.dim() == 3 else 1
-    _call(cache, lib.nm_kv_copy_pages, cache.data_ptr(), N, nbytes, layers, cache.stride(0) if layers > 1 else N * nbytes,
-          _i32(moves, "moves", cache, (moves.shape[0], 2)), moves.shape[0])
+    layers, stride = (cache.shape[0], cache.stride(0)) if cache.dim() == 3 else (1, N * nbytes)
+    if cache.stride()[-2:] != (nbytes, 1):
+        raise ValueError("the pages of a layer must be contiguous")
+    n = moves.shape[0]
+    _call(dev, lib.nm_kv_copy_pages, cache.data_ptr(), N, nbytes, layers, stride, _i32(moves, "moves", dev, n, 2), n)

@@ -793,49 +793,48 @@ nm_status nm_stream_read(const void *buf, size_t bytes, uint32_t *sink, size_t s
 static bool kv_page_size_ok(int p) { return p == 64 || p == 128 || p == 256 || p == 512; }
 
 // Checks of a ragged batch over a cache, shared by append, unpack and attention.
-static nm_status kv4_batch(const char *who, int64_t T, uint8_t *cache, int64_t num_pages, int page_size, int n_kv,
-                           int head_dim, const int32_t *page_table, int64_t ld_table, int table_cols,
-                           const int32_t *kv_len, const int32_t *q_start, int64_t S, nmk::Kv4Batch &b) {
-    if (!cache || !page_table || !kv_len || !q_start) return fail(NM_ERR_NULL, "%s: NULL pointer", who);
-    if (head_dim != 64 && head_dim != 128)
-        return fail(NM_ERR_SHAPE, "%s: head_dim=%d is not 64 or 128", who, head_dim);
-    if (!kv_page_size_ok(page_size))
-        return fail(NM_ERR_SHAPE, "%s: page_size=%d is not 64, 128, 256 or 512", who, page_size);
-    if (n_kv < 1 || n_kv > 256) return fail(NM_ERR_SHAPE, "%s: n_kv=%d out of range [1, 256]", who, n_kv);
-    if (T < 0 || T > (1 << 24) || S < 0 || S > (1 << 20) || (T > 0 && S < 1))
-        return fail(NM_ERR_SHAPE, "%s: bad sizes T=%lld S=%lld", who, (long long)T, (long long)S);
-    if (num_pages < 1 || num_pages > 0x7FFFFFFF)
-        return fail(NM_ERR_SHAPE, "%s: num_pages=%lld out of range", who, (long long)num_pages);
-    if (table_cols < 1 || table_cols > (1 << 24) || ld_table < table_cols)
-        return fail(NM_ERR_SHAPE, "%s: page table of %d columns, row stride %lld", who, table_cols, (long long)ld_table);
-    if (!aligned(cache, 16) || !aligned(page_table, 4) || !aligned(kv_len, 4) || !aligned(q_start, 4))
+static nm_status kv4_batch(const char *who, const nm_kv4_batch *p, nmk::Kv4Batch &b) {
+    if (!p || !p->cache || !p->page_table || !p->kv_len || !p->q_start) return fail(NM_ERR_NULL, "%s: NULL pointer", who);
+    if (p->head_dim != 64 && p->head_dim != 128)
+        return fail(NM_ERR_SHAPE, "%s: head_dim=%d is not 64 or 128", who, p->head_dim);
+    if (!kv_page_size_ok(p->page_size))
+        return fail(NM_ERR_SHAPE, "%s: page_size=%d is not 64, 128, 256 or 512", who, p->page_size);
+    if (p->n_kv < 1 || p->n_kv > 256) return fail(NM_ERR_SHAPE, "%s: n_kv=%d out of range [1, 256]", who, p->n_kv);
+    if (p->T < 0 || p->T > (1 << 24) || p->S < 0 || p->S > (1 << 20) || (p->T > 0 && p->S < 1))
+        return fail(NM_ERR_SHAPE, "%s: bad sizes T=%lld S=%lld", who, (long long)p->T, (long long)p->S);
+    if (p->num_pages < 1 || p->num_pages > 0x7FFFFFFF)
+        return fail(NM_ERR_SHAPE, "%s: num_pages=%lld out of range", who, (long long)p->num_pages);
+    if (p->table_cols < 1 || p->table_cols > (1 << 24) || p->ld_table < p->table_cols)
+        return fail(NM_ERR_SHAPE, "%s: page table of %d columns, row stride %lld", who, p->table_cols,
+                    (long long)p->ld_table);
+    if (!aligned(p->cache, 16) || !aligned(p->page_table, 4) || !aligned(p->kv_len, 4) || !aligned(p->q_start, 4))
         return fail(NM_ERR_ALIGN, "%s: cache needs 16-byte, page_table, kv_len and q_start 4-byte alignment", who);
-    b.f.page = page_size;
-    b.f.n_kv = n_kv;
-    b.f.dim = head_dim;
-    b.cache = cache;
-    b.num_pages = num_pages;
-    b.table = page_table;
-    b.ld_table = ld_table;
-    b.cols = table_cols;
-    b.kv_len = kv_len;
-    b.q_start = q_start;
-    b.S = (int)S;
-    b.T = (int)T;
+    b.f.page = p->page_size;
+    b.f.n_kv = p->n_kv;
+    b.f.dim = p->head_dim;
+    b.cache = p->cache;
+    b.num_pages = p->num_pages;
+    b.table = p->page_table;
+    b.ld_table = p->ld_table;
+    b.cols = p->table_cols;
+    b.kv_len = p->kv_len;
+    b.q_start = p->q_start;
+    b.S = (int)p->S;
+    b.T = (int)p->T;
     return NM_OK;
 }
 
-static nm_status kv4_rows(const char *who, const char *name, const nm_bf16 *p, int64_t ld, int64_t hd, int heads,
-                          int dim, nmk::Kv4Rows &r) {
-    if (!p) return fail(NM_ERR_NULL, "%s: %s is NULL", who, name);
-    if (ld < dim || (heads > 1 && hd < dim) || ld > kMaxDim || hd > kMaxDim || hd < 0)
+static nm_status kv4_rows(const char *who, const char *name, const nm_kv4_rows *p, int heads, int dim,
+                          nmk::Kv4Rows &r) {
+    if (!p || !p->p) return fail(NM_ERR_NULL, "%s: %s is NULL", who, name);
+    if (p->ld < dim || (heads > 1 && p->hd < dim) || p->ld > kMaxDim || p->hd > kMaxDim || p->hd < 0)
         return fail(NM_ERR_SHAPE, "%s: %s strides %lld (token) and %lld (head) for heads of %d", who, name,
-                    (long long)ld, (long long)hd, dim);
-    if (ld % 8 || hd % 8 || !aligned(p, 16))
+                    (long long)p->ld, (long long)p->hd, dim);
+    if (p->ld % 8 || p->hd % 8 || !aligned(p->p, 16))
         return fail(NM_ERR_ALIGN, "%s: %s needs 16-byte alignment, its strides multiples of 8", who, name);
-    r.p = const_cast<nm_bf16 *>(p);
-    r.ld = ld;
-    r.hd = hd;
+    r.p = p->p;
+    r.ld = p->ld;
+    r.hd = p->hd;
     return NM_OK;
 }
 
@@ -848,45 +847,33 @@ int64_t nm_kv4_page_bytes(int page_size, int n_kv, int head_dim) {
     return f.page_bytes();
 }
 
-nm_status nm_kv4_append(const nm_bf16 *k, int64_t ldk, int64_t hdk, const nm_bf16 *v, int64_t ldv, int64_t hdv,
-                        int64_t T, uint8_t *cache, int64_t num_pages, int page_size, int n_kv, int head_dim,
-                        const int32_t *page_table, int64_t ld_table, int table_cols, const int32_t *kv_len,
-                        const int32_t *q_start, int64_t S, void *hip_stream) {
+static nm_status kv4_move_rows(const char *who, const nm_kv4_batch *batch, const nm_kv4_rows *k, const nm_kv4_rows *v,
+                               bool write, void *hip_stream) {
+    nmk::Kv4Batch b;
+    nmk::Kv4Rows kr, vr;
+    nm_status st = kv4_batch(who, batch, b);
+    if (st != NM_OK || b.T == 0) return st;  // no rows: their pointers may be NULL
+    st = kv4_rows(who, "k", k, b.f.n_kv, b.f.dim, kr);
+    if (st == NM_OK) st = kv4_rows(who, "v", v, b.f.n_kv, b.f.dim, vr);
+    if (st != NM_OK) return st;
+    hipError_t e = write ? nmk::launch_kv4_append(b, kr, vr, (hipStream_t)hip_stream)
+                         : nmk::launch_kv4_unpack(b, kr, vr, (hipStream_t)hip_stream);
+    return e == hipSuccess ? NM_OK : hip_fail(who, e);
+}
+
+nm_status nm_kv4_append(const nm_kv4_batch *batch, const nm_kv4_rows *k, const nm_kv4_rows *v, void *hip_stream) {
     try {
         g_err[0] = 0;
-        const char *who = "nm_kv4_append";
-        nmk::Kv4Batch b;
-        nmk::Kv4Rows kr, vr;
-        nm_status st = kv4_batch(who, T, cache, num_pages, page_size, n_kv, head_dim, page_table, ld_table, table_cols,
-                                 kv_len, q_start, S, b);
-        if (st != NM_OK || T == 0) return st;  // no rows: their pointers may be NULL
-        st = kv4_rows(who, "k", k, ldk, hdk, n_kv, head_dim, kr);
-        if (st == NM_OK) st = kv4_rows(who, "v", v, ldv, hdv, n_kv, head_dim, vr);
-        if (st != NM_OK) return st;
-        hipError_t e = nmk::launch_kv4_append(b, kr, vr, (hipStream_t)hip_stream);
-        return e == hipSuccess ? NM_OK : hip_fail(who, e);
+        return kv4_move_rows("nm_kv4_append", batch, k, v, true, hip_stream);
     } catch (...) {
         return fail(NM_ERR_HIP, "nm_kv4_append: internal error");
     }
 }
 
-nm_status nm_kv4_unpack(const uint8_t *cache, int64_t num_pages, int page_size, int n_kv, int head_dim,
-                        const int32_t *page_table, int64_t ld_table, int table_cols, const int32_t *kv_len,
-                        const int32_t *q_start, int64_t S, int64_t T, nm_bf16 *k, int64_t ldk, int64_t hdk,
-                        nm_bf16 *v, int64_t ldv, int64_t hdv, void *hip_stream) {
+nm_status nm_kv4_unpack(const nm_kv4_batch *batch, const nm_kv4_rows *k, const nm_kv4_rows *v, void *hip_stream) {
     try {
         g_err[0] = 0;
-        const char *who = "nm_kv4_unpack";
-        nmk::Kv4Batch b;
-        nmk::Kv4Rows kr, vr;
-        nm_status st = kv4_batch(who, T, const_cast<uint8_t *>(cache), num_pages, page_size, n_kv, head_dim, page_table,
-                                 ld_table, table_cols, kv_len, q_start, S, b);
-        if (st != NM_OK || T == 0) return st;  // no rows: their pointers may be NULL
-        st = kv4_rows(who, "k", k, ldk, hdk, n_kv, head_dim, kr);
-        if (st == NM_OK) st = kv4_rows(who, "v", v, ldv, hdv, n_kv, head_dim, vr);
-        if (st != NM_OK) return st;
-        hipError_t e = nmk::launch_kv4_unpack(b, kr, vr, (hipStream_t)hip_stream);
-        return e == hipSuccess ? NM_OK : hip_fail(who, e);
+        return kv4_move_rows("nm_kv4_unpack", batch, k, v, false, hip_stream);
     } catch (...) {
         return fail(NM_ERR_HIP, "nm_kv4_unpack: internal error");
     }
@@ -899,26 +886,25 @@ size_t nm_kv4_attention_workspace_bytes(int64_t T, int64_t S, int n_heads, int n
     return nmk::kv4_attention_workspace(T, S, n_heads, n_kv, head_dim, max_q_len);
 }
 
-nm_status nm_kv4_attention(const nm_bf16 *q, int64_t ldq, int64_t hdq, int64_t T, int n_heads, const uint8_t *cache,
-                           int64_t num_pages, int page_size, int n_kv, int head_dim, const int32_t *page_table,
-                           int64_t ld_table, int table_cols, const int32_t *kv_len, const int32_t *q_start, int64_t S,
-                           int64_t max_q_len, float scale, int64_t window, nm_bf16 *out, int64_t ldo, int64_t hdo,
-                           float *lse, int64_t ld_lse, void *workspace, size_t workspace_bytes, void *hip_stream) {
+nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int n_heads, int64_t max_q_len, float scale,
+                           int64_t window, const nm_kv4_rows *out, float *lse, int64_t ld_lse, void *workspace,
+                           size_t workspace_bytes, void *hip_stream) {
     try {
         g_err[0] = 0;
         const char *who = "nm_kv4_attention";
         nmk::Kv4Attention a;
-        nm_status st = kv4_batch(who, T, const_cast<uint8_t *>(cache), num_pages, page_size, n_kv, head_dim, page_table,
-                                 ld_table, table_cols, kv_len, q_start, S, a.b);
+        nm_status st = kv4_batch(who, batch, a.b);
         if (st != NM_OK) return st;
+        const int n_kv = a.b.f.n_kv, head_dim = a.b.f.dim;
+        const int64_t T = a.b.T, S = a.b.S;
         if (n_heads < 1 || n_heads > 1024 || n_heads % n_kv)
             return fail(NM_ERR_SHAPE, "%s: %d query heads are not a multiple of %d key/value heads", who, n_heads, n_kv);
         if (window < 0 || max_q_len < 1)
             return fail(NM_ERR_SHAPE, "%s: window=%lld max_q_len=%lld", who, (long long)window, (long long)max_q_len);
         if (!(scale - scale == 0.f)) return fail(NM_ERR_SHAPE, "%s: scale is not finite", who);
         if (T == 0) return NM_OK;  // no rows: their pointers may be NULL
-        st = kv4_rows(who, "q", q, ldq, hdq, n_heads, head_dim, a.q);
-        if (st == NM_OK) st = kv4_rows(who, "out", out, ldo, hdo, n_heads, head_dim, a.out);
+        st = kv4_rows(who, "q", q, n_heads, head_dim, a.q);
+        if (st == NM_OK) st = kv4_rows(who, "out", out, n_heads, head_dim, a.out);
         if (st != NM_OK) return st;
         if (lse && ld_lse < n_heads) return fail(NM_ERR_SHAPE, "%s: ld_lse=%lld", who, (long long)ld_lse);
         if (!aligned(lse, 4)) return fail(NM_ERR_ALIGN, "%s: lse needs 4-byte alignment", who);
@@ -938,36 +924,33 @@ nm_status nm_kv4_attention(const nm_bf16 *q, int64_t ldq, int64_t hdq, int64_t T
     }
 }
 
-static nm_status kv_book(const char *who, int32_t *page_table, int64_t ld_table, int table_cols, int32_t *kv_len,
-                         int64_t S, int32_t *refcount, int64_t num_pages, int page_size, const void *list, int64_t n,
-                         const int32_t *moves, const int32_t *count, const void *workspace, size_t workspace_bytes,
-                         nmk::KvBook &b) {
-    if (!page_table || !kv_len || !refcount || !list || !moves || !count)
+static nm_status kv_book(const char *who, const nm_kv_book *p, const void *list, int64_t n, const int32_t *moves,
+                         const int32_t *count, const void *workspace, size_t workspace_bytes, nmk::KvBook &b) {
+    if (!p || !p->page_table || !p->kv_len || !p->refcount || !list || !moves || !count)
         return fail(NM_ERR_NULL, "%s: NULL pointer", who);
-    if (!kv_page_size_ok(page_size))
-        return fail(NM_ERR_SHAPE, "%s: page_size=%d is not 64, 128, 256 or 512", who, page_size);
-    if (S < 1 || S > (1 << 20) || n < 0 || n > (1 << 30))
-        return fail(NM_ERR_SHAPE, "%s: bad sizes S=%lld n=%lld", who, (long long)S, (long long)n);
-    if (num_pages < 1 || num_pages > kMaxDim)
-        return fail(NM_ERR_SHAPE, "%s: num_pages=%lld out of range [1, 2^30]", who, (long long)num_pages);
-    if (table_cols < 1 || ld_table < table_cols || S * (int64_t)table_cols > kMaxDim)
-        return fail(NM_ERR_SHAPE, "%s: page table of %lld x %d, row stride %lld", who, (long long)S, table_cols,
-                    (long long)ld_table);
-    if (!aligned(page_table, 4) || !aligned(kv_len, 4) || !aligned(refcount, 4) || !aligned(list, 4) ||
+    if (!kv_page_size_ok(p->page_size))
+        return fail(NM_ERR_SHAPE, "%s: page_size=%d is not 64, 128, 256 or 512", who, p->page_size);
+    if (p->S < 1 || p->S > (1 << 20)) return fail(NM_ERR_SHAPE, "%s: S=%lld out of range", who, (long long)p->S);
+    if (p->num_pages < 1 || p->num_pages > kMaxDim)
+        return fail(NM_ERR_SHAPE, "%s: num_pages=%lld out of range [1, 2^30]", who, (long long)p->num_pages);
+    if (p->table_cols < 1 || p->ld_table < p->table_cols || p->S * (int64_t)p->table_cols > kMaxDim)
+        return fail(NM_ERR_SHAPE, "%s: page table of %lld x %d, row stride %lld", who, (long long)p->S, p->table_cols,
+                    (long long)p->ld_table);
+    if (!aligned(p->page_table, 4) || !aligned(p->kv_len, 4) || !aligned(p->refcount, 4) || !aligned(list, 4) ||
         !aligned(moves, 4) || !aligned(count, 4))
         return fail(NM_ERR_ALIGN, "%s: 4-byte alignment needed", who);
-    const size_t need = nmk::kv_pages_workspace(n > S ? n : S, num_pages);
+    const size_t need = nmk::kv_pages_workspace(n > p->S ? n : p->S, p->num_pages);
     if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
         return fail(NM_ERR_WORKSPACE, "%s: 16-byte aligned workspace of %zu bytes required, %zu given", who, need,
                     workspace ? workspace_bytes : (size_t)0);
-    b.table = page_table;
-    b.ld = ld_table;
-    b.cols = table_cols;
-    b.kv_len = kv_len;
-    b.S = (int)S;
-    b.refs = refcount;
-    b.N = (int)num_pages;
-    b.page = page_size;
+    b.table = p->page_table;
+    b.ld = p->ld_table;
+    b.cols = p->table_cols;
+    b.kv_len = p->kv_len;
+    b.S = (int)p->S;
+    b.refs = p->refcount;
+    b.N = (int)p->num_pages;
+    b.page = p->page_size;
     return NM_OK;
 }
 
@@ -976,9 +959,8 @@ size_t nm_kv_pages_workspace_bytes(int64_t S, int64_t n_pairs, int64_t num_pages
     return nmk::kv_pages_workspace(n_pairs > S ? n_pairs : S, num_pages);
 }
 
-nm_status nm_kv_fork(const int32_t *parent, const int32_t *child, int64_t n, int32_t *page_table, int64_t ld_table,
-                     int table_cols, int32_t *kv_len, int64_t S, int32_t *refcount, int64_t num_pages, int page_size,
-                     int32_t *moves, int32_t *missing, void *workspace, size_t workspace_bytes, void *hip_stream) {
+nm_status nm_kv_fork(const nm_kv_book *book, const int32_t *parent, const int32_t *child, int64_t n, int32_t *moves,
+                     int32_t *missing, void *workspace, size_t workspace_bytes, void *hip_stream) {
     try {
         g_err[0] = 0;
         const char *who = "nm_kv_fork";
@@ -986,8 +968,7 @@ nm_status nm_kv_fork(const int32_t *parent, const int32_t *child, int64_t n, int
         if (n < 1 || n > (1 << 20)) return fail(NM_ERR_SHAPE, "%s: n=%lld out of range [1, 2^20]", who, (long long)n);
         if (!aligned(parent, 4)) return fail(NM_ERR_ALIGN, "%s: 4-byte alignment needed", who);
         nmk::KvBook b;
-        nm_status st = kv_book(who, page_table, ld_table, table_cols, kv_len, S, refcount, num_pages, page_size, child,
-                               n, moves, missing, workspace, workspace_bytes, b);
+        nm_status st = kv_book(who, book, child, n, moves, missing, workspace, workspace_bytes, b);
         if (st != NM_OK) return st;
         hipError_t e = nmk::launch_kv_fork(b, parent, child, (int)n, moves, missing, workspace, (hipStream_t)hip_stream);
         return e == hipSuccess ? NM_OK : hip_fail(who, e);
@@ -996,15 +977,13 @@ nm_status nm_kv_fork(const int32_t *parent, const int32_t *child, int64_t n, int
     }
 }
 
-nm_status nm_kv_resize(const int32_t *new_len, int32_t *page_table, int64_t ld_table, int table_cols, int32_t *kv_len,
-                       int64_t S, int32_t *refcount, int64_t num_pages, int page_size, int32_t *moves,
-                       int32_t *missing, void *workspace, size_t workspace_bytes, void *hip_stream) {
+nm_status nm_kv_resize(const nm_kv_book *book, const int32_t *new_len, int32_t *moves, int32_t *missing,
+                       void *workspace, size_t workspace_bytes, void *hip_stream) {
     try {
         g_err[0] = 0;
         const char *who = "nm_kv_resize";
         nmk::KvBook b;
-        nm_status st = kv_book(who, page_table, ld_table, table_cols, kv_len, S, refcount, num_pages, page_size,
-                               new_len, 0, moves, missing, workspace, workspace_bytes, b);
+        nm_status st = kv_book(who, book, new_len, 0, moves, missing, workspace, workspace_bytes, b);
         if (st != NM_OK) return st;
         hipError_t e = nmk::launch_kv_resize(b, new_len, moves, missing, workspace, (hipStream_t)hip_stream);
         return e == hipSuccess ? NM_OK : hip_fail(who, e);
@@ -1013,20 +992,17 @@ nm_status nm_kv_resize(const int32_t *new_len, int32_t *page_table, int64_t ld_t
     }
 }
 
-nm_status nm_kv_compact(int32_t *page_table, int64_t ld_table, int table_cols, int32_t *kv_len, int64_t S,
-                        int32_t *refcount, int64_t num_pages, int page_size, int32_t *moves, int64_t max_moves,
-                        int32_t *used, void *workspace, size_t workspace_bytes, void *hip_stream) {
+nm_status nm_kv_compact(const nm_kv_book *book, int32_t *moves, int64_t max_moves, int32_t *used, void *workspace,
+                        size_t workspace_bytes, void *hip_stream) {
     try {
         g_err[0] = 0;
         const char *who = "nm_kv_compact";
         if (max_moves < 1 || max_moves > kMaxDim / 2)
             return fail(NM_ERR_SHAPE, "%s: max_moves=%lld out of range [1, 2^29]", who, (long long)max_moves);
         nmk::KvBook b;
-        nm_status st = kv_book(who, page_table, ld_table, table_cols, kv_len, S, refcount, num_pages, page_size, kv_len,
-                               0, moves, used, workspace, workspace_bytes, b);
+        nm_status st = kv_book(who, book, moves, 0, moves, used, workspace, workspace_bytes, b);
         if (st != NM_OK) return st;
-        hipError_t e =
-            nmk::launch_kv_compact(b, moves, (int)max_moves, used, workspace, (hipStream_t)hip_stream);
+        hipError_t e = nmk::launch_kv_compact(b, moves, (int)max_moves, used, workspace, (hipStream_t)hip_stream);
         return e == hipSuccess ? NM_OK : hip_fail(who, e);
     } catch (...) {
         return fail(NM_ERR_HIP, "nm_kv_compact: internal error");

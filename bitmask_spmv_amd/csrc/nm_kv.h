@@ -61,6 +61,7 @@ struct Kv4Attention {
     int heads = 0;
     float scale = 1.f;
     int64_t window = 0;  // keys a query looks back over, itself among them; 0: all
+    bool whole = false;    // a workgroup to each row tile
     bool prompts = false;  // sequences of many rows are taken by the prompt kernel
 };
 

@@ -23,6 +23,8 @@
 // not be alike, nor known to the host.  A wave finishes the rows whose blocks are all its own;
 // pieces of rows cut between waves are joined in LDS, those cut between workgroups in fp32
 // through the workspace by a second kernel, in a fixed order.
+#include <atomic>
+
 #include "nm_device.h"
 #include "nm_kv.h"
 
@@ -34,6 +36,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kBlock = 64;      // tokens a wave takes at a time
 constexpr int kRows = 16;       // query rows of a tile
 constexpr int kWaves = 4;       // waves per workgroup
+// Context up to which each row tile may be one workgroup's, which needs no second launch:
+// 8 sequences of 1000 tokens 10.4 us against 12.5, of 2000 14.1 against 13.4; where there
+// are row tiles for a quarter of the workgroups twice that: 32 of 2000 15.3 against 20.6.
+constexpr int kWholeTokens = 1024;
 constexpr int kDecodeRows = 64; // query rows of a head up to which a sequence is walked row tile by row tile
 constexpr int kGroupsPerCu = 2; // resident workgroups: 8 waves a CU, 8.7 KB of cache in flight each
 
@@ -149,7 +155,7 @@ struct Seq {
     int q0, n, len;      // first row, rows, tokens
     int tiles;           // row tiles per key/value head
     int first, blocks;   // first 64-token block and how many (at least one)
-    __device__ int64_t units(int n_kv) const { return (int64_t)tiles * n_kv * blocks; }
+    __device__ int64_t units(int n_kv, bool whole) const { return (int64_t)tiles * n_kv * (whole ? 1 : blocks); }
 };
 
 __device__ __forceinline__ Seq seq_from(const Kv4Attention &a, int group, int q0, int q1, int len) {
@@ -470,20 +476,21 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attenti
     // my run of units
     SeqLane sl, behind;
     sl.load(a.b, lane);
-    int64_t w = seq_from(a, group, sl.q0, sl.q1, sl.len).units(f.n_kv);
+    int64_t w = seq_from(a, group, sl.q0, sl.q1, sl.len).units(f.n_kv, a.whole);
     int64_t upto = units_scan(w, lane);
     int64_t total = lane64(upto, 63);
     for (int s0 = 64; s0 < a.b.S; s0 += 64) {
         if (s0 == 64) behind.load(a.b, s0 + lane);
         const SeqLane x = behind;
         behind.load(a.b, s0 + 64 + lane);
-        total += lane64(units_scan(seq_from(a, group, x.q0, x.q1, x.len).units(f.n_kv), lane), 63);
+        total += lane64(units_scan(seq_from(a, group, x.q0, x.q1, x.len).units(f.n_kv, a.whole), lane), 63);
     }
     const int64_t waves = (int64_t)gridDim.x * kWaves;
     const int64_t run = total < ((int64_t)1 << 31) ? (int64_t)(((uint32_t)total + (uint32_t)waves - 1) / (uint32_t)waves)
                                                    : (total + waves - 1) / waves;
-    int64_t u = ((int64_t)blockIdx.x * kWaves + wave) * run;
-    const int64_t end = u + run < total ? u + run : total;
+    int64_t u = a.whole ? blockIdx.x : ((int64_t)blockIdx.x * kWaves + wave) * run;
+    const int64_t stop = a.whole ? u + 1 : u + run;
+    const int64_t end = stop < total ? stop : total;
     if (lane < 2) sh.tag[wave][lane].state = kNone;
 
     int s0 = 0;        // the 64 sequences that the lanes hold
@@ -495,7 +502,7 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attenti
             base += lane64(upto, 63);
             s0 += 64;
             sl.load(a.b, s0 + lane);
-            w = seq_from(a, group, sl.q0, sl.q1, sl.len).units(f.n_kv);
+            w = seq_from(a, group, sl.q0, sl.q1, sl.len).units(f.n_kv, a.whole);
             upto = units_scan(w, lane);
             continue;
         }
@@ -503,12 +510,22 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attenti
         const Seq sq = seq_from(a, group, __builtin_amdgcn_readlane(sl.q0, at), __builtin_amdgcn_readlane(sl.q1, at),
                                 __builtin_amdgcn_readlane(sl.len, at));
         const int64_t in = u - base - lane64(upto - w, at);
-        const int item = in < ((int64_t)1 << 31) ? (int)((uint32_t)in / (uint32_t)sq.blocks) : (int)(in / sq.blocks);
-        const int b0 = (int)(in - (int64_t)item * sq.blocks);
-        const int64_t room = end - u;
-        const int b1 = (int)(room < sq.blocks - b0 ? b0 + room : sq.blocks);
+        int item, b0, b1;
+        if (a.whole) {  // a unit is a row tile, a quarter of its blocks is mine (the last waves may have none)
+            const int mine = (sq.blocks + kWaves - 1) / kWaves;
+            item = (int)in;
+            b0 = wave * mine;
+            b1 = b0 + mine < sq.blocks ? b0 + mine : sq.blocks;
+            u = end;
+            if (b0 >= b1) break;
+        } else {
+            item = in < ((int64_t)1 << 31) ? (int)((uint32_t)in / (uint32_t)sq.blocks) : (int)(in / sq.blocks);
+            b0 = (int)(in - (int64_t)item * sq.blocks);
+            const int64_t room = end - u;
+            b1 = (int)(room < sq.blocks - b0 ? b0 + room : sq.blocks);
+            u += b1 - b0;
+        }
         const int head = item / sq.tiles, tile = item - head * sq.tiles;
-        u += b1 - b0;
 
         // two blocks in flight: the next one's loads are under way while one is multiplied
         const int32_t *row = a.b.table + (int64_t)s * a.b.ld_table;
@@ -611,7 +628,7 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attenti
             if (first < 0) out0 = tag; else out1 = tag;
         }
     }
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && !a.whole) {
         tags[me * 2] = out0;
         tags[me * 2 + 1] = out1;
     }
@@ -861,12 +878,18 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
 }
 
 int device_cus() {
+    static std::atomic<int> known[64];
     int dev = 0, cu = 0;
-    if (hipGetDevice(&dev) != hipSuccess ||
-        hipDeviceGetAttribute(&cu, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cu <= 0) {
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) {
         (void)hipGetLastError();
         return 256;
     }
+    if ((cu = known[dev].load(std::memory_order_relaxed)) > 0) return cu;
+    if (hipDeviceGetAttribute(&cu, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cu <= 0) {
+        (void)hipGetLastError();
+        return 256;
+    }
+    known[dev].store(cu, std::memory_order_relaxed);
     return cu;
 }
 
@@ -888,11 +911,17 @@ hipError_t launch(Kv4Attention a, int64_t max_q, void *ws, hipStream_t st) {
     const int groups = device_cus() * kGroupsPerCu;
     Part<D> *parts = (Part<D> *)ws;
     PartTag *tags = (PartTag *)(parts + 2 * (size_t)groups);
+    // Few and short: a workgroup to each row tile (sequence s has none but its own of
+    // q_start[s] * group / rows + s on, so their number is bounded), nothing to join.
+    const int64_t tiles = ((int64_t)a.b.T * group / kRows + a.b.S) * a.b.f.n_kv;
+    const int64_t longest = (int64_t)a.b.cols * a.b.f.page;
+    a.whole = tiles <= groups && longest <= (4 * tiles < groups ? kWholeTokens : 2 * kWholeTokens);
+    const int grid = a.whole ? (int)tiles : groups;
     if (max_q * group <= kRows)
-        kv4_decode_kernel<D, true><<<groups, kWaves * kWave, 0, st>>>(a, parts, tags);
+        kv4_decode_kernel<D, true><<<grid, kWaves * kWave, 0, st>>>(a, parts, tags);
     else
-        kv4_decode_kernel<D, false><<<groups, kWaves * kWave, 0, st>>>(a, parts, tags);
-    kv4_join_kernel<D><<<groups, 256, 0, st>>>(a, parts, tags);
+        kv4_decode_kernel<D, false><<<grid, kWaves * kWave, 0, st>>>(a, parts, tags);
+    if (!a.whole) kv4_join_kernel<D><<<groups, 256, 0, st>>>(a, parts, tags);
     return hipGetLastError();
 }
 

@@ -408,17 +408,18 @@ nm_status nm_stream_read(const void *buf, size_t bytes, uint32_t *sink, size_t s
  * [g][c] are channels 8c..8c+7 of tokens 4g..4g+3; K scale [G][r][b][j] is block b of
  * token 64G + 16j + r; V scale [g][b][i] block b of token 4g + i.
  *
- * A ragged batch.  page_table int32 [S][ld_table] (table_cols entries used): page of
- * tokens c*page_size.. of sequence s.  kv_len int32 [S]: tokens of the sequence, new ones
- * included.  q_start int32 [S + 1], non-decreasing, q_start[0] = 0: sequence s owns rows
+ * A ragged batch (nm_kv4_batch).  page_table [S][ld_table] (table_cols entries used): page
+ * of tokens c*page_size.. of sequence s.  kv_len [S]: tokens of the sequence, new ones
+ * included.  q_start [S + 1], non-decreasing, q_start[0] = 0: sequence s owns rows
  * q_start[s] .. q_start[s+1] of the token arrays; of its n rows row i is at place
- * kv_len[s] - n + i.  All are DEVICE arrays and may change between replays of a captured
- * graph.  Sequences without rows are allowed.  A place below 0, behind the table's last
+ * kv_len[s] - n + i.  The struct is read during the call only; its arrays are DEVICE arrays
+ * and may change between replays of a captured graph.  Sequences without rows are allowed.
+ * A place below 0, behind the table's last
  * column or on a page number outside [0, num_pages) holds nothing: it is not written, reads
  * as zeros (unpack) and is left out (attention).  Rows from q_start[S] to T are not touched.
- * Token arrays are bf16 [T][heads][D] with element strides ld* (token) and hd* (head), both
- * multiples of 8, the base 16-byte aligned.  T <= 2^24, S <= 2^20, n_kv <= 256; T = 0 is
- * allowed.  The cache is 16-byte aligned.
+ * Token arrays (nm_kv4_rows) are bf16 [T][heads][D] with element strides ld (token) and hd
+ * (head), both multiples of 8, the base 16-byte aligned.  T <= 2^24, S <= 2^20, n_kv <= 256;
+ * T = 0 is allowed (the rows' pointers may then be NULL).  The cache is 16-byte aligned.
  *
  * nm_kv4_append -- stores rows of k and v.  Per block of 32 channels, with E the biased
  * exponent of the largest magnitude a and m its significand in [1, 2):
@@ -440,26 +441,32 @@ nm_status nm_stream_read(const void *buf, size_t bytes, uint32_t *sink, size_t s
  * rest of a page hold does not matter.  Workspace: nm_kv4_attention_workspace_bytes, 16-byte aligned;
  * calls that may overlap in time need workspaces of their own.
  */
+typedef struct {
+    uint8_t *cache;            /* [num_pages][page_bytes]; written by nm_kv4_append only */
+    int64_t num_pages;
+    const int32_t *page_table; /* [S][ld_table] */
+    int64_t ld_table;
+    const int32_t *kv_len;     /* [S] */
+    const int32_t *q_start;    /* [S + 1] */
+    int64_t S, T;
+    int table_cols, page_size, n_kv, head_dim;
+} nm_kv4_batch;
+typedef struct {
+    nm_bf16 *p;
+    int64_t ld, hd;
+} nm_kv4_rows;
 int64_t nm_kv4_page_bytes(int page_size, int n_kv, int head_dim); /* 0 for sizes that are refused */
-nm_status nm_kv4_append(const nm_bf16 *k, int64_t ldk, int64_t hdk, const nm_bf16 *v, int64_t ldv, int64_t hdv,
-                        int64_t T, uint8_t *cache, int64_t num_pages, int page_size, int n_kv, int head_dim,
-                        const int32_t *page_table, int64_t ld_table, int table_cols, const int32_t *kv_len,
-                        const int32_t *q_start, int64_t S, void *hip_stream);
-nm_status nm_kv4_unpack(const uint8_t *cache, int64_t num_pages, int page_size, int n_kv, int head_dim,
-                        const int32_t *page_table, int64_t ld_table, int table_cols, const int32_t *kv_len,
-                        const int32_t *q_start, int64_t S, int64_t T, nm_bf16 *k, int64_t ldk, int64_t hdk,
-                        nm_bf16 *v, int64_t ldv, int64_t hdv, void *hip_stream);
+nm_status nm_kv4_append(const nm_kv4_batch *batch, const nm_kv4_rows *k, const nm_kv4_rows *v, void *hip_stream);
+nm_status nm_kv4_unpack(const nm_kv4_batch *batch, const nm_kv4_rows *k, const nm_kv4_rows *v, void *hip_stream);
 size_t nm_kv4_attention_workspace_bytes(int64_t T, int64_t S, int n_heads, int n_kv, int head_dim, int64_t max_q_len);
-nm_status nm_kv4_attention(const nm_bf16 *q, int64_t ldq, int64_t hdq, int64_t T, int n_heads, const uint8_t *cache,
-                           int64_t num_pages, int page_size, int n_kv, int head_dim, const int32_t *page_table,
-                           int64_t ld_table, int table_cols, const int32_t *kv_len, const int32_t *q_start, int64_t S,
-                           int64_t max_q_len, float scale, int64_t window, nm_bf16 *out, int64_t ldo, int64_t hdo,
-                           float *lse, int64_t ld_lse, void *workspace, size_t workspace_bytes, void *hip_stream);
+nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int n_heads, int64_t max_q_len, float scale,
+                           int64_t window, const nm_kv4_rows *out, float *lse, int64_t ld_lse, void *workspace,
+                           size_t workspace_bytes, void *hip_stream);
 
 /*
- * Keeping the pages of a cache.  The state is the page table (entries behind a sequence's
- * last page are -1), kv_len and a reference count per page, int32 [num_pages]: how many
- * sequences hold it, 0 = free.  One table serves the caches of all layers.  Free pages are
+ * Keeping the pages of a cache.  The state (nm_kv_book) is the page table (entries behind a
+ * sequence's last page are -1), kv_len and a reference count per page: how many sequences
+ * hold it, 0 = free.  One table serves the caches of all layers.  Free pages are
  * handed out lowest number first, in the order of the requests, so a result depends on the
  * state and the arguments alone.  S * table_cols and num_pages <= 2^30, pairs <= 2^20, moves <= 2^29.  Workspace for all
  * three: nm_kv_pages_workspace_bytes(S, n_pairs, num_pages), 16-byte aligned (n_pairs 0
@@ -494,16 +501,22 @@ nm_status nm_kv4_attention(const nm_bf16 *q, int64_t ldq, int64_t hdq, int64_t T
  * target of two, or source and target, ends up with unspecified bytes.  page_bytes and
  * layer_stride are multiples of 16.
  */
+typedef struct {
+    int32_t *page_table; /* [S][ld_table] */
+    int64_t ld_table;
+    int32_t *kv_len;     /* [S] */
+    int64_t S;
+    int32_t *refcount;   /* [num_pages] */
+    int64_t num_pages;
+    int table_cols, page_size;
+} nm_kv_book;
 size_t nm_kv_pages_workspace_bytes(int64_t S, int64_t n_pairs, int64_t num_pages);
-nm_status nm_kv_resize(const int32_t *new_len, int32_t *page_table, int64_t ld_table, int table_cols, int32_t *kv_len,
-                       int64_t S, int32_t *refcount, int64_t num_pages, int page_size, int32_t *moves,
-                       int32_t *missing, void *workspace, size_t workspace_bytes, void *hip_stream);
-nm_status nm_kv_fork(const int32_t *parent, const int32_t *child, int64_t n, int32_t *page_table, int64_t ld_table,
-                     int table_cols, int32_t *kv_len, int64_t S, int32_t *refcount, int64_t num_pages, int page_size,
-                     int32_t *moves, int32_t *missing, void *workspace, size_t workspace_bytes, void *hip_stream);
-nm_status nm_kv_compact(int32_t *page_table, int64_t ld_table, int table_cols, int32_t *kv_len, int64_t S,
-                        int32_t *refcount, int64_t num_pages, int page_size, int32_t *moves, int64_t max_moves,
-                        int32_t *used, void *workspace, size_t workspace_bytes, void *hip_stream);
+nm_status nm_kv_resize(const nm_kv_book *book, const int32_t *new_len, int32_t *moves, int32_t *missing,
+                       void *workspace, size_t workspace_bytes, void *hip_stream);
+nm_status nm_kv_fork(const nm_kv_book *book, const int32_t *parent, const int32_t *child, int64_t n, int32_t *moves,
+                     int32_t *missing, void *workspace, size_t workspace_bytes, void *hip_stream);
+nm_status nm_kv_compact(const nm_kv_book *book, int32_t *moves, int64_t max_moves, int32_t *used, void *workspace,
+                        size_t workspace_bytes, void *hip_stream);
 nm_status nm_kv_copy_pages(uint8_t *cache, int64_t num_pages, int64_t page_bytes, int64_t layers, int64_t layer_stride,
                            const int32_t *moves, int64_t n, void *hip_stream);
 

@@ -14,30 +14,34 @@ ODD = 0x10001
 HALF = 0x10008
 
 i64, p, i32, sz, f32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
-BATCH = [("cache", p, A), ("num_pages", i64, 4), ("page_size", i32, 64), ("n_kv", i32, 2), ("head_dim", i32, 128),
-         ("page_table", p, A), ("ld_table", i64, 8), ("table_cols", i32, 8), ("kv_len", p, A), ("q_start", p, A), ("S", i64, 3)]
+BATCH = [("cache", p, A), ("num_pages", i64, 4), ("page_table", p, A), ("ld_table", i64, 8), ("kv_len", p, A),
+         ("q_start", p, A), ("S", i64, 3), ("T", i64, 5), ("table_cols", i32, 8), ("page_size", i32, 64), ("n_kv", i32, 2),
+         ("head_dim", i32, 128)]
+BOOK = [("page_table", p, A), ("ld_table", i64, 8), ("kv_len", p, A), ("S", i64, 3), ("refcount", p, A),
+        ("num_pages", i64, 40), ("table_cols", i32, 8), ("page_size", i32, 64)]
+WS = [("workspace", p, A), ("workspace_bytes", sz, 1 << 40), ("stream", p, None)]
 
 
 def rows(n):
-    return [(n, p, A), ("ld" + n, i64, 256), ("hd" + n, i64, 128)]
+    return ("rows " + n, [(n, p, A), ("ld" + n, i64, 1024), ("hd" + n, i64, 128)])
 
 
-BOOK = [("page_table", p, A), ("ld_table", i64, 8), ("table_cols", i32, 8), ("kv_len", p, A), ("S", i64, 3),
-        ("refcount", p, A), ("num_pages", i64, 40), ("page_size", i32, 64)]
-WS = [("workspace", p, A), ("workspace_bytes", sz, 1 << 20), ("stream", p, None)]
+# an argument: (name, type, value), or (name, fields) of a struct that is passed by address
 CALLS = {
-    "nm_kv4_append": [*rows("k"), *rows("v"), ("T", i64, 5), *BATCH, ("stream", p, None)],
-    "nm_kv4_unpack": [*BATCH, ("T", i64, 5), *rows("k"), *rows("v"), ("stream", p, None)],
-    "nm_kv4_attention": [("q", p, A), ("ldq", i64, 1024), ("hdq", i64, 128), ("T", i64, 5), ("n_heads", i32, 8), *BATCH,
-                         ("max_q_len", i64, 1), ("scale", f32, 0.1), ("window", i64, 0), ("out", p, A), ("ldo", i64, 1024),
-                         ("hdo", i64, 128), ("lse", p, A), ("ld_lse", i64, 8), ("workspace", p, A),
-                         ("workspace_bytes", sz, 1 << 40), ("stream", p, None)],
-    "nm_kv_resize": [("new_len", p, A), *BOOK, ("moves", p, A), ("missing", p, A), *WS],
-    "nm_kv_fork": [("parent", p, A), ("child", p, A), ("n", i64, 2), *BOOK, ("moves", p, A), ("missing", p, A), *WS],
-    "nm_kv_compact": [*BOOK, ("moves", p, A), ("max_moves", i64, 9), ("used", p, A), *WS],
+    "nm_kv4_append": [("batch", BATCH), rows("k"), rows("v"), ("stream", p, None)],
+    "nm_kv4_unpack": [("batch", BATCH), rows("k"), rows("v"), ("stream", p, None)],
+    "nm_kv4_attention": [("batch", BATCH), rows("q"), ("n_heads", i32, 8), ("max_q_len", i64, 1), ("scale", f32, 0.1),
+                         ("window", i64, 0), rows("o"), ("lse", p, A), ("ld_lse", i64, 8), *WS],
+    "nm_kv_resize": [("book", BOOK), ("new_len", p, A), ("moves", p, A), ("missing", p, A), *WS],
+    "nm_kv_fork": [("book", BOOK), ("parent", p, A), ("child", p, A), ("n", i64, 2), ("moves", p, A), ("missing", p, A), *WS],
+    "nm_kv_compact": [("book", BOOK), ("moves", p, A), ("max_moves", i64, 9), ("used", p, A), *WS],
     "nm_kv_copy_pages": [("cache", p, A), ("num_pages", i64, 4), ("page_bytes", i64, 64), ("layers", i64, 2),
                          ("layer_stride", i64, 256), ("moves", p, A), ("n", i64, 3), ("stream", p, None)],
 }
+
+
+def fields(name):
+    return [f for a in CALLS[name] for f in (a[1] if len(a) == 2 else [a])]
 
 
 @pytest.fixture(scope="module")
@@ -45,7 +49,7 @@ def L():
     lib = ctypes.CDLL(LIB)
     lib.nm_last_error.restype = ctypes.c_char_p
     for name, args in CALLS.items():
-        getattr(lib, name).argtypes = [a[1] for a in args]
+        getattr(lib, name).argtypes = [p if len(a) == 2 else a[1] for a in args]
     lib.nm_kv4_page_bytes.argtypes, lib.nm_kv4_page_bytes.restype = [i32] * 3, i64
     lib.nm_kv4_attention_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i64]
     lib.nm_kv4_attention_workspace_bytes.restype = sz
@@ -54,9 +58,29 @@ def L():
 
 
 def call(L, name, **bad):
-    args = CALLS[name]
-    assert not set(bad) - {a[0] for a in args}
-    return getattr(L, name)(*[bad.get(n, v) for n, _, v in args])
+    assert not set(bad) - {f[0] for f in fields(name)} - {a[0] for a in CALLS[name]}
+    args, keep = [], []
+    for a in CALLS[name]:
+        if len(a) == 3:
+            args.append(bad.get(a[0], a[2]))
+        elif a[0] in bad:
+            args.append(bad[a[0]])
+        else:
+            S = type("S", (ctypes.Structure,), {"_fields_": [(n, t) for n, t, _ in a[1]]})
+            keep.append(S(*[bad.get(n, v) for n, _, v in a[1]]))
+            args.append(ctypes.addressof(keep[-1]))
+    return getattr(L, name)(*args)
+
+
+def test_python_packs_the_structs_as_c_does():
+    """The binding's struct formats have the sizes of the C structs."""
+    import struct
+
+    for fmt, fl in (("@PqPqPPqq4i", BATCH), ("@Pqq", rows("k")[1]), ("@PqPqPq2i", BOOK)):
+        S = type("S", (ctypes.Structure,), {"_fields_": [(n, t) for n, t, _ in fl]})
+        assert struct.calcsize(fmt) == sum(ctypes.sizeof(t) for _, t, _ in fl) <= ctypes.sizeof(S)
+        text = open(os.path.join(ROOT, "bitmask_spmv_amd", "__init__.py")).read()
+        assert f'struct.Struct("{fmt}")' in text
 
 
 OPTIONAL = {"stream", "lse"}
@@ -64,7 +88,10 @@ OPTIONAL = {"stream", "lse"}
 
 @pytest.mark.parametrize("name", sorted(CALLS))
 def test_null_pointers_and_odd_addresses(L, name):
-    for arg, kind, _ in CALLS[name]:
+    for a in CALLS[name]:
+        if len(a) == 2:
+            assert call(L, name, **{a[0]: None}) == NULL, a[0]
+    for arg, kind, _ in fields(name):
         if kind is not p or arg in OPTIONAL:
             continue
         st = call(L, name, **{arg: None})
@@ -91,7 +118,7 @@ def test_sizes_of_a_batch(L, name, bad):
 
 
 @pytest.mark.parametrize("name,bad,want", [
-    ("nm_kv4_append", dict(ldk=120), SHAPE), ("nm_kv4_append", dict(hdv=64), SHAPE), ("nm_kv4_append", dict(ldk=260), ALIGN),
+    ("nm_kv4_append", dict(ldk=120), SHAPE), ("nm_kv4_append", dict(hdv=64), SHAPE), ("nm_kv4_append", dict(ldk=1028), ALIGN),
     ("nm_kv4_append", dict(k=HALF), ALIGN), ("nm_kv4_append", dict(cache=HALF), ALIGN), ("nm_kv4_unpack", dict(hdk=132), ALIGN),
     ("nm_kv4_unpack", dict(ldv=-8), SHAPE), ("nm_kv4_attention", dict(n_heads=7), SHAPE),
     ("nm_kv4_attention", dict(n_heads=0), SHAPE), ("nm_kv4_attention", dict(n_heads=2048), SHAPE),
@@ -108,7 +135,7 @@ def test_rows_heads_and_scales(L, name, bad, want):
 @pytest.mark.parametrize("bad,want", [
     (dict(page_size=32), SHAPE), (dict(S=0), SHAPE), (dict(S=(1 << 20) + 1), SHAPE), (dict(num_pages=0), SHAPE),
     (dict(num_pages=(1 << 30) + 1), SHAPE), (dict(table_cols=0), SHAPE), (dict(ld_table=5), SHAPE),
-    (dict(S=1 << 20, table_cols=2048, ld_table=2048), SHAPE), (dict(workspace_bytes=16), WORKSPACE)])
+    (dict(S=1 << 20, table_cols=2048, ld_table=2048), SHAPE), (dict(workspace_bytes=8), WORKSPACE)])
 def test_page_keeping(L, name, bad, want):
     assert call(L, name, **bad) == want
 
@@ -126,7 +153,7 @@ def test_lists(L, name, bad, want):
 def test_nothing_to_do_is_not_an_error(L):
     assert call(L, "nm_kv4_append", T=0, k=None, v=None) == OK
     assert call(L, "nm_kv4_unpack", T=0, S=0, k=None, v=None) == OK
-    assert call(L, "nm_kv4_attention", T=0, q=None, out=None, lse=None) == OK
+    assert call(L, "nm_kv4_attention", T=0, q=None, o=None, lse=None) == OK
     assert call(L, "nm_kv_copy_pages", n=0, moves=None) == OK
 
 
