@@ -35,6 +35,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kBlock = 64;      // tokens a wave takes at a time
 constexpr int kRows = 16;       // query rows of a tile
+// O is rescaled only when a score passes the largest one so far by 2^kSlack; weights are kept
+// relative to that point, so that they stay at or below 1 (and O below keys times the largest value).
+constexpr float kSlack = 8.f;
 constexpr int kWaves = 4;       // waves per workgroup
 // Context up to which each row tile may be one workgroup's, which needs no second launch:
 // 8 sequences of 1000 tokens 10.4 us against 12.5, of 2000 14.1 against 13.4; where there
@@ -59,6 +62,12 @@ __device__ __forceinline__ int32_t uniform_load(const int32_t *p) {
 }
 
 __device__ __forceinline__ float pow2_byte(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// Scale i of a dword's four for the conversion instruction, which reads the exponent field
+// alone: what lands in the sign and fraction does not matter.
+__device__ __forceinline__ float scale_field(uint32_t dword, int i) {
+    return __uint_as_float(i < 3 ? dword << (23 - 8 * i) : dword >> 1);
+}
 
 __device__ __forceinline__ float rows_max(float v) {  // over the four lanes of a column
     const uint32_t u = __float_as_uint(v);
@@ -219,18 +228,42 @@ __device__ __forceinline__ int64_t lane64(int64_t v, int i) {
     return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
-// The page of 64-token block b of a sequence's table row, -1 where there is none.
-__device__ __forceinline__ int page_of(const Kv4Batch &b, const int32_t *row, int block) {
-    const int col = block / (b.f.page / kBlock);
-    if (block < 0 || col >= b.cols) return -1;
-    const int page = uniform_load(row + col);
-    return page < b.num_pages ? page : -1;
-}
+// Where the 64-token blocks of one head lie: lane i holds the address of block `first` + i of
+// a sequence, so that a walk reads the page table once for kAhead blocks and turns a page into
+// an address off its critical path.  Without a valid page the address is that of page 0,
+// so that loads need no branch (a branch around them would make the wave wait for all it has in
+// flight), and the block's bit in `valid` is clear.
+struct Blocks {
+    static constexpr int kAhead = 60;  // of 64: a walk looks up to three blocks ahead
+    uint32_t lo, hi;
+    uint64_t valid;
+    __device__ void load(const Kv4Batch &b, const int32_t *row, int head, int first, int lane) {
+        const int per = b.f.page / kBlock, block = first + lane;
+        const int col = block / per;
+        int page = col < b.cols ? row[col] : -1;
+        const bool ok = page >= 0 && page < b.num_pages;
+        if (!ok) page = 0;
+        valid = __ballot(ok);
+        const uint64_t at = (uint64_t)(uintptr_t)b.cache + (uint64_t)page * (uint64_t)b.f.page_bytes() +
+                            (uint64_t)head * (uint64_t)b.f.head_bytes() +
+                            (uint64_t)((block & (per - 1)) * (kBlock / 2)) * b.f.dim;
+        lo = (uint32_t)at;
+        hi = (uint32_t)(at >> 32);
+    }
+    // K values of block i of the 64 (V values v_at behind them); places that scales differ
+    // by are in scales_at.
+    __device__ const uint8_t *at(int i) const {
+        const uint32_t l = __builtin_amdgcn_readlane((int)lo, i), h = __builtin_amdgcn_readlane((int)hi, i);
+        return (const uint8_t *)(uintptr_t)((uint64_t)h << 32 | l);
+    }
+    __device__ bool ok(int i) const { return (valid >> i) & 1; }
+};
 
-// Head block of a page; that of page 0 for no page, so that loads need no branch (a branch
-// around them would make the wave wait for all it has in flight).
-__device__ __forceinline__ const uint8_t *head_block(const Kv4Batch &b, int page, int head) {
-    return b.cache + (int64_t)(page < 0 ? 0 : page) * b.f.page_bytes() + (int64_t)head * b.f.head_bytes();
+// From a block's K values to its K scales: the tokens before it in the page count D / 32
+// scale bytes, not D / 2 value bytes.
+__device__ __forceinline__ int scales_at(const Kv4Format &f, int block) {
+    const int tok0 = (block & (f.page / kBlock - 1)) * kBlock;
+    return f.ks_at() - tok0 * (f.dim / 2 - f.dim / 32);
 }
 
 // One tile's running softmax in registers: column c = lane % 16 is query row c, the four
@@ -238,7 +271,7 @@ __device__ __forceinline__ const uint8_t *head_block(const Kv4Batch &b, int page
 template <int D>
 struct Tile {
     f32x4 o[D / 16];
-    float m, l;  // m: largest raw score so far
+    float m, l;  // m: the raw score that weights are relative to
 };
 
 template <int D>
@@ -259,7 +292,7 @@ struct Bytes {
 template <int D>
 struct Lane {
     int col, g;
-    int k_off, ks_off, v_off, vs_off;  // byte places of this lane within a block of 64 tokens
+    uint32_t k_off, ks_off, v_off, vs_off;  // byte places of this lane within a block of 64 tokens
     __device__ Lane(int lane) {
         col = lane & 15;
         g = lane >> 4;
@@ -279,10 +312,9 @@ __device__ __forceinline__ T load_cache(const uint8_t *p) {
 }
 
 template <int D, bool NT>
-__device__ __forceinline__ void load_block(Bytes<D> &x, const uint8_t *head, const Kv4Format &f, int tok0,
+__device__ __forceinline__ void load_block(Bytes<D> &x, const uint8_t *k, const Kv4Format &f, int block,
                                            const Lane<D> &ln) {
-    const uint8_t *k = head + tok0 * (D / 2), *v = head + f.v_at() + tok0 * (D / 2);
-    const uint8_t *ks = head + f.ks_at() + tok0 * (D / 32), *vs = head + f.vs_at() + tok0 * (D / 32);
+    const uint8_t *v = k + f.v_at(), *ks = k + scales_at(f, block), *vs = ks + f.page * (D / 32);
 #pragma unroll
     for (int j = 0; j < 4; ++j) x.k[j] = load_cache<NT, u32x4>(k + ln.k_off + j * 8 * D);
     x.ks = load_cache<NT, uint32_t>(ks + ln.ks_off);
@@ -308,21 +340,24 @@ __device__ __forceinline__ void scores(const Bytes<D> &x, const Query<D> &q, f32
 #undef NM_KV4_DOT
 }
 
-// Scores -> weights relative to the new maximum; O and l follow it.
+// What weights are relative to, as a power of two.
+__device__ __forceinline__ float reference(float m, float c) { return m == -INFINITY ? 0.f : __builtin_fmaf(m, c, kSlack); }
+
+// Scores -> weights; O and l follow the reference.
 template <int D>
 __device__ __forceinline__ void weights(Tile<D> &t, f32x4 (&s)[4], float c) {
     float mx = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3]));
 #pragma unroll
     for (int j = 1; j < 4; ++j) mx = fmaxf(mx, fmaxf(fmaxf(s[j][0], s[j][1]), fmaxf(s[j][2], s[j][3])));
     const float mn = fmaxf(t.m, rows_max(mx));
-    if (__any(mn > t.m)) {
+    if (__any((mn - t.m) * c > kSlack)) {
         const float keep = t.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((t.m - mn) * c);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) t.o[i] *= keep;
         t.l *= keep;
         t.m = mn;
     }
-    const float mc = mn == -INFINITY ? 0.f : mn * c;
+    const float mc = reference(t.m, c);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -347,7 +382,7 @@ __device__ __forceinline__ void add_values(Tile<D> &t, const Bytes<D> &x, const 
         for (int e = 0; e < 8; ++e) {
             w[e] = x.v[2 * s + (e >> 2)][e & 3];
             if (D == 64) w[e] >>= (col & 1) * 16;
-            f[e] = pow2_byte((x.vs[2 * s + (e >> 2)] >> ((e & 3) * 8)) & 255u);
+            f[e] = scale_field(x.vs[2 * s + (e >> 2)], e & 3);
         }
 #pragma unroll
         for (int by = 0; by < D / 32; ++by) {
@@ -415,7 +450,7 @@ __device__ __forceinline__ void keep_part(Part<D> &p, const Tile<D> &t, float c,
         }
     const float l = cross_rows_sum(t.l);
     if (ln.g == 0) {
-        p.m[ln.col] = t.m == -INFINITY ? -INFINITY : t.m * c;
+        p.m[ln.col] = t.m == -INFINITY ? -INFINITY : reference(t.m, c);
         p.l[ln.col] = l;
     }
 }
@@ -529,13 +564,11 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attenti
 
         // two blocks in flight: the next one's loads are under way while one is multiplied
         const int32_t *row = a.b.table + (int64_t)s * a.b.ld_table;
-        const int per = f.page / kBlock;
-        auto load = [&](Bytes<D> &x, int page, int b) {
-            load_block<D, NT>(x, head_block(a.b, page, head), f, ((sq.first + b) & (per - 1)) * kBlock, ln);
-        };
+        Blocks lies;
+        int held = b0;  // first of the blocks whose places are held
+        lies.load(a.b, row, head, sq.first + held, lane);
         Bytes<D> x0, x1;
-        int p0 = page_of(a.b, row, sq.first + b0), p1 = page_of(a.b, row, sq.first + b0 + 1);
-        load(x0, p0, b0);
+        load_block<D, NT>(x0, lies.at(0), f, sq.first + b0, ln);
 
         // queries of my column
         const int64_t r = (int64_t)tile * kRows + ln.col;
@@ -574,15 +607,16 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attenti
             add_values(tl, x, sc, ln.col);
         };
         for (int b = b0; b < b1; b += 2) {
-            const int p2 = page_of(a.b, row, sq.first + b + 2);
-            load(x1, p1, b + 1);
-            if (p0 >= 0) add(x0, b);
+            if (b - held == Blocks::kAhead) {
+                held = b;
+                lies.load(a.b, row, head, sq.first + held, lane);
+            }
+            const int i = b - held;
+            load_block<D, NT>(x1, lies.at(i + 1), f, sq.first + b + 1, ln);
+            if (lies.ok(i)) add(x0, b);
             if (b + 1 >= b1) break;
-            const int p3 = page_of(a.b, row, sq.first + b + 3);
-            load(x0, p2, b + 2);
-            if (p1 >= 0) add(x1, b + 1);
-            p0 = p2;
-            p1 = p3;
+            load_block<D, NT>(x0, lies.at(i + 2), f, sq.first + b + 2, ln);
+            if (lies.ok(i + 1)) add(x1, b + 1);
         }
 
         const bool begins = b0 == 0, ends = b1 == sq.blocks;
@@ -593,7 +627,7 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attenti
 #pragma unroll
                 for (int m = 0; m < D / 16; ++m) o[(D / 16) * i + m] = tl.o[m][i];
             const float l = cross_rows_sum(tl.l);
-            if (real) store_row<D>(a, t, h, ln.g, o, tl.m * c, l, ln.g == 0);
+            if (real) store_row<D>(a, t, h, ln.g, o, reference(tl.m, c), l, ln.g == 0);
         } else {
             const int slot = begins ? 1 : 0;
             keep_part(sh.part[wave][slot], tl, c, ln);
@@ -676,25 +710,70 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attention a, const Par
 // quarter of the next block's values into the operand order of the product and leaves them
 // in LDS (two buffers, one barrier a block), so a value is converted once for 128 rows and
 // read from LDS without bank conflicts; keys go from the page into the matrix
-// instruction as in decode.
-constexpr int kPromptTiles = 2;                              // 16-row tiles per wave
-constexpr int kPromptRows = kWaves * kPromptTiles * kRows;   // rows of a workgroup
+// instruction as in decode.  Here 32 x 32 tiles: a matrix instruction keeps the vector unit
+// from issuing for about 8 cycles whatever its size, and softmax needs that unit for
+// about as long as the matrix unit is busy (four vector instructions to every 16 x 16 x 32
+// product: 23.6 ns in 16 x 16 tiles, 18.9 ns in 32 x 32 ones; 15 ns without them).
+constexpr int kPromptTile = 32;                       // rows of a wave
+constexpr int kPromptRows = kWaves * kPromptTile;     // rows of a workgroup
 
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// Lane (col, hh) = (lane % 32, lane / 32): column col is a query row, token rows of the scores are
+// 8 (i / 4) + 4 hh + i % 4 of a tile of 32.  Channels: row m of channel tile mt is channel
+// 8 c8 + b with (c8, b) = (m % 16, 2 mt + m / 16) at dim 128, (m % 8, 4 mt + m / 8) at
+// dim 64, so that the 8 channels of a V unit end up in one lane.
 template <int D>
-struct RawValues {  // 32 tokens x half of a lane's channels, converted by one wave
-    u32x4 v[2];
-    uint32_t vs[2];
+struct PromptQuery {
+    u32x6 p[D / 64][4];       // 64 channels each: this lane's 32 of them
+    uint32_t scales[D / 64];  // a byte for each piece
 };
 
 template <int D>
+__device__ __forceinline__ void split_query(u32x4 (&x4)[4], uint32_t signs, u32x6 (&p)[4], uint32_t &scales) {
+    union { u32x4 u[4]; uint32_t w[16]; bf16x32 h; } x;
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x.u[i] = x4[i];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        top = max(top, max(x.w[i] & 0x7FFFu, (x.w[i] >> 16) & 0x7FFFu));
+        x.w[i] ^= signs;
+    }
+    const uint32_t e = max(top >> 7, 20u);  // biased exponent of the largest magnitude
+    const uint32_t at[4] = {e - 2, e - 6, e - 11, e - 16};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float s = pow2_byte(at[k]);
+        p[k] = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(x.h, s);
+        if (k < 3) {  // what is left is a bf16 number: the bits that the piece did not take
+            const f32x32 d = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(p[k], s);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                x.w[i] = pack_bf16(bf16_lo(x.w[i]) - d[2 * i], bf16_hi(x.w[i]) - d[2 * i + 1]);
+        }
+    }
+    scales = at[0] | at[1] << 8 | at[2] << 16 | at[3] << 24;
+}
+
+__device__ __forceinline__ float halves_max(float v) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+__device__ __forceinline__ float halves_sum(float v) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+
+template <int D>
 __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attention a, int tiles) {
-    constexpr int MT = D / 16;  // channel tiles
-    __shared__ u32x4 values[2][2][MT][kWave];
+    constexpr int MT = D / 32, CH = D / 64;  // channel tiles of the values, chunks of the keys
+    __shared__ u32x4 values[2][4][MT][kWave];
     a.b.f.dim = D;
     const Kv4Format &f = a.b.f;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 31, hh = lane >> 5;
     const int group = a.heads / f.n_kv;
-    const Lane<D> ln(lane);
 
     // Row tile: sequence s owns the tiles from q_start[s] * group / rows + s on, which are
     // enough for it.  Later rows, which see more, go first; the heads of a tile go to
@@ -722,159 +801,234 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
     const int64_t any_from = a.window > 0 ? place0 - a.window + 1 : 0;
     const int64_t any_upto = len < cap ? (int64_t)len - 1 : cap - 1;
 
-    Query<D> q[kPromptTiles];
-    Tile<D> tl[kPromptTiles];
-    int upto[kPromptTiles], from[kPromptTiles];
-    const int64_t w0 = r0 + wave * (kPromptTiles * kRows);  // the wave's first row
+    const int64_t w0 = r0 + wave * kPromptTile;  // the wave's first row
+    const int64_t r = w0 + col;
+    const int qi = (int)(r / group), t = q0 + qi, h = head * group + (int)(r - (int64_t)qi * group);
+    const bool real = r < rows && t < a.b.T;
+    PromptQuery<D> q;
 #pragma unroll
-    for (int k = 0; k < kPromptTiles; ++k) {
-        const int64_t r = w0 + k * kRows + ln.col;
-        const int qi = (int)(r / group), t = q0 + qi, h = head * group + (int)(r % group);
-        const bool real = r < rows && t < a.b.T;
-        q[k] = load_query<D>(a.q.p + t * a.q.ld + h * a.q.hd, real, a.scale, ln.g);
-        const int64_t place = place0 + qi;
-        upto[k] = real ? (int)(place < cap ? place : cap - 1) : -1;
-        from[k] = a.window > 0 && place - a.window + 1 > 0 ? (int)(place - a.window + 1) : 0;
-        clear(tl[k]);
+    for (int k = 0; k < CH; ++k) {
+        u32x4 x[4];
+        const uint16_t *p = a.q.p + t * a.q.ld + h * a.q.hd + k * 64 + hh * 32;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = real ? reinterpret_cast<const u32x4 *>(p)[i] : (u32x4){0, 0, 0, 0};
+        split_query<D>(x, a.scale < 0.f ? 0x80008000u : 0u, q.p[k], q.scales[k]);
     }
-    // blocks that the workgroup walks, that the wave needs, that need no mask for the wave
+    const int64_t place = place0 + qi;
+    const int upto = real ? (int)(place < cap ? place : cap - 1) : -1;
+    const int from = a.window > 0 && place - a.window + 1 > 0 ? (int)(place - a.window + 1) : 0;
+    f32x16 o[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) o[i] = f32x16{};
+    float m = -INFINITY, l = 0.f;
+
+    // blocks that the workgroup walks, and those that need no mask for the wave
     const int64_t last_row = (r0 + kPromptRows < rows ? r0 + kPromptRows : rows) - 1;
     const int64_t see_last = place0 + last_row / group < cap ? place0 + last_row / group : cap - 1;
     const int64_t see_first = a.window > 0 ? place0 + r0 / group - a.window + 1 : 0;
     const int b_first = (int)((see_first > 0 ? see_first : 0) / kBlock);
     const int b_end = see_last >= 0 ? (int)(see_last / kBlock) + 1 : 0;
-    const int64_t wl = w0 + kPromptTiles * kRows - 1;
-    const int64_t w_last = place0 + (wl < rows - 1 ? wl : rows - 1) / group;
+    const int64_t wl = w0 + kPromptTile - 1 < rows - 1 ? w0 + kPromptTile - 1 : rows - 1;
+    const int64_t w_last = place0 + wl / group;                    // the last key that any of its rows sees
     const int64_t w_all = place0 + w0 / group < cap - 1 ? place0 + w0 / group : cap - 1;
     const int64_t w_all_from = a.window > 0 ? w_last - a.window + 1 : 0;
-    const bool idle = w0 >= rows;
 
     const int32_t *row = a.b.table + (int64_t)s * a.b.ld_table;
-    const int per = f.page / kBlock;
-    // this wave's share of a block's values: tokens 32 vs .. + 31, bytes vb .. of each word
-    const int vstep = wave >> 1, vhalf = wave & 1;
-    auto load_values = [&](RawValues<D> &x, const uint8_t *hd, int b) {
-        const int tok0 = b % per * kBlock;
-        const uint8_t *v = hd + f.v_at() + tok0 * (D / 2), *vs = hd + f.vs_at() + tok0 * (D / 32);
+    Blocks lies;
+    int held = b_first;  // first of the blocks whose places are held
+    lies.load(a.b, row, head, held, lane);
+
+    // keys: token 32 tt + col, block 2 k + hh; their scales lie by token % 16
+    const uint32_t k_off = col * (D / 2) + hh * 16;
+    const uint32_t ks_off = ((col & 15) * (D / 32) + hh) * 4;
+    u32x4 kx[2][CH];
+    uint32_t ks[CH];
+    auto load_keys = [&](int b) {
+        const uint8_t *kp = lies.at(b - held), *sp = kp + scales_at(f, b);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            x.v[i] = *reinterpret_cast<const u32x4 *>(v + ln.v_off + (2 * vstep + i) * 8 * D);
-            x.vs[i] = *reinterpret_cast<const uint32_t *>(vs + ln.vs_off + (2 * vstep + i) * (D / 2));
+        for (int k = 0; k < CH; ++k) {
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+                kx[tt][k] = *reinterpret_cast<const u32x4 *>(kp + k_off + (tt * 16 * D + k * 32));
+            ks[k] = *reinterpret_cast<const uint32_t *>(sp + ks_off + k * 8);
         }
-    };
-    auto put_values = [&](RawValues<D> &x, int b, u32x4 (*to)[MT][kWave]) {
-        const int64_t j0 = (int64_t)b * kBlock;
-        if (j0 < any_from || j0 + kBlock - 1 > any_upto) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int64_t tok = j0 + 32 * vstep + 16 * (e >> 2) + 4 * ln.g + (e & 3);
-                if (tok > any_upto || tok < any_from) x.vs[e >> 2] &= ~(255u << (8 * (e & 3)));
-            }
-        }
-        uint32_t w[8];
-        float sc[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w[e] = x.v[e >> 2][e & 3] >> (D == 128 ? vhalf * 16 : (ln.col & 1) * 16 + vhalf * 8);
-            sc[e] = pow2_byte((x.vs[e >> 2] >> ((e & 3) * 8)) & 255u);
-        }
-#pragma unroll
-        for (int by = 0; by < D / 64; ++by) {
-            uint32_t cv[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) cv[e] = fp4_pair(w[e], sc[e], by);
-            u32x4 lo, hi;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                lo[e] = __builtin_amdgcn_perm(cv[2 * e + 1], cv[2 * e], 0x05040100u);
-                hi[e] = __builtin_amdgcn_perm(cv[2 * e + 1], cv[2 * e], 0x07060302u);
-            }
-            const int mt = 2 * (vhalf * (D / 64) + by);
-            to[vstep][mt][lane] = lo;
-            to[vstep][mt + 1][lane] = hi;
-        }
-    };
-    auto load_keys = [&](u32x4 (&k)[4], uint32_t &ks, const uint8_t *hd, int b) {
-        const int tok0 = b % per * kBlock;
-        const uint8_t *kp = hd + tok0 * (D / 2);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const u32x4 *>(kp + ln.k_off + j * 8 * D);
-        ks = *reinterpret_cast<const uint32_t *>(hd + f.ks_at() + tok0 * (D / 32) + ln.ks_off);
     };
 
-    Bytes<D> x;  // keys of the block in hand
-    RawValues<D> rv;
-    int now = b_first < b_end ? page_of(a.b, row, b_first) : -1;
-    int next = b_first + 1 < b_end ? page_of(a.b, row, b_first + 1) : -1;
-    int after = page_of(a.b, row, b_first + 2);
-    load_keys(x.k, x.ks, head_block(a.b, now, head), b_first);
-    load_values(rv, head_block(a.b, now, head), b_first);
-    put_values(rv, b_first, values[b_first & 1]);
-    load_values(rv, head_block(a.b, next, head), b_first + 1);
+    // this wave's share of a block's values: tokens 16 u + 4 vh + {0..3, 8..11} of unit column c8,
+    // bytes b0 .. of their words (a byte is two channels)
+    constexpr int kBytes = D / 64;
+    const int vg = lane >> 4, vh = vg & 1, vu = 2 * (wave >> 1) + (vg >> 1);
+    const int c8 = D == 128 ? (lane & 15) : (lane & 7);
+    const int byte0 = D == 128 ? 2 * (wave & 1) : (2 * (wave & 1) + ((lane >> 3) & 1));
+    const uint32_t v_off = ((4 * vu + vh) * (D / 8) + c8) * 16, vs_off = ((4 * vu + vh) * (D / 32) + (c8 >> 2)) * 4;
+    u32x4 vx[2];
+    uint32_t vs[2];
+    auto load_values = [&](int b) {
+        const uint8_t *kp = lies.at(b - held), *vp = kp + f.v_at(), *sp = kp + scales_at(f, b) + f.page * (D / 32);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            vx[i] = *reinterpret_cast<const u32x4 *>(vp + v_off + i * 4 * D);
+            vs[i] = *reinterpret_cast<const uint32_t *>(sp + vs_off + i * (D / 4));
+        }
+    };
+    // a weight of 0 times what an unseen place holds must be 0
+    auto hide_values = [&](int b) {
+        const int64_t j0 = (int64_t)b * kBlock;
+        const bool page = lies.ok(b - held);
+        if (j0 < any_from || j0 + kBlock - 1 > any_upto || !page) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int64_t tok = j0 + 16 * vu + 8 * (e >> 2) + 4 * vh + (e & 3);
+                if (tok > any_upto || tok < any_from || !page) vs[e >> 2] &= ~(255u << (8 * (e & 3)));
+            }
+        }
+    };
+    auto put_values = [&](int by, u32x4 (*to)[MT][kWave]) {  // byte byte0 + by of the words
+        uint32_t cv[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) cv[e] = fp4_pair(vx[e >> 2][e & 3] >> (8 * byte0), scale_field(vs[e >> 2], e & 3), by);
+        u32x4 even, odd;  // channels 2 (byte0 + by) and the next
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            even[e] = __builtin_amdgcn_perm(cv[2 * e + 1], cv[2 * e], 0x05040100u);
+            odd[e] = __builtin_amdgcn_perm(cv[2 * e + 1], cv[2 * e], 0x07060302u);
+        }
+        if constexpr (D == 128) {
+            to[vu][byte0 + by][vh * 32 + c8] = even;
+            to[vu][byte0 + by][vh * 32 + 16 + c8] = odd;
+        } else {
+            u32x4 *p = &to[vu][byte0 >> 1][vh * 32 + 16 * (byte0 & 1) + c8];
+            p[0] = even;
+            p[8] = odd;
+        }
+    };
+
+    // scores of the block whose keys are in hand
+    auto dot = [&](f32x16 (&sc)[2]) {
+        // of a scale dword's four tokens 16 j + col % 16 this lane's are j = col / 16 and that + 2
+        int sk[CH];
+#pragma unroll
+        for (int k = 0; k < CH; ++k) sk[k] = (int)(ks[k] >> ((col >> 4) * 8));
+        const f32x16 zero = {};
+#define NM_KV4_DOT(T, K, P, C)                                                                                        \
+    sc[T] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(kx[T][K]), wide(q.p[K][P]), C, 4, 2, 2 * T, sk[K], P, \
+                                                            (int)q.scales[K])
+        NM_KV4_DOT(0, 0, 0, zero); NM_KV4_DOT(1, 0, 0, zero);
+        NM_KV4_DOT(0, 0, 1, sc[0]); NM_KV4_DOT(1, 0, 1, sc[1]);
+        NM_KV4_DOT(0, 0, 2, sc[0]); NM_KV4_DOT(1, 0, 2, sc[1]);
+        NM_KV4_DOT(0, 0, 3, sc[0]); NM_KV4_DOT(1, 0, 3, sc[1]);
+        if constexpr (CH == 2) {
+            NM_KV4_DOT(0, CH - 1, 0, sc[0]); NM_KV4_DOT(1, CH - 1, 0, sc[1]);
+            NM_KV4_DOT(0, CH - 1, 1, sc[0]); NM_KV4_DOT(1, CH - 1, 1, sc[1]);
+            NM_KV4_DOT(0, CH - 1, 2, sc[0]); NM_KV4_DOT(1, CH - 1, 2, sc[1]);
+            NM_KV4_DOT(0, CH - 1, 3, sc[0]); NM_KV4_DOT(1, CH - 1, 3, sc[1]);
+        }
+#undef NM_KV4_DOT
+    };
+
+    load_keys(b_first);
+    load_values(b_first);
+    hide_values(b_first);
+#pragma unroll
+    for (int by = 0; by < kBytes; ++by) put_values(by, values[b_first & 1]);
+    load_values(b_first + 1);
     __syncthreads();
     for (int b = b_first; b < b_end; ++b) {
-        const int then = page_of(a.b, row, b + 3);
-        put_values(rv, b + 1, values[(b + 1) & 1]);
-        load_values(rv, head_block(a.b, after, head), b + 2);
+        if (b - held == Blocks::kAhead) {
+            held = b;
+            lies.load(a.b, row, head, held, lane);
+        }
+        hide_values(b + 1);
+        // The next block's values are converted while the matrix unit computes this one's scores.
+        f32x16 sc[2];
+        dot(sc);
+#pragma unroll
+        for (int by = 0; by < kBytes; ++by) put_values(by, values[(b + 1) & 1]);
+#pragma unroll
+        for (int i = 0; i < 8 * CH; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        load_values(b + 2);
+        load_keys(b + 1);
+
         const int64_t j0 = (int64_t)b * kBlock;
-        const bool work = now >= 0 && !idle && j0 <= w_last && j0 + kBlock > w_all_from - (int64_t)(w_last - place0 - w0 / group);
-        f32x4 sc[kPromptTiles][4];
-        if (work) {
+        const bool page = lies.ok(b - held);
+        if (j0 < w_all_from || j0 + kBlock - 1 > w_all || !page) {
 #pragma unroll
-            for (int k = 0; k < kPromptTiles; ++k) scores(x, q[k], sc[k]);
+            for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int tok = (int)j0 + 32 * tt + 8 * (i >> 2) + 4 * hh + (i & 3);
+                    if (tok > upto || tok < from || !page) sc[tt][i] = -INFINITY;
+                }
         }
-        load_keys(x.k, x.ks, head_block(a.b, next, head), b + 1);
-        if (work) {
-            if (j0 < w_all_from || j0 + kBlock - 1 > w_all) {
+        float mx = fmaxf(sc[0][0], sc[1][0]);
 #pragma unroll
-                for (int k = 0; k < kPromptTiles; ++k)
+        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, fmaxf(sc[0][i], sc[1][i]));
+        const float mn = fmaxf(m, halves_max(mx));
+        if (__any((mn - m) * c > kSlack)) {
+            const float keep = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - mn) * c);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+            for (int i = 0; i < MT; ++i) o[i] *= keep;
+            l *= keep;
+            m = mn;
+        }
+        const float mc = reference(m, c);
+        // Values are read from LDS kRead - 1 products ahead; the second half's weights are computed
+        // while the first half's products run.
+        constexpr int kRead = 5, kSteps = 4 * MT;
+        const u32x4 *from_lds = &values[b & 1][0][0][lane];
+        u32x4 v[kRead];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int tok = (int)j0 + 16 * j + 4 * ln.g + i;
-                            if (tok > upto[k] || tok < from[k]) sc[k][j][i] = -INFINITY;
-                        }
+        for (int k = 0; k < kRead - 1; ++k) v[k] = from_lds[k * kWave];
+        __builtin_amdgcn_sched_barrier(0);
+        uint32_t p[16];  // weights, as pairs: 8 tokens of each of four 16-token steps
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sc[tt][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[tt][i], c, -mc));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[8 * tt + i] = pack_bf16(sc[tt][2 * i], sc[tt][2 * i + 1]);
+#pragma unroll
+            for (int k = tt * kSteps / 2; k < (tt + 1) * kSteps / 2; ++k) {
+                if (k + kRead - 1 < kSteps) v[(k + kRead - 1) % kRead] = from_lds[(k + kRead - 1) * kWave];
+                union { u32x4 u; bf16x8 h; } x;
+                union { uint32_t w[4]; bf16x8 h; } w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w.w[e] = p[4 * (k / MT) + e];
+                x.u = v[k % kRead];
+                o[k % MT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x.h, w.h, o[k % MT], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0x406);  // vector and scalar work may pass
             }
 #pragma unroll
-            for (int k = 0; k < kPromptTiles; ++k) weights(tl[k], sc[k], c);
-#pragma unroll
-            for (int st = 0; st < 2; ++st) {
-                union { uint32_t w[4]; bf16x8 h; } p[kPromptTiles];
-#pragma unroll
-                for (int k = 0; k < kPromptTiles; ++k) {
-                    p[k].w[0] = pack_bf16(sc[k][2 * st][0], sc[k][2 * st][1]);
-                    p[k].w[1] = pack_bf16(sc[k][2 * st][2], sc[k][2 * st][3]);
-                    p[k].w[2] = pack_bf16(sc[k][2 * st + 1][0], sc[k][2 * st + 1][1]);
-                    p[k].w[3] = pack_bf16(sc[k][2 * st + 1][2], sc[k][2 * st + 1][3]);
-                }
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    union { u32x4 u; bf16x8 h; } v;
-                    v.u = values[b & 1][st][mt][lane];
-#pragma unroll
-                    for (int k = 0; k < kPromptTiles; ++k)
-                        tl[k].o[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v.h, p[k].h, tl[k].o[mt], 0, 0, 0);
-                }
-            }
+            for (int i = 0; i < 4; ++i)
+                l += (sc[tt][4 * i] + sc[tt][4 * i + 1]) + (sc[tt][4 * i + 2] + sc[tt][4 * i + 3]);
         }
-        now = next;
-        next = after;
-        after = then;
         __syncthreads();
     }
+    l = halves_sum(l);
+    if (!real) return;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint16_t *out = a.out.p + t * a.out.ld + h * a.out.hd;
+    // the lane's rows m = 8 i + 4 hh + j of every channel tile
 #pragma unroll
-    for (int k = 0; k < kPromptTiles; ++k) {
-        const int64_t r = w0 + k * kRows + ln.col;
-        const int t = q0 + (int)(r / group), h = head * group + (int)(r % group);
-        float o[D / 4];
+    for (int i = 0; i < (D == 128 ? 2 : 1); ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j) {
+            u32x4 w;
+            if constexpr (D == 128) {  // unit column 8 i + 4 hh + j; channels 2 mt (rows below 16) and 2 mt + 1
 #pragma unroll
-            for (int m = 0; m < MT; ++m) o[MT * i + m] = tl[k].o[m][i];
-        const float l = cross_rows_sum(tl[k].l);
-        if (r < rows && t < a.b.T) store_row<D>(a, t, h, ln.g, o, tl[k].m * c, l, ln.g == 0);
-    }
+                for (int mt = 0; mt < MT; ++mt) w[mt] = pack_bf16(o[mt][4 * i + j] * inv, o[mt][4 * (i + 2) + j] * inv);
+            } else {  // unit column 4 hh + j; channels 4 mt + row / 8
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    w[k] = pack_bf16(o[k >> 1][4 * (2 * (k & 1)) + j] * inv, o[k >> 1][4 * (2 * (k & 1) + 1) + j] * inv);
+            }
+            *reinterpret_cast<u32x4 *>(out + (8 * i + 4 * hh + j) * 8) = w;
+        }
+    if (hh == 0 && a.lse) a.lse[t * a.ld_lse + h] = l > 0.f ? (reference(m, c) + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
 int device_cus() {

@@ -63,15 +63,16 @@ def attention_bounds(r):
     exponent's argument and exp2 itself: 4 steps of the largest score.  exp(x) is off by the score's
     difference, for weight and for sum, hence 2 delta.  Weights are rounded to bf16 for the products, 2^-8 (half
     a step, relative); n products and joined parts are summed in fp32, as is the sum itself.  The result is
-    rounded once to bf16.  Weights below 2^-126 of a row's largest and products below 2^-126 are not normal
-    fp32 numbers and may count as 0: each key then lacks at most 2^-126 (|V| + 1)."""
+    rounded once to bf16.  The largest weight of a row is kept between 2^-8 and 1.  Weights and products below
+    2^-126 are not normal fp32 numbers and may count as 0: each key then lacks at most 2^-126 (|V| + 1) of a sum
+    that is divided by at least 2^-8."""
     keys = r["keys"]
     delta = 2.0**-20 * r["srow"] + 140 * 2.0**-24 * r["smax"] + 2.0**-22
     fp32 = 2.0**-24 * (keys + 64)
     lse = delta + fp32 + 2.0**-22 * np.abs(np.where(np.isfinite(r["lse"]), r["lse"], 0.0))
     rel = (2.0**-8 + 2 * delta + 2 * fp32)[..., None]
     out = 2.0**-8 * np.abs(r["out"]) + rel * r["absum"] * (1 + 2.0**-8)
-    out = out + 2.0**-126 * (1 + keys * (r["vmax"] + 1))[..., None]
+    out = out + 2.0**-118 * (1 + keys * (r["vmax"] + 1))[..., None]
     return out, lse
 
 
