@@ -118,10 +118,10 @@ def _load() -> ctypes.CDLL:
     L.nm_kv4_page_bytes.argtypes, L.nm_kv4_page_bytes.restype = [i32, i32, i32], i64
     d = ctypes.c_char_p  # a descriptor struct, packed by the caller
     L.nm_kv4_append.argtypes = L.nm_kv4_unpack.argtypes = [d, d, d, p]
-    L.nm_kv4_attention_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i64]
+    L.nm_kv4_attention_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i64, i64]
     L.nm_kv4_attention_workspace_bytes.restype = sz
     L.nm_kv4_attention.argtypes = [d, d, i32, i64, f32, i64, d, p, i64, p, sz, p]
-    L.nm_kv_pages_workspace_bytes.argtypes, L.nm_kv_pages_workspace_bytes.restype = [i64, i64, i64], sz
+    L.nm_kv_pages_workspace_bytes.argtypes, L.nm_kv_pages_workspace_bytes.restype = [i64, i64, i64, i32], sz
     L.nm_kv_resize.argtypes = [d, p, p, p, p, sz, p]
     L.nm_kv_fork.argtypes = [d, p, p, i64, p, p, p, sz, p]
     L.nm_kv_compact.argtypes = [d, p, i64, p, p, sz, p]
@@ -691,18 +691,17 @@ def _kv_rows(t: torch.Tensor, name: str, dev: int, shape) -> bytes:
 
 
 def _kv_batch(dev: int, cache: torch.Tensor, page_table, kv_len, q_start, page_size: int, n_kv: int, T: int, D: int):
-    """(nm_kv4_batch, S), checked."""
+    """(nm_kv4_batch, S, tokens a table row has room for), checked."""
     if not isinstance(cache, torch.Tensor) or cache.dtype is not torch.uint8 or cache.get_device() != dev:
         raise TypeError(f"cache must be a uint8 tensor on cuda:{dev}")
     if cache.dim() != 2 or not cache.is_contiguous():
         raise ValueError("cache must be contiguous, [num_pages, page_bytes]")
     N, nbytes = cache.shape
-    want = lib.nm_kv4_page_bytes(page_size, n_kv, D)
-    if want and nbytes != want:
-        raise ValueError(f"cache pages must be of {want} bytes (got {nbytes})")
+    if nbytes != page_size * n_kv * (D + D // 16):  # nm_kv4_page_bytes, where it is not 0
+        raise ValueError(f"cache pages of {page_size} tokens of {n_kv} heads of {D} cannot have {nbytes} bytes")
     tp, ld, cols, S = _table(page_table, dev)
     return _KV4_BATCH.pack(cache.data_ptr(), N, tp, ld, _i32(kv_len, "kv_len", dev, S),
-                           _i32(q_start, "q_start", dev, S + 1), S, T, cols, page_size, n_kv, D), S
+                           _i32(q_start, "q_start", dev, S + 1), S, T, cols, page_size, n_kv, D), S, cols * page_size
 
 
 def _kv_workspace(nbytes: int, t: torch.Tensor, workspace: torch.Tensor | None):
@@ -724,7 +723,7 @@ def nm_kv4_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_ta
     dev, shape = _where(k, "k"), k.shape
     kr, vr = _kv_rows(k, "k", dev, shape), _kv_rows(v, "v", dev, shape)
     T, H, D = shape
-    b, _ = _kv_batch(dev, cache, page_table, kv_len, q_start, page_size, H, T, D)
+    b, _, _ = _kv_batch(dev, cache, page_table, kv_len, q_start, page_size, H, T, D)
     _call(dev, lib.nm_kv4_append, b, kr, vr)
 
 
@@ -735,13 +734,15 @@ def nm_kv4_unpack(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.T
     dev, shape = _where(k_out, "k_out"), k_out.shape
     kr, vr = _kv_rows(k_out, "k_out", dev, shape), _kv_rows(v_out, "v_out", dev, shape)
     T, H, D = shape
-    b, _ = _kv_batch(dev, cache, page_table, kv_len, q_start, page_size, H, T, D)
+    b, _, _ = _kv_batch(dev, cache, page_table, kv_len, q_start, page_size, H, T, D)
     _call(dev, lib.nm_kv4_unpack, b, kr, vr)
     return k_out, v_out
 
 
-def nm_kv4_attention_workspace_bytes(T: int, S: int, n_heads: int, n_kv: int, head_dim: int, max_q_len: int) -> int:
-    return int(lib.nm_kv4_attention_workspace_bytes(T, S, n_heads, n_kv, head_dim, max_q_len))
+def nm_kv4_attention_workspace_bytes(T: int, S: int, n_heads: int, n_kv: int, head_dim: int, max_q_len: int,
+                                     room: int) -> int:
+    """room: tokens that a row of the page table has room for (columns * page_size)."""
+    return int(lib.nm_kv4_attention_workspace_bytes(T, S, n_heads, n_kv, head_dim, max_q_len, room))
 
 
 def nm_kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
@@ -760,15 +761,15 @@ def nm_kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Ten
         lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
     elif lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != (T, Hq) or lse.stride(1) != 1:
         raise ValueError("lse must be fp32 [T, heads], contiguous in its last dimension, on q's device")
-    b, S = _kv_batch(dev, cache, page_table, kv_len, q_start, page_size, n_kv, T, D)
-    ws, wp, wn = _kv_workspace(lib.nm_kv4_attention_workspace_bytes(T, S, Hq, n_kv, D, max_q_len), q, workspace)
+    b, S, room = _kv_batch(dev, cache, page_table, kv_len, q_start, page_size, n_kv, T, D)
+    ws, wp, wn = _kv_workspace(lib.nm_kv4_attention_workspace_bytes(T, S, Hq, n_kv, D, max_q_len, room), q, workspace)
     _call(dev, lib.nm_kv4_attention, b, qr, Hq, max_q_len, D ** -0.5 if scale is None else scale, window,
           _kv_rows(out, "out", dev, shape), lse.data_ptr(), lse.stride(0) if T > 1 else Hq, wp, wn)
     return out, lse
 
 
-def nm_kv_pages_workspace_bytes(S: int, n_pairs: int, num_pages: int) -> int:
-    return int(lib.nm_kv_pages_workspace_bytes(S, n_pairs, num_pages))
+def nm_kv_pages_workspace_bytes(S: int, n_pairs: int, num_pages: int, table_cols: int) -> int:
+    return int(lib.nm_kv_pages_workspace_bytes(S, n_pairs, num_pages, table_cols))
 
 
 def _kv_book(dev: int, page_table, kv_len, refcount, page_size, n_pairs, workspace):
@@ -776,7 +777,7 @@ def _kv_book(dev: int, page_table, kv_len, refcount, page_size, n_pairs, workspa
     tp, ld, cols, S = _table(page_table, dev)
     N = refcount.numel()
     b = _KV_BOOK.pack(tp, ld, _i32(kv_len, "kv_len", dev, S), S, _i32(refcount, "refcount", dev, N), N, cols, page_size)
-    return b, S, *_kv_workspace(lib.nm_kv_pages_workspace_bytes(S, n_pairs, N), page_table, workspace)
+    return b, S, *_kv_workspace(lib.nm_kv_pages_workspace_bytes(S, n_pairs, N, cols), page_table, workspace)
 
 
 def nm_kv_resize(new_len: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, refcount: torch.Tensor,

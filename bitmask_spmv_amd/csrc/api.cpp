@@ -879,11 +879,12 @@ nm_status nm_kv4_unpack(const nm_kv4_batch *batch, const nm_kv4_rows *k, const n
     }
 }
 
-size_t nm_kv4_attention_workspace_bytes(int64_t T, int64_t S, int n_heads, int n_kv, int head_dim, int64_t max_q_len) {
+size_t nm_kv4_attention_workspace_bytes(int64_t T, int64_t S, int n_heads, int n_kv, int head_dim, int64_t max_q_len,
+                                        int64_t room) {
     if (T < 0 || T > (1 << 24) || S < 0 || S > (1 << 20) || n_kv < 1 || n_kv > 256 || n_heads < 1 || n_heads > 1024 ||
-        n_heads % n_kv || (head_dim != 64 && head_dim != 128) || max_q_len < 1)
+        n_heads % n_kv || (head_dim != 64 && head_dim != 128) || max_q_len < 1 || room < 1)
         return 0;
-    return nmk::kv4_attention_workspace(T, S, n_heads, n_kv, head_dim, max_q_len);
+    return nmk::kv4_attention_workspace(T, S, n_heads, n_kv, head_dim, room);
 }
 
 nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int n_heads, int64_t max_q_len, float scale,
@@ -908,7 +909,7 @@ nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int 
         if (st != NM_OK) return st;
         if (lse && ld_lse < n_heads) return fail(NM_ERR_SHAPE, "%s: ld_lse=%lld", who, (long long)ld_lse);
         if (!aligned(lse, 4)) return fail(NM_ERR_ALIGN, "%s: lse needs 4-byte alignment", who);
-        const size_t need = nmk::kv4_attention_workspace(T, S, n_heads, n_kv, head_dim, max_q_len);
+        const size_t need = nmk::kv4_attention_workspace(T, S, n_heads, n_kv, head_dim, (int64_t)a.b.cols * a.b.f.page);
         if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
             return fail(NM_ERR_WORKSPACE, "%s: 16-byte aligned workspace of %zu bytes required, %zu given", who, need,
                         workspace ? workspace_bytes : (size_t)0);
@@ -939,8 +940,8 @@ static nm_status kv_book(const char *who, const nm_kv_book *p, const void *list,
     if (!aligned(p->page_table, 4) || !aligned(p->kv_len, 4) || !aligned(p->refcount, 4) || !aligned(list, 4) ||
         !aligned(moves, 4) || !aligned(count, 4))
         return fail(NM_ERR_ALIGN, "%s: 4-byte alignment needed", who);
-    const size_t need = nmk::kv_pages_workspace(n > p->S ? n : p->S, p->num_pages);
-    if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
+    const size_t need = nmk::kv_pages_workspace(p->S, n, p->num_pages, p->table_cols);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
         return fail(NM_ERR_WORKSPACE, "%s: 16-byte aligned workspace of %zu bytes required, %zu given", who, need,
                     workspace ? workspace_bytes : (size_t)0);
     b.table = p->page_table;
@@ -954,9 +955,11 @@ static nm_status kv_book(const char *who, const nm_kv_book *p, const void *list,
     return NM_OK;
 }
 
-size_t nm_kv_pages_workspace_bytes(int64_t S, int64_t n_pairs, int64_t num_pages) {
-    if (S < 1 || S > (1 << 20) || n_pairs < 0 || n_pairs > (1 << 20) || num_pages < 1 || num_pages > kMaxDim) return 0;
-    return nmk::kv_pages_workspace(n_pairs > S ? n_pairs : S, num_pages);
+size_t nm_kv_pages_workspace_bytes(int64_t S, int64_t n_pairs, int64_t num_pages, int table_cols) {
+    if (S < 1 || S > (1 << 20) || n_pairs < 0 || n_pairs > (1 << 20) || num_pages < 1 || num_pages > kMaxDim ||
+        table_cols < 1)
+        return 0;
+    return nmk::kv_pages_workspace(S, n_pairs, num_pages, table_cols);
 }
 
 nm_status nm_kv_fork(const nm_kv_book *book, const int32_t *parent, const int32_t *child, int64_t n, int32_t *moves,

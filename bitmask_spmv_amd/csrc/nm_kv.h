@@ -67,7 +67,7 @@ struct Kv4Attention {
 
 hipError_t launch_kv4_append(const Kv4Batch &b, const Kv4Rows &k, const Kv4Rows &v, hipStream_t st);
 hipError_t launch_kv4_unpack(const Kv4Batch &b, const Kv4Rows &k, const Kv4Rows &v, hipStream_t st);
-size_t kv4_attention_workspace(int64_t T, int64_t S, int heads, int n_kv, int dim, int64_t max_q);
+size_t kv4_attention_workspace(int64_t T, int64_t S, int heads, int n_kv, int dim, int64_t room);
 hipError_t launch_kv4_attention(const Kv4Attention &a, int64_t max_q, void *ws, hipStream_t st);
 
 // Page keeping.  Tables int32 [S][ld], lengths int32 [S], reference counts int32 [N].
@@ -81,7 +81,7 @@ struct KvBook {
     int N = 0;
     int page = 64;
 };
-size_t kv_pages_workspace(int64_t requests, int64_t num_pages);
+size_t kv_pages_workspace(int64_t S, int64_t n_pairs, int64_t num_pages, int64_t cols);
 hipError_t launch_kv_fork(const KvBook &b, const int32_t *parent, const int32_t *child, int n, int32_t *moves,
                           int32_t *missing, void *ws, hipStream_t st);
 hipError_t launch_kv_resize(const KvBook &b, const int32_t *new_len, int32_t *moves, int32_t *missing, void *ws,

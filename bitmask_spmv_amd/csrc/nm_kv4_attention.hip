@@ -1052,6 +1052,13 @@ size_t decode_workspace(int groups) {
     return (size_t)groups * 2 * (sizeof(Part<D>) + sizeof(PartTag));
 }
 
+// Few and short: a workgroup to each row tile (sequence s has none but its own of
+// q_start[s] * group / rows + s on, so their number is bounded), nothing to join.
+int64_t whole_tiles(int64_t T, int64_t S, int heads, int n_kv) { return (T * (heads / n_kv) / kRows + S) * n_kv; }
+bool whole(int64_t tiles, int groups, int64_t room) {
+    return tiles <= groups && room <= (4 * tiles < groups ? kWholeTokens : 2 * kWholeTokens);
+}
+
 template <int D>
 hipError_t launch(Kv4Attention a, int64_t max_q, void *ws, hipStream_t st) {
     const int group = a.heads / a.b.f.n_kv;
@@ -1065,11 +1072,8 @@ hipError_t launch(Kv4Attention a, int64_t max_q, void *ws, hipStream_t st) {
     const int groups = device_cus() * kGroupsPerCu;
     Part<D> *parts = (Part<D> *)ws;
     PartTag *tags = (PartTag *)(parts + 2 * (size_t)groups);
-    // Few and short: a workgroup to each row tile (sequence s has none but its own of
-    // q_start[s] * group / rows + s on, so their number is bounded), nothing to join.
-    const int64_t tiles = ((int64_t)a.b.T * group / kRows + a.b.S) * a.b.f.n_kv;
-    const int64_t longest = (int64_t)a.b.cols * a.b.f.page;
-    a.whole = tiles <= groups && longest <= (4 * tiles < groups ? kWholeTokens : 2 * kWholeTokens);
+    const int64_t tiles = whole_tiles(a.b.T, a.b.S, a.heads, a.b.f.n_kv);
+    a.whole = whole(tiles, groups, (int64_t)a.b.cols * a.b.f.page);
     const int grid = a.whole ? (int)tiles : groups;
     if (max_q * group <= kRows)
         kv4_decode_kernel<D, true><<<grid, kWaves * kWave, 0, st>>>(a, parts, tags);
@@ -1081,8 +1085,9 @@ hipError_t launch(Kv4Attention a, int64_t max_q, void *ws, hipStream_t st) {
 
 }  // namespace
 
-size_t kv4_attention_workspace(int64_t, int64_t, int, int, int dim, int64_t) {
+size_t kv4_attention_workspace(int64_t T, int64_t S, int heads, int n_kv, int dim, int64_t room) {
     const int groups = device_cus() * kGroupsPerCu;
+    if (whole(whole_tiles(T, S, heads, n_kv), groups, room)) return 0;
     return dim == 128 ? decode_workspace<128>(groups) : decode_workspace<64>(groups);
 }
 

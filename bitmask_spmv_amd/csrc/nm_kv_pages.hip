@@ -9,8 +9,8 @@
 // Steps of fork and resize: pages given back; free pages counted, beside them the prefix
 // sums of what is asked; pages handed out -- the free page of rank k goes to the request
 // whose share of the prefix sums holds k.  Small pools and few requests go through all
-// steps in one workgroup (one launch: 6-8 us; three launches: 14-20 us); larger ones take a
-// launch for each step, a workgroup to each 4096 pages.
+// steps in one workgroup and need no workspace (one launch: 4-9 us; three launches: 12-17 us);
+// larger ones take a launch for each step, a workgroup to each 4096 pages.
 #include "nm_device.h"
 #include "nm_kv.h"
 
@@ -22,7 +22,7 @@ constexpr int kWavesPerGroup = kThreads / kWave;
 constexpr int kChunk = 4096;         // pages per workgroup: 64 words of 64
 constexpr int kSmallPages = 16384;   // one workgroup: 256 words of 64 pages in LDS,
 constexpr int kSmallRequests = 64;   // pairs, a wave to each in turn (4: 9 us against 13; 224: 64 us against 14),
-constexpr int kSmallRows = 256;      // table rows, a wave to each in turn,
+constexpr int kSmallRows = 256;      // sequences, a thread to each and a wave to their rows in turn,
 constexpr int kSmallEntries = 65536; // and their entries
 constexpr int kPrefixLds = 4096;     // requests whose prefix sums a workgroup searches in LDS
 
@@ -639,6 +639,11 @@ __global__ __launch_bounds__(kCopyThreads) void copy_pages_kernel(uint8_t *cache
     }
 }
 
+// Whether one workgroup takes an operator; n: pairs of a fork.
+bool small(int64_t N, int64_t S, int64_t n, int64_t cols) {
+    return N <= kSmallPages && S <= kSmallRows && n <= kSmallRequests && (S > n ? S : n) * cols <= kSmallEntries;
+}
+
 size_t compact_base(int64_t N) {
     const int64_t chunks = chunks_of(N);
     return (size_t)(chunks * 64 * 8 + ((chunks * 4 + 15) & ~(int64_t)15));
@@ -646,7 +651,9 @@ size_t compact_base(int64_t N) {
 
 }  // namespace
 
-size_t kv_pages_workspace(int64_t requests, int64_t num_pages) {
+size_t kv_pages_workspace(int64_t S, int64_t n_pairs, int64_t num_pages, int64_t cols) {
+    if (small(num_pages, S, n_pairs, cols)) return 0;
+    const int64_t requests = n_pairs > S ? n_pairs : S;
     const size_t chunks = (size_t)chunks_of(num_pages);
     const size_t ask = chunks * 64 * 8 + (size_t)requests * sizeof(Request) + chunks * 4 + (size_t)requests * 8;
     const size_t compact = compact_base(num_pages) + (size_t)num_pages * 4;
@@ -655,7 +662,7 @@ size_t kv_pages_workspace(int64_t requests, int64_t num_pages) {
 
 hipError_t launch_kv_fork(const KvBook &b, const int32_t *parent, const int32_t *child, int n, int32_t *moves,
                           int32_t *missing, void *ws, hipStream_t st) {
-    if (b.N <= kSmallPages && n <= kSmallRequests && (int64_t)n * b.cols <= kSmallEntries) {
+    if (small(b.N, b.S, n, b.cols)) {
         fork_small_kernel<<<1, kThreads, 0, st>>>(b, parent, child, n, moves, missing);
         return hipGetLastError();
     }
@@ -670,7 +677,7 @@ hipError_t launch_kv_fork(const KvBook &b, const int32_t *parent, const int32_t 
 
 hipError_t launch_kv_resize(const KvBook &b, const int32_t *new_len, int32_t *moves, int32_t *missing, void *ws,
                             hipStream_t st) {
-    if (b.N <= kSmallPages && b.S <= kThreads && (int64_t)b.S * b.cols <= kSmallEntries) {
+    if (small(b.N, b.S, 0, b.cols)) {
         resize_small_kernel<<<1, kThreads, 0, st>>>(b, new_len, moves, missing);
         return hipGetLastError();
     }
@@ -683,7 +690,7 @@ hipError_t launch_kv_resize(const KvBook &b, const int32_t *new_len, int32_t *mo
 }
 
 hipError_t launch_kv_compact(const KvBook &b, int32_t *moves, int cap, int32_t *used, void *ws, hipStream_t st) {
-    if (b.N <= kSmallPages && b.S <= kSmallRows && (int64_t)b.S * b.cols <= kSmallEntries) {
+    if (small(b.N, b.S, 0, b.cols)) {
         compact_small_kernel<<<1, kThreads, 0, st>>>(b, moves, cap, used);
         return hipGetLastError();
     }

@@ -438,7 +438,8 @@ nm_status nm_stream_read(const void *buf, size_t bytes, uint32_t *sink, size_t s
  * result is rounded once to bf16.  max_q_len >= 1 is a hint (the largest number of rows of a
  * sequence) that the choice of kernels goes by; a wrong one costs time only.  Cached values
  * must be finite in the places that are looked at; what masked places, other pages and the
- * rest of a page hold does not matter.  Workspace: nm_kv4_attention_workspace_bytes, 16-byte aligned;
+ * rest of a page hold does not matter.  Workspace: nm_kv4_attention_workspace_bytes, 16-byte aligned
+ * (room = table_cols * page_size: contexts that all fit in 1024 tokens, for instance, may need none);
  * calls that may overlap in time need workspaces of their own.
  */
 typedef struct {
@@ -458,7 +459,8 @@ typedef struct {
 int64_t nm_kv4_page_bytes(int page_size, int n_kv, int head_dim); /* 0 for sizes that are refused */
 nm_status nm_kv4_append(const nm_kv4_batch *batch, const nm_kv4_rows *k, const nm_kv4_rows *v, void *hip_stream);
 nm_status nm_kv4_unpack(const nm_kv4_batch *batch, const nm_kv4_rows *k, const nm_kv4_rows *v, void *hip_stream);
-size_t nm_kv4_attention_workspace_bytes(int64_t T, int64_t S, int n_heads, int n_kv, int head_dim, int64_t max_q_len);
+size_t nm_kv4_attention_workspace_bytes(int64_t T, int64_t S, int n_heads, int n_kv, int head_dim, int64_t max_q_len,
+                                        int64_t room);
 nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int n_heads, int64_t max_q_len, float scale,
                            int64_t window, const nm_kv4_rows *out, float *lse, int64_t ld_lse, void *workspace,
                            size_t workspace_bytes, void *hip_stream);
@@ -469,8 +471,8 @@ nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int 
  * hold it, 0 = free.  One table serves the caches of all layers.  Free pages are
  * handed out lowest number first, in the order of the requests, so a result depends on the
  * state and the arguments alone.  S * table_cols and num_pages <= 2^30, pairs <= 2^20, moves <= 2^29.  Workspace for all
- * three: nm_kv_pages_workspace_bytes(S, n_pairs, num_pages), 16-byte aligned (n_pairs 0
- * where there is no fork).
+ * three: nm_kv_pages_workspace_bytes(S, n_pairs, num_pages, table_cols), 16-byte aligned (n_pairs
+ * 0 where there is no fork; small pools need none).
  *
  * moves int32 [..][2] receives pairs (from, to) of pages whose bytes the caller has
  * nm_kv_copy_pages copy in every cache before the pages are read or written; pairs without
@@ -510,7 +512,7 @@ typedef struct {
     int64_t num_pages;
     int table_cols, page_size;
 } nm_kv_book;
-size_t nm_kv_pages_workspace_bytes(int64_t S, int64_t n_pairs, int64_t num_pages);
+size_t nm_kv_pages_workspace_bytes(int64_t S, int64_t n_pairs, int64_t num_pages, int table_cols);
 nm_status nm_kv_resize(const nm_kv_book *book, const int32_t *new_len, int32_t *moves, int32_t *missing,
                        void *workspace, size_t workspace_bytes, void *hip_stream);
 nm_status nm_kv_fork(const nm_kv_book *book, const int32_t *parent, const int32_t *child, int64_t n, int32_t *moves,

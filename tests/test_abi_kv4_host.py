@@ -14,11 +14,11 @@ ODD = 0x10001
 HALF = 0x10008
 
 i64, p, i32, sz, f32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
-BATCH = [("cache", p, A), ("num_pages", i64, 4), ("page_table", p, A), ("ld_table", i64, 8), ("kv_len", p, A),
-         ("q_start", p, A), ("S", i64, 3), ("T", i64, 5), ("table_cols", i32, 8), ("page_size", i32, 64), ("n_kv", i32, 2),
+BATCH = [("cache", p, A), ("num_pages", i64, 4), ("page_table", p, A), ("ld_table", i64, 80), ("kv_len", p, A),
+         ("q_start", p, A), ("S", i64, 3), ("T", i64, 5), ("table_cols", i32, 80), ("page_size", i32, 64), ("n_kv", i32, 2),
          ("head_dim", i32, 128)]
 BOOK = [("page_table", p, A), ("ld_table", i64, 8), ("kv_len", p, A), ("S", i64, 3), ("refcount", p, A),
-        ("num_pages", i64, 40), ("table_cols", i32, 8), ("page_size", i32, 64)]
+        ("num_pages", i64, 40000), ("table_cols", i32, 8), ("page_size", i32, 64)]
 WS = [("workspace", p, A), ("workspace_bytes", sz, 1 << 40), ("stream", p, None)]
 
 
@@ -51,9 +51,9 @@ def L():
     for name, args in CALLS.items():
         getattr(lib, name).argtypes = [p if len(a) == 2 else a[1] for a in args]
     lib.nm_kv4_page_bytes.argtypes, lib.nm_kv4_page_bytes.restype = [i32] * 3, i64
-    lib.nm_kv4_attention_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i64]
+    lib.nm_kv4_attention_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i64, i64]
     lib.nm_kv4_attention_workspace_bytes.restype = sz
-    lib.nm_kv_pages_workspace_bytes.argtypes, lib.nm_kv_pages_workspace_bytes.restype = [i64] * 3, sz
+    lib.nm_kv_pages_workspace_bytes.argtypes, lib.nm_kv_pages_workspace_bytes.restype = [i64, i64, i64, i32], sz
     return lib
 
 
@@ -96,7 +96,7 @@ def test_null_pointers_and_odd_addresses(L, name):
             continue
         st = call(L, name, **{arg: None})
         if arg == "workspace":
-            need = L.nm_kv4_attention_workspace_bytes(5, 3, 8, 2, 128, 1) if name == "nm_kv4_attention" else 1
+            need = L.nm_kv4_attention_workspace_bytes(5, 3, 8, 2, 128, 1, 80 * 64) if name == "nm_kv4_attention" else 1
             if need:
                 assert st == WORKSPACE, arg
                 assert call(L, name, workspace=HALF) == WORKSPACE
@@ -162,8 +162,14 @@ def test_size_queries(L):
     assert L.nm_kv4_page_bytes(512, 1, 64) == 512 * 2 * 34
     for bad in ((0, 8, 128), (48, 8, 128), (64, 0, 128), (64, 8, 80), (64, 300, 128)):
         assert L.nm_kv4_page_bytes(*bad) == 0
-    for bad in ((-1, 1, 8, 2, 128, 1), (5, 3, 7, 2, 128, 1), (5, 3, 8, 2, 96, 1), (5, 3, 8, 2, 128, 0)):
+    assert L.nm_kv4_attention_workspace_bytes(5, 3, 8, 2, 128, 1, 4096) > 0
+    assert L.nm_kv4_attention_workspace_bytes(5, 3, 8, 2, 128, 1, 1024) == 0  # one workgroup to each row tile
+    for bad in ((-1, 1, 8, 2, 128, 1, 4096), (5, 3, 7, 2, 128, 1, 4096), (5, 3, 8, 2, 96, 1, 4096),
+                (5, 3, 8, 2, 128, 0, 4096), (5, 3, 8, 2, 128, 1, 0)):
         assert L.nm_kv4_attention_workspace_bytes(*bad) == 0
-    assert L.nm_kv_pages_workspace_bytes(0, 0, 5) == 0 and L.nm_kv_pages_workspace_bytes(1, 0, 0) == 0
-    assert L.nm_kv_pages_workspace_bytes(1, 0, 1) > 0
-    assert L.nm_kv_pages_workspace_bytes(4, 100, 5000) >= L.nm_kv_pages_workspace_bytes(4, 0, 5000)
+    for bad in ((0, 0, 5, 1), (1, 0, 0, 1), (1, -1, 5, 1), (1, 0, 5, 0)):
+        assert L.nm_kv_pages_workspace_bytes(*bad) == 0
+    assert L.nm_kv_pages_workspace_bytes(8, 8, 4096, 64) == 0  # one workgroup
+    for big in ((8, 8, 16385, 64), (257, 0, 100, 4), (8, 65, 100, 4), (256, 0, 100, 257)):
+        assert L.nm_kv_pages_workspace_bytes(*big) > 0
+    assert L.nm_kv_pages_workspace_bytes(4, 100, 50000, 8) >= L.nm_kv_pages_workspace_bytes(4, 0, 50000, 8)

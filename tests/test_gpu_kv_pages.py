@@ -62,7 +62,7 @@ class Pool:
         return md
 
 
-@pytest.mark.parametrize("N,S,ps", [(10, 4, 64), (64, 9, 128), (4096, 40, 64), (4097, 300, 64), (16384, 1024, 64),
+@pytest.mark.parametrize("N,S,ps", [(10, 4, 64), (64, 9, 128), (4096, 40, 64), (4097, 300, 64), (16384, 1024, 64), (16384, 256, 64), (5000, 190, 256),
                                     (16385, 30, 64), (20000, 700, 512), (40000, 1100, 128)])
 def test_a_long_run_of_operators(N, S, ps):
     """Random growth, truncation, forks (some of them refused) and compaction, the pool short at times."""
