@@ -3,6 +3,7 @@
 // first HIP call, so invalid calls never touch the GPU.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -900,6 +901,9 @@ nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int 
         const int64_t T = a.b.T, S = a.b.S;
         if (n_heads < 1 || n_heads > 1024 || n_heads % n_kv)
             return fail(NM_ERR_SHAPE, "%s: %d query heads are not a multiple of %d key/value heads", who, n_heads, n_kv);
+        if (T * (n_heads / n_kv) > kMaxDim)
+            return fail(NM_ERR_SHAPE, "%s: T=%lld rows of %d heads share a key/value head: more than 2^30", who,
+                        (long long)T, n_heads / n_kv);
         if (window < 0 || max_q_len < 1)
             return fail(NM_ERR_SHAPE, "%s: window=%lld max_q_len=%lld", who, (long long)window, (long long)max_q_len);
         if (!(scale - scale == 0.f)) return fail(NM_ERR_SHAPE, "%s: scale is not finite", who);
@@ -917,7 +921,7 @@ nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int 
         a.ld_lse = ld_lse;
         a.heads = n_heads;
         a.scale = scale;
-        a.window = window;
+        a.window = std::min(window, (int64_t)1 << 40);  // longer than any sequence
         hipError_t e = nmk::launch_kv4_attention(a, max_q_len, workspace, (hipStream_t)hip_stream);
         return e == hipSuccess ? NM_OK : hip_fail(who, e);
     } catch (...) {
@@ -956,7 +960,7 @@ static nm_status kv_book(const char *who, const nm_kv_book *p, const void *list,
 }
 
 size_t nm_kv_pages_workspace_bytes(int64_t S, int64_t n_pairs, int64_t num_pages, int table_cols) {
-    if (S < 1 || S > (1 << 20) || n_pairs < 0 || n_pairs > (1 << 20) || num_pages < 1 || num_pages > kMaxDim ||
+    if (S < 1 || S > (1 << 20) || n_pairs < 0 || n_pairs > (1 << 16) || num_pages < 1 || num_pages > kMaxDim ||
         table_cols < 1)
         return 0;
     return nmk::kv_pages_workspace(S, n_pairs, num_pages, table_cols);
@@ -968,7 +972,7 @@ nm_status nm_kv_fork(const nm_kv_book *book, const int32_t *parent, const int32_
         g_err[0] = 0;
         const char *who = "nm_kv_fork";
         if (!parent) return fail(NM_ERR_NULL, "%s: NULL pointer", who);
-        if (n < 1 || n > (1 << 20)) return fail(NM_ERR_SHAPE, "%s: n=%lld out of range [1, 2^20]", who, (long long)n);
+        if (n < 1 || n > (1 << 16)) return fail(NM_ERR_SHAPE, "%s: n=%lld out of range [1, 2^16]", who, (long long)n);
         if (!aligned(parent, 4)) return fail(NM_ERR_ALIGN, "%s: 4-byte alignment needed", who);
         nmk::KvBook b;
         nm_status st = kv_book(who, book, child, n, moves, missing, workspace, workspace_bytes, b);

@@ -100,8 +100,48 @@ __device__ __forceinline__ uint32_t fp4_pair(uint32_t w, float s, int byte) {
 // most 2^-20 of that, and nothing of numbers within 2^-8 of it.  The instruction aligns the products of 8
 // neighbouring channels to about 13 bits below the largest of them: those of 4-bit and 6-bit
 // numbers always fit, those of 4-bit and 8-bit (E4M3) ones do not (two 8-bit pieces, at the
-// same matrix time, were measured 2^-17 of |q| |k| off).  At dim 64 the instruction's upper
-// 64 channels multiply the same keys again: lanes 32.. hold the second and fourth piece.
+// same matrix time, were measured 2^-17 of |q| |k| off).  Of a block with an infinity or NaN the
+// scales are NaN, and so is what its row gets.  `at`: the pieces' scales, a byte each.
+struct Pieces {
+    u32x6 p[4];
+    uint32_t at[4];
+};
+
+__device__ __forceinline__ Pieces split_query(const uint16_t *from, bool real, float scale) {
+    union { u32x4 u[4]; uint32_t w[16]; bf16x32 h; } x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x.u[i] = real ? *reinterpret_cast<const u32x4 *>(from + i * 8) : (u32x4){0, 0, 0, 0};
+    const uint32_t signs = scale < 0.f ? 0x80008000u : 0u;
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        top = max(top, max(x.w[i] & 0x7FFFu, (x.w[i] >> 16) & 0x7FFFu));
+        x.w[i] ^= signs;
+    }
+    const uint32_t e = max(top >> 7, 20u);  // biased exponent of the largest magnitude
+    Pieces q;
+    q.at[0] = e - 2;
+    q.at[1] = e - 6;
+    q.at[2] = e - 11;
+    q.at[3] = e - 16;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float s = pow2_byte(q.at[k]);
+        q.p[k] = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(x.h, s);
+        if (k < 3) {  // what is left is a bf16 number: the bits that the piece did not take
+            const f32x32 d = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(q.p[k], s);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                x.w[i] = pack_bf16(bf16_lo(x.w[i]) - d[2 * i], bf16_hi(x.w[i]) - d[2 * i + 1]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) q.at[k] = e == 255u ? 255u : q.at[k];
+    return q;
+}
+
+// The pieces of a decode tile's row.  At dim 64 the instruction's upper 64 channels multiply the
+// same keys again: lanes 32.. hold the second and fourth piece.
 template <int D>
 struct Query {
     static constexpr int kSteps = D / 32;
@@ -111,41 +151,16 @@ struct Query {
 
 template <int D>
 __device__ __forceinline__ Query<D> load_query(const uint16_t *row, bool real, float scale, int g) {
-    union { u32x4 u[4]; uint32_t w[16]; bf16x32 h; } x;
-    const int block = D == 128 ? g : (g & 1);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        x.u[i] = real ? *reinterpret_cast<const u32x4 *>(row + block * 32 + i * 8) : (u32x4){0, 0, 0, 0};
-    const uint32_t signs = scale < 0.f ? 0x80008000u : 0u;
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        top = max(top, max(x.w[i] & 0x7FFFu, (x.w[i] >> 16) & 0x7FFFu));
-        x.w[i] ^= signs;
-    }
-    const uint32_t e = max(top >> 7, 20u);  // biased exponent of the largest magnitude
-    const uint32_t at[4] = {e - 2, e - 6, e - 11, e - 16};
-    u32x6 p[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float s = pow2_byte(at[k]);
-        p[k] = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(x.h, s);
-        if (k < 3) {  // what is left is a bf16 number: the bits that the piece did not take
-            const f32x32 d = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(p[k], s);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                x.w[i] = pack_bf16(bf16_lo(x.w[i]) - d[2 * i], bf16_hi(x.w[i]) - d[2 * i + 1]);
-        }
-    }
+    const Pieces x = split_query(row + (D == 128 ? g : (g & 1)) * 32, real, scale);
     Query<D> q;
     if constexpr (D == 128) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) q.p[k] = p[k];
-        q.scales = at[0] | at[1] << 8 | at[2] << 16 | at[3] << 24;
+        for (int k = 0; k < 4; ++k) q.p[k] = x.p[k];
+        q.scales = x.at[0] | x.at[1] << 8 | x.at[2] << 16 | x.at[3] << 24;
     } else {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) q.p[k] = g < 2 ? p[2 * k] : p[2 * k + 1];
-        q.scales = g < 2 ? at[0] | at[2] << 8 : at[1] | at[3] << 8;
+        for (int k = 0; k < 2; ++k) q.p[k] = g < 2 ? x.p[2 * k] : x.p[2 * k + 1];
+        q.scales = g < 2 ? x.at[0] | x.at[2] << 8 : x.at[1] | x.at[3] << 8;
     }
     return q;
 }
@@ -405,7 +420,7 @@ __device__ __forceinline__ void add_values(Tile<D> &t, const Bytes<D> &x, const 
 template <int D>
 __device__ __forceinline__ void store_row(const Kv4Attention &a, int t, int h, int g, const float *o, float m, float l,
                                           bool with_lse) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
     uint16_t *p = a.out.p + t * a.out.ld + h * a.out.hd + g * (D / 4);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
@@ -414,7 +429,7 @@ __device__ __forceinline__ void store_row(const Kv4Attention &a, int t, int h, i
         for (int j = 0; j < 4; ++j) w[j] = pack_bf16(o[8 * i + 2 * j] * inv, o[8 * i + 2 * j + 1] * inv);
         *reinterpret_cast<u32x4 *>(p + 8 * i) = w;
     }
-    if (with_lse && a.lse) a.lse[t * a.ld_lse + h] = l > 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    if (with_lse && a.lse) a.lse[t * a.ld_lse + h] = l != 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
 // Pieces of rows cut between waves (LDS) or workgroups (workspace): unnormalised O by
@@ -488,12 +503,12 @@ struct Join {
         if (row >= tag.rows) return;
         const int r = tag.tile * kRows + row;
         const int t = tag.q0 + r / group, h = tag.head * group + r % group;
-        if (t >= a.b.T) return;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        if ((uint32_t)t >= (uint32_t)a.b.T) return;
+        const float inv = l != 0.f ? 1.f / l : 0.f;
         uint32_t *p = reinterpret_cast<uint32_t *>(a.out.p + t * a.out.ld + h * a.out.hd + c * N);
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) p[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
-        if (c == 0 && a.lse) a.lse[t * a.ld_lse + h] = l > 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+        if (c == 0 && a.lse) a.lse[t * a.ld_lse + h] = l != 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
     }
 };
 
@@ -573,7 +588,7 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attenti
         // queries of my column
         const int64_t r = (int64_t)tile * kRows + ln.col;
         const int qi = (int)r / group, t = sq.q0 + qi, h = head * group + ((int)r - qi * group);
-        const bool real = r < (int64_t)sq.n * group && t < a.b.T;
+        const bool real = r < (int64_t)sq.n * group && (uint32_t)t < (uint32_t)a.b.T;
         const Query<D> q = load_query<D>(a.q.p + t * a.q.ld + h * a.q.hd, real, a.scale, ln.g);
         // keys that my row sees: [from, upto]
         const int64_t place = (int64_t)sq.len - sq.n + qi;
@@ -729,33 +744,6 @@ struct PromptQuery {
     uint32_t scales[D / 64];  // a byte for each piece
 };
 
-template <int D>
-__device__ __forceinline__ void split_query(u32x4 (&x4)[4], uint32_t signs, u32x6 (&p)[4], uint32_t &scales) {
-    union { u32x4 u[4]; uint32_t w[16]; bf16x32 h; } x;
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x.u[i] = x4[i];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        top = max(top, max(x.w[i] & 0x7FFFu, (x.w[i] >> 16) & 0x7FFFu));
-        x.w[i] ^= signs;
-    }
-    const uint32_t e = max(top >> 7, 20u);  // biased exponent of the largest magnitude
-    const uint32_t at[4] = {e - 2, e - 6, e - 11, e - 16};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float s = pow2_byte(at[k]);
-        p[k] = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(x.h, s);
-        if (k < 3) {  // what is left is a bf16 number: the bits that the piece did not take
-            const f32x32 d = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(p[k], s);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                x.w[i] = pack_bf16(bf16_lo(x.w[i]) - d[2 * i], bf16_hi(x.w[i]) - d[2 * i + 1]);
-        }
-    }
-    scales = at[0] | at[1] << 8 | at[2] << 16 | at[3] << 24;
-}
-
 __device__ __forceinline__ float halves_max(float v) {
     const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
@@ -804,15 +792,14 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
     const int64_t w0 = r0 + wave * kPromptTile;  // the wave's first row
     const int64_t r = w0 + col;
     const int qi = (int)(r / group), t = q0 + qi, h = head * group + (int)(r - (int64_t)qi * group);
-    const bool real = r < rows && t < a.b.T;
+    const bool real = r < rows && (uint32_t)t < (uint32_t)a.b.T;
     PromptQuery<D> q;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-        u32x4 x[4];
-        const uint16_t *p = a.q.p + t * a.q.ld + h * a.q.hd + k * 64 + hh * 32;
+        const Pieces x = split_query(a.q.p + t * a.q.ld + h * a.q.hd + k * 64 + hh * 32, real, a.scale);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = real ? reinterpret_cast<const u32x4 *>(p)[i] : (u32x4){0, 0, 0, 0};
-        split_query<D>(x, a.scale < 0.f ? 0x80008000u : 0u, q.p[k], q.scales[k]);
+        for (int i = 0; i < 4; ++i) q.p[k][i] = x.p[i];
+        q.scales[k] = x.at[0] | x.at[1] << 8 | x.at[2] << 16 | x.at[3] << 24;
     }
     const int64_t place = place0 + qi;
     const int upto = real ? (int)(place < cap ? place : cap - 1) : -1;
@@ -1010,7 +997,7 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
     }
     l = halves_sum(l);
     if (!real) return;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
     uint16_t *out = a.out.p + t * a.out.ld + h * a.out.hd;
     // the lane's rows m = 8 i + 4 hh + j of every channel tile
 #pragma unroll
@@ -1028,7 +1015,7 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
             }
             *reinterpret_cast<u32x4 *>(out + (8 * i + 4 * hh + j) * 8) = w;
         }
-    if (hh == 0 && a.lse) a.lse[t * a.ld_lse + h] = l > 0.f ? (reference(m, c) + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    if (hh == 0 && a.lse) a.lse[t * a.ld_lse + h] = l != 0.f ? (reference(m, c) + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
 int device_cus() {

@@ -425,7 +425,7 @@ nm_status nm_stream_read(const void *buf, size_t bytes, uint32_t *sink, size_t s
  * exponent of the largest magnitude a and m its significand in [1, 2):
  *     e = min(max(E - 2 + (m > 1.75), 16), 252);
  * values are rounded to the nearest E2M1 multiple of 2^(e - 127), ties to the even code,
- * magnitudes above 6 to 6.  Two rows of one call at the same place (a page shared by two
+ * magnitudes above 6 to 6; an infinity or NaN is kept as 6 * 2^125 with its sign.  Two rows of one call at the same place (a page shared by two
  * sequences: see nm_kv_resize) leave one of the two there, token by token and head by head.
  *
  * nm_kv4_unpack -- the same rows of the cache as bf16 (exact).
@@ -437,8 +437,9 @@ nm_status nm_stream_read(const void *buf, size_t bytes, uint32_t *sink, size_t s
  * NULL.  out must not overlap q.  Scores, maxima, sums and outputs are kept in fp32, the
  * result is rounded once to bf16.  max_q_len >= 1 is a hint (the largest number of rows of a
  * sequence) that the choice of kernels goes by; a wrong one costs time only.  Cached values
- * must be finite in the places that are looked at; what masked places, other pages and the
- * rest of a page hold does not matter.  Workspace: nm_kv4_attention_workspace_bytes, 16-byte aligned
+ * must be finite in the places that are looked at (nm_kv4_append stores no others); what masked
+ * places, other pages and the rest of a page hold does not matter.  A query with an infinity or
+ * NaN among its channels gives NaN, in its own row and head alone.  T * n_heads / n_kv <= 2^30.  Workspace: nm_kv4_attention_workspace_bytes, 16-byte aligned
  * (room = table_cols * page_size: contexts that all fit in 1024 tokens, for instance, may need none);
  * calls that may overlap in time need workspaces of their own.
  */
@@ -470,7 +471,7 @@ nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int 
  * sequence's last page are -1), kv_len and a reference count per page: how many sequences
  * hold it, 0 = free.  One table serves the caches of all layers.  Free pages are
  * handed out lowest number first, in the order of the requests, so a result depends on the
- * state and the arguments alone.  S * table_cols and num_pages <= 2^30, pairs <= 2^20, moves <= 2^29.  Workspace for all
+ * state and the arguments alone.  S * table_cols and num_pages <= 2^30, pairs <= 2^16, moves <= 2^29.  Workspace for all
  * three: nm_kv_pages_workspace_bytes(S, n_pairs, num_pages, table_cols), 16-byte aligned (n_pairs
  * 0 where there is no fork; small pools need none).
  *

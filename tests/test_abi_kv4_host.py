@@ -126,7 +126,9 @@ def test_sizes_of_a_batch(L, name, bad):
     ("nm_kv4_attention", dict(scale=float("nan")), SHAPE), ("nm_kv4_attention", dict(scale=float("inf")), SHAPE),
     ("nm_kv4_attention", dict(ldo=100), SHAPE), ("nm_kv4_attention", dict(hdq=124), SHAPE),
     ("nm_kv4_attention", dict(hdo=129), ALIGN), ("nm_kv4_attention", dict(ld_lse=7), SHAPE),
-    ("nm_kv4_attention", dict(lse=0x10002), ALIGN)])
+    ("nm_kv4_attention", dict(lse=0x10002), ALIGN),
+    # rows of a key/value head are numbered in 32 bits
+    ("nm_kv4_attention", dict(T=(1 << 24) - 7, n_heads=256, n_kv=2, ldo=32768, ldq=32768, ld_lse=256), SHAPE)])
 def test_rows_heads_and_scales(L, name, bad, want):
     assert call(L, name, **bad) == want
 
@@ -141,7 +143,7 @@ def test_page_keeping(L, name, bad, want):
 
 
 @pytest.mark.parametrize("name,bad,want", [
-    ("nm_kv_fork", dict(n=0), SHAPE), ("nm_kv_fork", dict(n=(1 << 20) + 1), SHAPE), ("nm_kv_compact", dict(max_moves=0), SHAPE),
+    ("nm_kv_fork", dict(n=0), SHAPE), ("nm_kv_fork", dict(n=(1 << 16) + 1), SHAPE), ("nm_kv_compact", dict(max_moves=0), SHAPE),
     ("nm_kv_compact", dict(max_moves=(1 << 29) + 1), SHAPE), ("nm_kv_copy_pages", dict(page_bytes=24), ALIGN),
     ("nm_kv_copy_pages", dict(page_bytes=0), SHAPE), ("nm_kv_copy_pages", dict(layers=0), SHAPE),
     ("nm_kv_copy_pages", dict(layer_stride=240), SHAPE), ("nm_kv_copy_pages", dict(layer_stride=264), ALIGN),
