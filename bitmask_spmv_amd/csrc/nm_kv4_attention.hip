@@ -320,10 +320,13 @@ struct Lane {
     }
 };
 
+// Cache bytes at an address put together from its halves: said to be global memory (a load that might be
+// from LDS as well counts among the LDS operations too, and waits for one would wait for it).
 // NT: bytes that are read once (one row tile per head) stay out of the caches' way.
 template <bool NT, class T>
 __device__ __forceinline__ T load_cache(const uint8_t *p) {
-    return NT ? __builtin_nontemporal_load(reinterpret_cast<const T *>(p)) : *reinterpret_cast<const T *>(p);
+    typedef const __attribute__((address_space(1))) T *Global;
+    return NT ? __builtin_nontemporal_load((Global)(uintptr_t)p) : *(Global)(uintptr_t)p;
 }
 
 template <int D, bool NT>
@@ -859,8 +862,8 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
         for (int k = 0; k < CH; ++k) {
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt)
-                kx[tt][k] = *reinterpret_cast<const u32x4 *>(kp + k_off + (tt * 16 * D + k * 32));
-            ks[k] = *reinterpret_cast<const uint32_t *>(sp + ks_off + k * 8);
+                kx[tt][k] = load_cache<false, u32x4>(kp + k_off + (tt * 16 * D + k * 32));
+            ks[k] = load_cache<false, uint32_t>(sp + ks_off + k * 8);
         }
     };
 
@@ -877,8 +880,8 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
         const uint8_t *kp = lies.at(b - held), *vp = kp + f.v_at(), *sp = kp + scales_at(f, b) + f.page * (D / 32);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            vx[i] = *reinterpret_cast<const u32x4 *>(vp + v_off + i * 4 * D);
-            vs[i] = *reinterpret_cast<const uint32_t *>(sp + vs_off + i * (D / 4));
+            vx[i] = load_cache<false, u32x4>(vp + v_off + i * 4 * D);
+            vs[i] = load_cache<false, uint32_t>(sp + vs_off + i * (D / 4));
         }
     };
     // a weight of 0 times what an unseen place holds must be 0
