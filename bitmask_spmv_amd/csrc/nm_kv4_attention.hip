@@ -107,10 +107,20 @@ struct Pieces {
     uint32_t at[4];
 };
 
-__device__ __forceinline__ Pieces split_query(const uint16_t *from, bool real, float scale) {
-    union { u32x4 u[4]; uint32_t w[16]; bf16x32 h; } x;
+union Channels {  // 32 of them
+    u32x4 u[4];
+    uint32_t w[16];
+    bf16x32 h;
+};
+
+__device__ __forceinline__ Channels read_query(const uint16_t *from, bool real) {
+    Channels x;
 #pragma unroll
     for (int i = 0; i < 4; ++i) x.u[i] = real ? *reinterpret_cast<const u32x4 *>(from + i * 8) : (u32x4){0, 0, 0, 0};
+    return x;
+}
+
+__device__ __forceinline__ Pieces split_query(Channels x, float scale) {
     const uint32_t signs = scale < 0.f ? 0x80008000u : 0u;
     uint32_t top = 0;
 #pragma unroll
@@ -151,7 +161,7 @@ struct Query {
 
 template <int D>
 __device__ __forceinline__ Query<D> load_query(const uint16_t *row, bool real, float scale, int g) {
-    const Pieces x = split_query(row + (D == 128 ? g : (g & 1)) * 32, real, scale);
+    const Pieces x = split_query(read_query(row + (D == 128 ? g : (g & 1)) * 32, real), scale);
     Query<D> q;
     if constexpr (D == 128) {
 #pragma unroll
@@ -755,6 +765,15 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attention a, const Par
 // from issuing for about 8 cycles whatever its size, and softmax needs that unit for
 // about as long as the matrix unit is busy (four vector instructions to every 16 x 16 x 32
 // product: 23.6 ns in 16 x 16 tiles, 18.9 ns in 32 x 32 ones; 15 ns without them).
+//
+// Both units run at once only where a wave alternates between them: a burst of products
+// keeps the other wave of the SIMD from issuing vector instructions (two halves of a workgroup that
+// took turns at products and softmax, a barrier between: 1250 cycles of products and 1200 of
+// softmax a block took 2500 together).  So the walk is a pipeline over tiles of 32 tokens, one step
+// of which has the products of three of them: see `step`.  A block takes 3760 cycles against 4110 for
+// scores, softmax and values one after the other; the clock falls by 4 % (2.14 GHz: the
+// card's power is the bound), so 3 prompts of up to 4K rows behind 2K take 464 us against 475, 455 GFLOP
+// at 980 TFLOP/s.
 constexpr int kPromptTile = 32;                       // rows of a wave
 constexpr int kPromptRows = kWaves * kPromptTile;     // rows of a workgroup
 
@@ -797,54 +816,47 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
     int s = 0;
     for (int n = a.b.S; n > 1;) {  // the last s whose first tile is at or before vt, 64 looks at a time
         const int step = (n + 63) >> 6, at = s + lane * step;
-        const bool yes = lane * step < n && (int64_t)a.b.q_start[at] * group / kPromptRows + at <= vt;
+        const bool yes = lane * step < n && (uint32_t)(a.b.q_start[at] * group) / kPromptRows + at <= (uint32_t)vt;
         const uint64_t m = __ballot(yes);
         s += (m ? 63 - __clzll((long long)m) : 0) * step;
         n = min(step, a.b.S - s);
     }
     const int q0 = uniform_load(a.b.q_start + s), n = uniform_load(a.b.q_start + s + 1) - q0;
     const int len = uniform_load(a.b.kv_len + s);
-    const int64_t rows = (int64_t)n * group;
+    const int rows = n * group;  // at most 2^30, as all rows of a call together
     if (rows <= kDecodeRows) return;
-    const int64_t r0 = (int64_t)(vt - (int)((int64_t)q0 * group / kPromptRows + s)) * kPromptRows;
+    const int r0 = (vt - (int)((uint32_t)(q0 * group) / kPromptRows) - s) * kPromptRows;
     if (r0 < 0 || r0 >= rows) return;
 
     const float c = fmaxf(fabsf(a.scale), 1e-37f) * kLog2e;
-    const int64_t cap = (int64_t)a.b.cols * f.page;
-    const int64_t place0 = (int64_t)len - n;  // of the sequence's first row
-    const int64_t any_from = a.window > 0 ? place0 - a.window + 1 : 0;
-    const int64_t any_upto = len < cap ? (int64_t)len - 1 : cap - 1;
+    const int64_t room = (int64_t)a.b.cols * f.page;
+    const int cap = len < room ? len : (int)room;  // tokens that have a place
+    const int place0 = len - n;                    // of the sequence's first row
+    // The first and the last key that a row at some place sees; the same for places at the end of the keys.
+    const int window = a.window > 0 && a.window < len ? (int)a.window : 0;
+    auto first_of = [&](int place) { return window && place >= window ? place - window + 1 : 0; };
+    auto last_of = [&](int place) { return place < cap ? place : cap - 1; };
+    const int any_from = first_of(place0), any_upto = cap - 1;
 
-    const int64_t w0 = r0 + wave * kPromptTile;  // the wave's first row
-    const int64_t r = w0 + col;
-    const int qi = (int)(r / group), t = q0 + qi, h = head * group + (int)(r - (int64_t)qi * group);
+    const int w0 = r0 + wave * kPromptTile;  // the wave's first row
+    const int r = w0 + col;
+    const int qi = (int)((uint32_t)r / (uint32_t)group), t = q0 + qi, h = head * group + (r - qi * group);
     const bool real = r < rows && (uint32_t)t < (uint32_t)a.b.T;
-    PromptQuery<D> q;
+    Channels raw[CH];  // split into pieces once the first block's bytes are on their way
 #pragma unroll
-    for (int k = 0; k < CH; ++k) {
-        const Pieces x = split_query(a.q.p + t * a.q.ld + h * a.q.hd + k * 64 + hh * 32, real, a.scale);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q.p[k][i] = x.p[i];
-        q.scales[k] = x.at[0] | x.at[1] << 8 | x.at[2] << 16 | x.at[3] << 24;
-    }
-    const int64_t place = place0 + qi;
-    const int upto = real ? (int)(place < cap ? place : cap - 1) : -1;
-    const int from = a.window > 0 && place - a.window + 1 > 0 ? (int)(place - a.window + 1) : 0;
+    for (int k = 0; k < CH; ++k) raw[k] = read_query(a.q.p + t * a.q.ld + h * a.q.hd + k * 64 + hh * 32, real);
+    const int upto = real ? last_of(place0 + qi) : -1, from = first_of(place0 + qi);
     f32x16 o[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) o[i] = f32x16{};
-    float m = -INFINITY, l = 0.f;
+    float ref = -INFINITY, l = 0.f;  // what weights are relative to, a power of two, and their sum
 
     // blocks that the workgroup walks, and those that need no mask for the wave
-    const int64_t last_row = (r0 + kPromptRows < rows ? r0 + kPromptRows : rows) - 1;
-    const int64_t see_last = place0 + last_row / group < cap ? place0 + last_row / group : cap - 1;
-    const int64_t see_first = a.window > 0 ? place0 + r0 / group - a.window + 1 : 0;
-    const int b_first = (int)((see_first > 0 ? see_first : 0) / kBlock);
-    const int b_end = see_last >= 0 ? (int)(see_last / kBlock) + 1 : 0;
-    const int64_t wl = w0 + kPromptTile - 1 < rows - 1 ? w0 + kPromptTile - 1 : rows - 1;
-    const int64_t w_last = place0 + wl / group;                    // the last key that any of its rows sees
-    const int64_t w_all = place0 + w0 / group < cap - 1 ? place0 + w0 / group : cap - 1;
-    const int64_t w_all_from = a.window > 0 ? w_last - a.window + 1 : 0;
+    auto place_of = [&](int r) { return place0 + (int)((uint32_t)min(r, rows - 1) / (uint32_t)group); };
+    const int b_first = first_of(place_of(r0)) / kBlock;
+    const int see_last = last_of(place_of(r0 + kPromptRows - 1));
+    const int b_end = see_last >= 0 ? see_last / kBlock + 1 : 0;
+    const int w_all = last_of(place_of(w0)), w_all_from = first_of(place_of(w0 + kPromptTile - 1));
 
     const int32_t *row = a.b.table + (int64_t)s * a.b.ld_table;
     Blocks lies;
@@ -855,20 +867,18 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
     const uint32_t k_off = col * (D / 2) + hh * 16;
     const uint32_t ks_off = ((col & 15) * (D / 32) + hh) * 4;
     u32x4 kx[2][CH];
-    uint32_t ks[CH];
-    auto load_keys = [&](int b) {
+    uint32_t ks[2][CH];
+    auto load_keys = [&](int b, int tt) {
         const uint8_t *kp = lies.at(b - held), *sp = kp + scales_at(f, b);
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-#pragma unroll
-            for (int tt = 0; tt < 2; ++tt)
-                kx[tt][k] = load_cache<false, u32x4>(kp + k_off + (tt * 16 * D + k * 32));
-            ks[k] = load_cache<false, uint32_t>(sp + ks_off + k * 8);
+            kx[tt][k] = load_cache<false, u32x4>(kp + k_off + (tt * 16 * D + k * 32));
+            ks[tt][k] = load_cache<false, uint32_t>(sp + ks_off + k * 8);
         }
     };
 
-    // this wave's share of a block's values: tokens 16 u + 4 vh + {0..3, 8..11} of unit column c8,
-    // bytes b0 .. of their words (a byte is two channels)
+    // this wave's share of a block's values: tokens 16 vu + 4 vh + {0..3, 8..11} of unit column c8,
+    // bytes byte0 .. of their words (a byte is two channels)
     constexpr int kBytes = D / 64;
     const int vg = lane >> 4, vh = vg & 1, vu = 2 * (wave >> 1) + (vg >> 1);
     const int c8 = D == 128 ? (lane & 15) : (lane & 7);
@@ -884,28 +894,34 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
             vs[i] = load_cache<false, uint32_t>(sp + vs_off + i * (D / 4));
         }
     };
+    load_keys(b_first, 0);
+    load_keys(b_first, 1);
+    load_values(b_first);
+    PromptQuery<D> q;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+        const Pieces x = split_query(raw[k], a.scale);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q.p[k][i] = x.p[i];
+        q.scales[k] = x.at[0] | x.at[1] << 8 | x.at[2] << 16 | x.at[3] << 24;
+    }
     // a weight of 0 times what an unseen place holds must be 0
     auto hide_values = [&](int b) {
-        const int64_t j0 = (int64_t)b * kBlock;
+        const int j0 = b * kBlock;
         const bool page = lies.ok(b - held);
         if (j0 < any_from || j0 + kBlock - 1 > any_upto || !page) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int64_t tok = j0 + 16 * vu + 8 * (e >> 2) + 4 * vh + (e & 3);
+                const int tok = j0 + 16 * vu + 8 * (e >> 2) + 4 * vh + (e & 3);
                 if (tok > any_upto || tok < any_from || !page) vs[e >> 2] &= ~(255u << (8 * (e & 3)));
             }
         }
     };
-    auto put_values = [&](int by, u32x4 (*to)[MT][kWave]) {  // byte byte0 + by of the words
-        uint32_t cv[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) cv[e] = fp4_pair(vx[e >> 2][e & 3] >> (8 * byte0), scale_field(vs[e >> 2], e & 3), by);
-        u32x4 even, odd;  // channels 2 (byte0 + by) and the next
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            even[e] = __builtin_amdgcn_perm(cv[2 * e + 1], cv[2 * e], 0x05040100u);
-            odd[e] = __builtin_amdgcn_perm(cv[2 * e + 1], cv[2 * e], 0x07060302u);
-        }
+    // token e of the eight, byte byte0 + by of its word; then the channels 2 (byte0 + by) and the next of all of them
+    auto convert = [&](int by, int e) {
+        return fp4_pair(vx[e >> 2][e & 3] >> (8 * byte0), scale_field(vs[e >> 2], e & 3), by);
+    };
+    auto put_values = [&](int by, const u32x4 &even, const u32x4 &odd, u32x4 (*to)[MT][kWave]) {
         if constexpr (D == 128) {
             to[vu][byte0 + by][vh * 32 + c8] = even;
             to[vu][byte0 + by][vh * 32 + 16 + c8] = odd;
@@ -915,111 +931,175 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
             p[8] = odd;
         }
     };
+    auto even_of = [](uint32_t hi, uint32_t lo) { return __builtin_amdgcn_perm(hi, lo, 0x05040100u); };
+    auto odd_of = [](uint32_t hi, uint32_t lo) { return __builtin_amdgcn_perm(hi, lo, 0x07060302u); };
 
-    // scores of the block whose keys are in hand
-    auto dot = [&](f32x16 (&sc)[2]) {
-        // of a scale dword's four tokens 16 j + col % 16 this lane's are j = col / 16 and that + 2
-        int sk[CH];
-#pragma unroll
-        for (int k = 0; k < CH; ++k) sk[k] = (int)(ks[k] >> ((col >> 4) * 8));
+    // Products of the scores: number i of a 32-token tile's 4 CH, that of chunk i / 4 and piece i % 4.  Of a
+    // scale dword's four tokens 16 j + col % 16 this lane's are j = col / 16 and that + 2.
+    auto dot = [&](int tt, int i, f32x16 &acc) {
         const f32x16 zero = {};
-#define NM_KV4_DOT(T, K, P, C)                                                                                        \
-    sc[T] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(kx[T][K]), wide(q.p[K][P]), C, 4, 2, 2 * T, sk[K], P, \
-                                                            (int)q.scales[K])
-        NM_KV4_DOT(0, 0, 0, zero); NM_KV4_DOT(1, 0, 0, zero);
-        NM_KV4_DOT(0, 0, 1, sc[0]); NM_KV4_DOT(1, 0, 1, sc[1]);
-        NM_KV4_DOT(0, 0, 2, sc[0]); NM_KV4_DOT(1, 0, 2, sc[1]);
-        NM_KV4_DOT(0, 0, 3, sc[0]); NM_KV4_DOT(1, 0, 3, sc[1]);
-        if constexpr (CH == 2) {
-            NM_KV4_DOT(0, CH - 1, 0, sc[0]); NM_KV4_DOT(1, CH - 1, 0, sc[1]);
-            NM_KV4_DOT(0, CH - 1, 1, sc[0]); NM_KV4_DOT(1, CH - 1, 1, sc[1]);
-            NM_KV4_DOT(0, CH - 1, 2, sc[0]); NM_KV4_DOT(1, CH - 1, 2, sc[1]);
-            NM_KV4_DOT(0, CH - 1, 3, sc[0]); NM_KV4_DOT(1, CH - 1, 3, sc[1]);
+        const int sk = (int)(ks[tt][i / 4] >> ((col >> 4) * 8));
+#define NM_KV4_DOT(T, P)                                                                                                  \
+    acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(kx[T][i / 4]), wide(q.p[i / 4][P]), i ? acc : zero, 4, 2,  \
+                                                          2 * T, sk, P, (int)q.scales[i / 4])
+        switch (4 * tt + i % 4) {
+        case 0: NM_KV4_DOT(0, 0); break;
+        case 1: NM_KV4_DOT(0, 1); break;
+        case 2: NM_KV4_DOT(0, 2); break;
+        case 3: NM_KV4_DOT(0, 3); break;
+        case 4: NM_KV4_DOT(1, 0); break;
+        case 5: NM_KV4_DOT(1, 1); break;
+        case 6: NM_KV4_DOT(1, 2); break;
+        default: NM_KV4_DOT(1, 3); break;
         }
 #undef NM_KV4_DOT
     };
-
-    load_keys(b_first);
-    load_values(b_first);
-    hide_values(b_first);
+    constexpr int kDots = 4 * CH, kSums = 2 * MT;  // matrix products of a 32-token tile: scores, values
+    auto sum = [&](int i, const u32x4 &v, const uint32_t (&w)[8]) {
+        union { u32x4 u; bf16x8 h; } x;
+        union { uint32_t w[4]; bf16x8 h; } y;
+        x.u = v;
 #pragma unroll
-    for (int by = 0; by < kBytes; ++by) put_values(by, values[b_first & 1]);
-    load_values(b_first + 1);
-    __syncthreads();
-    for (int b = b_first; b < b_end; ++b) {
-        if (b - held == Blocks::kAhead) {
-            held = b;
-            lies.load(a.b, row, head, held, lane);
-        }
-        hide_values(b + 1);
-        // The next block's values are converted while the matrix unit computes this one's scores.
-        f32x16 sc[2];
-        dot(sc);
-#pragma unroll
-        for (int by = 0; by < kBytes; ++by) put_values(by, values[(b + 1) & 1]);
-#pragma unroll
-        for (int i = 0; i < 8 * CH; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        load_values(b + 2);
-        load_keys(b + 1);
-
-        const int64_t j0 = (int64_t)b * kBlock;
+        for (int e = 0; e < 4; ++e) y.w[e] = w[4 * (i / MT) + e];
+        o[i % MT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x.h, y.h, o[i % MT], 0, 0, 0);
+    };
+    // Scores of tile tt of block b: unseen ones to -infinity.
+    auto hide = [&](int b, int tt, f32x16 &sc) {
+        const int j0 = b * kBlock + 32 * tt;
         const bool page = lies.ok(b - held);
-        if (j0 < w_all_from || j0 + kBlock - 1 > w_all || !page) {
+        if (j0 < w_all_from || j0 + 31 > w_all || !page) {
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int tok = (int)j0 + 32 * tt + 8 * (i >> 2) + 4 * hh + (i & 3);
-                    if (tok > upto || tok < from || !page) sc[tt][i] = -INFINITY;
-                }
+            for (int i = 0; i < 16; ++i) {
+                const int tok = j0 + 8 * (i >> 2) + 4 * hh + (i & 3);
+                if (tok > upto || tok < from || !page) sc[i] = -INFINITY;
+            }
         }
-        float mx = fmaxf(sc[0][0], sc[1][0]);
+    };
+    auto largest = [&](const f32x16 &sc) {
+        float x = __builtin_amdgcn_fmed3f(sc[0], sc[1], INFINITY), y = __builtin_amdgcn_fmed3f(sc[2], sc[3], INFINITY);
 #pragma unroll
-        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, fmaxf(sc[0][i], sc[1][i]));
-        const float mn = fmaxf(m, halves_max(mx));
-        if (__any((mn - m) * c > kSlack)) {
-            const float keep = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - mn) * c);
+        for (int i = 4; i < 16; i += 4) {
+            x = __builtin_amdgcn_fmed3f(__builtin_amdgcn_fmed3f(x, sc[i], INFINITY), sc[i + 1], INFINITY);
+            y = __builtin_amdgcn_fmed3f(__builtin_amdgcn_fmed3f(y, sc[i + 2], INFINITY), sc[i + 3], INFINITY);
+        }
+        return halves_max(fmaxf(x, y)) * c;
+    };
+    // A new reference where a score has passed the old one.  The first is the largest score itself + kSlack,
+    // so that a lone key's weight is a power of two; the next ones lie whole powers of two from it, so that
+    // the weights w, which are rounded already and not yet multiplied, follow exactly.
+    auto raise = [&](float top, uint32_t (&w)[8]) {
+        if (__any(top > ref)) {
+            const float by = floorf(top - ref) + kSlack;
+            const float next = ref == -INFINITY ? top + kSlack : ref + by;
+            const float keep = top > ref ? __builtin_ldexpf(1.f, (int)fmaxf(-by, -1000.f)) : 1.f;
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[i] *= keep;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = pack_bf16(bf16_lo(w[i]) * keep, bf16_hi(w[i]) * keep);
             l *= keep;
-            m = mn;
+            if (top > ref) ref = next;
         }
-        const float mc = reference(m, c);
-        // Values are read from LDS kRead - 1 products ahead; the second half's weights are computed
-        // while the first half's products run.
-        constexpr int kRead = 5, kSteps = 4 * MT;
-        const u32x4 *from_lds = &values[b & 1][0][0][lane];
+    };
+
+    // Tile t = 2 b + tt: between them, product by product, the values of tile t (weights w are ready), the scores
+    // of tile t + 2 (into n), the softmax of tile t + 1 (scores sc to weights wn) and half of the conversion of
+    // block b + 1.
+    auto step = [&](int b, int tt, uint32_t (&w)[8], uint32_t (&wn)[8], f32x16 &sc, f32x16 &n) {
+        const u32x4 *from_lds = &values[b & 1][2 * tt][0][lane];
+        hide(tt ? b + 1 : b, tt ^ 1, sc);
+        raise(largest(sc), w);
+        const float mc = ref == -INFINITY ? 0.f : ref;
+        if (tt == 0) hide_values(b + 1);
+
+        constexpr int kRead = 3;  // value operands read ahead
         u32x4 v[kRead];
 #pragma unroll
-        for (int k = 0; k < kRead - 1; ++k) v[k] = from_lds[k * kWave];
+        for (int i = 0; i < kRead - 1; ++i) v[i] = from_lds[i * kWave];
+        uint32_t cv[8];
+        u32x4 even, odd;
+        float part = 0.f;
         __builtin_amdgcn_sched_barrier(0);
-        uint32_t p[16];  // weights, as pairs: 8 tokens of each of four 16-token steps
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) sc[tt][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[tt][i], c, -mc));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[8 * tt + i] = pack_bf16(sc[tt][2 * i], sc[tt][2 * i + 1]);
-#pragma unroll
-            for (int k = tt * kSteps / 2; k < (tt + 1) * kSteps / 2; ++k) {
-                if (k + kRead - 1 < kSteps) v[(k + kRead - 1) % kRead] = from_lds[(k + kRead - 1) * kWave];
-                union { u32x4 u; bf16x8 h; } x;
-                union { uint32_t w[4]; bf16x8 h; } w;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w.w[e] = p[4 * (k / MT) + e];
-                x.u = v[k % kRead];
-                o[k % MT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x.h, w.h, o[k % MT], 0, 0, 0);
-                __builtin_amdgcn_sched_barrier(0x406);  // vector and scalar work may pass
+        for (int k = 0; k < 8; ++k) {
+            if (k + kRead - 1 < kSums) v[(k + kRead - 1) % kRead] = from_lds[(k + kRead - 1) * kWave];
+            if (k < kSums) sum(k, v[k % kRead], w);
+            if (k < kDots) dot(tt, k, n);
+            const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[2 * k], c, -mc));
+            const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[2 * k + 1], c, -mc));
+            wn[k] = pack_bf16(e0, e1);
+            part += e0 + e1;
+            if (tt < kBytes) {
+                cv[k] = convert(tt, k);
+                if (k & 1) {
+                    even[k / 2] = even_of(cv[k], cv[k - 1]);
+                    odd[k / 2] = odd_of(cv[k], cv[k - 1]);
+                }
             }
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 9, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // this step's work: not to be put off to where it is used
+        asm volatile("" : "+v"(n));
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                l += (sc[tt][4 * i] + sc[tt][4 * i + 1]) + (sc[tt][4 * i + 2] + sc[tt][4 * i + 3]);
+        for (int k = 0; k < 8; ++k) asm volatile("" : "+v"(wn[k]));
+        l += part;
+        if (tt < kBytes) put_values(tt, even, odd, values[(b + 1) & 1]);
+        if (tt == kBytes - 1) load_values(b + 2);
+        load_keys(b + 2, tt);
+    };
+
+    if (b_first < b_end) {
+        // fill the pipeline: values of the first block, scores of its two tiles, weights of the first
+        uint32_t wa[8], wb[8];
+        f32x16 sa, sb;
+        hide_values(b_first);
+#pragma unroll
+        for (int by = 0; by < kBytes; ++by) {
+            u32x4 even, odd;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t lo = convert(by, 2 * e), hi = convert(by, 2 * e + 1);
+                even[e] = even_of(hi, lo);
+                odd[e] = odd_of(hi, lo);
+            }
+            put_values(by, even, odd, values[b_first & 1]);
+        }
+        load_values(b_first + 1);
+#pragma unroll
+        for (int i = 0; i < kDots; ++i) dot(0, i, sa);
+#pragma unroll
+        for (int i = 0; i < kDots; ++i) dot(1, i, sb);
+        load_keys(b_first + 1, 0);
+        load_keys(b_first + 1, 1);
+        hide(b_first, 0, sa);
+        {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) wa[k] = 0;
+            raise(largest(sa), wa);
+            const float mc = ref == -INFINITY ? 0.f : ref;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sa[2 * k], c, -mc));
+                const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sa[2 * k + 1], c, -mc));
+                wa[k] = pack_bf16(e0, e1);
+                l += e0 + e1;
+            }
         }
         __syncthreads();
+        int b = b_first;
+        do {
+            if (b - held == Blocks::kAhead) {
+                held = b;
+                lies.load(a.b, row, head, held, lane);
+            }
+            step(b, 0, wa, wb, sb, sa);
+            step(b, 1, wb, wa, sa, sb);
+            __syncthreads();
+        } while (++b < b_end);
     }
     l = halves_sum(l);
     if (!real) return;
@@ -1041,7 +1121,7 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
             }
             *reinterpret_cast<u32x4 *>(out + (8 * i + 4 * hh + j) * 8) = w;
         }
-    if (hh == 0 && a.lse) a.lse[t * a.ld_lse + h] = l != 0.f ? (reference(m, c) + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    if (hh == 0 && a.lse) a.lse[t * a.ld_lse + h] = l != 0.f ? (ref + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
 int device_cus() {
