@@ -44,6 +44,11 @@ constexpr int kWaves = 4;       // waves per workgroup
 // are row tiles for a quarter of the workgroups twice that: 32 of 2000 15.3 against 20.6.
 constexpr int kWholeTokens = 1024;
 constexpr int kDecodeRows = 64; // query rows of a head up to which a sequence is walked row tile by row tile
+// Row tiles of a call, one to so many waves at most, up to which prompts are walked by row tiles too: a
+// workgroup of the prompt kernel walks all keys of its rows, so a short prompt behind a long context would keep a few
+// CUs busy for long (32 query, 8 key heads: 40 rows behind 20K tokens 416 us there and 49 in row tiles, 512 behind
+// nothing 24 and 20, 640 behind 3K 88 and 94, 1024 behind nothing 35 and 44).
+constexpr int kFewTiles = 2;
 constexpr int kGroupsPerCu = 2; // resident workgroups: 8 waves a CU, 8.7 KB of cache in flight each
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -1155,14 +1160,14 @@ bool whole(int64_t tiles, int groups, int64_t room) {
 template <int D>
 hipError_t launch(Kv4Attention a, int64_t max_q, void *ws, hipStream_t st) {
     const int group = a.heads / a.b.f.n_kv;
-    // Where no sequence has many rows every one is walked by row tiles; else each goes to the
-    // kernel that its own rows ask for.
-    a.prompts = max_q * group > kDecodeRows;
+    const int groups = device_cus() * kGroupsPerCu;
+    // Where no sequence has many rows, or all rows make few row tiles for the machine's waves, every sequence is
+    // walked by row tiles, split over its keys; else each goes to the kernel that its own rows ask for.
+    a.prompts = max_q * group > kDecodeRows && (int64_t)a.b.T * a.heads > (int64_t)groups * kWaves * kRows / kFewTiles;
     if (a.prompts) {
         const int64_t tiles = (int64_t)a.b.T * group / kPromptRows + a.b.S;
         kv4_prompt_kernel<D><<<(unsigned)(tiles * a.b.f.n_kv), kWaves * kWave, 0, st>>>(a, (int)tiles);
     }
-    const int groups = device_cus() * kGroupsPerCu;
     Part<D> *parts = (Part<D> *)ws;
     PartTag *tags = (PartTag *)(parts + 2 * (size_t)groups);
     const int64_t tiles = whole_tiles(a.b.T, a.b.S, a.heads, a.b.f.n_kv);
