@@ -9,7 +9,7 @@
 // Steps of fork and resize: pages given back; free pages counted, beside them the prefix
 // sums of what is asked; pages handed out -- the free page of rank k goes to the request
 // whose share of the prefix sums holds k.  Small pools and few requests go through all
-// steps in one workgroup and need no workspace (one launch: 4-9 us; three launches: 12-17 us);
+// steps in one workgroup and need no workspace (one launch: 4-6 us; three launches: 12-17 us);
 // larger ones take a launch for each step, a workgroup to each 4096 pages.
 #include "nm_device.h"
 #include "nm_kv.h"
@@ -21,7 +21,7 @@ constexpr int kThreads = 1024;
 constexpr int kWavesPerGroup = kThreads / kWave;
 constexpr int kChunk = 4096;         // pages per workgroup: 64 words of 64
 constexpr int kSmallPages = 16384;   // one workgroup: 256 words of 64 pages in LDS,
-constexpr int kSmallRequests = 64;   // pairs, a wave to each in turn (4: 9 us against 13; 224: 64 us against 14),
+constexpr int kSmallRequests = 64;   // pairs, a wave to each in turn (4: 6 us against 13; 224: 60 us against 14),
 constexpr int kSmallRows = 256;      // sequences, a thread to each and a wave to their rows in turn,
 constexpr int kSmallEntries = 65536; // and their entries
 constexpr int kPrefixLds = 4096;     // requests whose prefix sums a workgroup searches in LDS
@@ -71,6 +71,15 @@ __device__ __forceinline__ int fresh(const int32_t *p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// A barrier behind which atomics and stores of the workgroup have been carried out: each wave waits for its own,
+// and what reads their results reads where they were made (`fresh`).  A fence for the whole device
+// would also write the caches back, for readers that a single workgroup does not have (resize of 16
+// sequences 8.5 -> 5.6 us, of it a part by reading last pages before the barrier).
+__device__ __forceinline__ void done_in_group() {
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+}
+
 __device__ __forceinline__ uint64_t below(int lane) { return (1ull << lane) - 1; }
 
 // Inclusive sum over the lanes of a wave.
@@ -118,34 +127,37 @@ __device__ __forceinline__ bool slots_exist(const KvBook &b, int p, int c) {
     return p >= 0 && p < b.S && c >= 0 && c < b.S && p != c;
 }
 
-__device__ __forceinline__ Request resize_request(const KvBook &b, int s, int want) {
+// The page that a sequence of `len` tokens writes next into, if its last page is partly filled; else -1.
+__device__ __forceinline__ int tail_page(const KvBook &b, int s, int64_t len) {
+    if (len <= 0 || len > (int64_t)b.cols * b.page || len % b.page == 0) return -1;
+    const int tail = b.table[(int64_t)s * b.ld + len / b.page];
+    return in_pool(tail, b.N) ? tail : -1;
+}
+
+// old: the length now; tail: its tail_page, which `holders` sequences hold.
+__device__ __forceinline__ Request resize_request(const KvBook &b, int s, int want, int old, int tail, int holders) {
     Request r = {0, 0, -1, -1};
-    const int old = b.kv_len[s] > 0 ? b.kv_len[s] : 0;
+    if (old < 0) old = 0;
     if (want < 0 || (int64_t)want > (int64_t)b.cols * b.page) return r;
     r.row = s;
     const int have = pages_for(old, b.page, b.cols), pages = pages_for(want, b.page, b.cols);
     r.col = have;
     if (want <= old) return r;
-    if (old % b.page != 0 && have > 0) {  // writes into its last page: shared pages are copied first
-        const int tail = b.table[(int64_t)s * b.ld + have - 1];
-        if (in_pool(tail, b.N) && fresh(&b.refs[tail]) > 1) {
-            r.tail = tail;
-            r.col = have - 1;
-        }
+    if (tail >= 0 && holders > 1) {  // writes into its last page: shared pages are copied first
+        r.tail = tail;
+        r.col = have - 1;
     }
     r.need = pages > r.col ? pages - r.col : 0;
     return r;
 }
 
-__device__ __forceinline__ Request fork_request(const KvBook &b, int p, int c) {
+__device__ __forceinline__ Request fork_request(const KvBook &b, int c, int64_t len, int tail) {
     Request r = {0, 0, -1, c};
-    const int64_t len = b.kv_len[p];
     if (len <= 0 || len > (int64_t)b.cols * b.page) return r;
     r.col = (int)(len / b.page);
     if (len % b.page) {
-        const int tail = b.table[(int64_t)p * b.ld + r.col];
         r.need = 1;
-        r.tail = in_pool(tail, b.N) ? tail : -1;
+        r.tail = tail;
     }
     return r;
 }
@@ -264,18 +276,19 @@ __global__ __launch_bounds__(kThreads) void resize_small_kernel(KvBook b, const 
     __shared__ SmallPool p;
     __shared__ SmallRequests q;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, s = threadIdx.x;
-    const int want = s < b.S ? new_len[s] : -1;
-    const int have = s < b.S ? pages_for(b.kv_len[s], b.page, b.cols) : 0;
+    const int want = s < b.S ? new_len[s] : -1, old = s < b.S ? b.kv_len[s] : 0;
+    const int tail = s < b.S ? tail_page(b, s, old) : -1;  // of use to a sequence that grows, whose row stays as it is
+    const int have = pages_for(old, b.page, b.cols);
     const int keep = want < 0 ? have : pages_for(want, b.page, b.cols);
     for (uint64_t left = __ballot(keep < have); left; left &= left - 1) {  // my wave's sequences that give pages back
         const int i = __builtin_ctzll(left);
         release_row(b, wave * 64 + i, __builtin_amdgcn_readlane(keep, i), __builtin_amdgcn_readlane(have, i), lane, 64);
     }
-    __threadfence();
-    __syncthreads();
+    done_in_group();
+    const int holders = tail >= 0 ? fresh(&b.refs[tail]) : 0;
     const int nfree = small_bits(p, b.refs, b.N, false);
     Request r = {0, 0, -1, -1};
-    if (s < b.S) r = resize_request(b, s, want);
+    if (s < b.S) r = resize_request(b, s, want, old, tail, holders);
     const int asked = small_hand_out(b, p, q, b.S, r, nfree, moves);
     if (s == 0) *missing = asked > nfree ? asked - nfree : 0;
     if (s < b.S) resize_row(b, s, r, r.row >= 0 && (r.need == 0 || q.prefix[s] <= nfree), want, moves);
@@ -286,8 +299,12 @@ __global__ __launch_bounds__(kThreads) void fork_small_kernel(KvBook b, const in
     __shared__ SmallPool p;
     __shared__ SmallRequests q;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = threadIdx.x;
-    if (t < n) q.child[t] = child[t];
+    const int to_t = t < n ? child[t] : -1, from_t = t < n ? parent[t] : -1;
+    if (t < n) q.child[t] = to_t;
     __syncthreads();
+    // a parent is nobody's child: its row stays as it is
+    const int64_t len = slots_exist(b, from_t, to_t) ? b.kv_len[from_t] : 0;
+    const int tail = tail_page(b, from_t, len);
     for (int i = wave; i < n; i += kWavesPerGroup) {
         const int from = parent[i], to = q.child[i];
         bool ok = slots_exist(b, from, to);
@@ -296,11 +313,10 @@ __global__ __launch_bounds__(kThreads) void fork_small_kernel(KvBook b, const in
         if (lane == 0) q.valid[i] = ok;
         if (ok) release_row(b, to, 0, pages_for(b.kv_len[to], b.page, b.cols), lane, 64);
     }
-    __threadfence();
-    __syncthreads();
+    done_in_group();
     const int nfree = small_bits(p, b.refs, b.N, false);
     Request r = {0, 0, -1, -1};
-    if (t < n && q.valid[t]) r = fork_request(b, parent[t], q.child[t]);
+    if (t < n && q.valid[t]) r = fork_request(b, to_t, len, tail);
     const int asked = small_hand_out(b, p, q, n, r, nfree, moves);
     if (t == 0) *missing = asked > nfree ? asked - nfree : 0;
     for (int i = wave; i < n; i += kWavesPerGroup) {
@@ -382,7 +398,10 @@ __global__ __launch_bounds__(kThreads) void resize_count_kernel(KvBook b, const 
     if ((int)blockIdx.x < (int)gridDim.x - 1)
         count_chunk(b.refs, b.N, w, false);
     else
-        scan_requests(b.S, w, [&](int s) { return resize_request(b, s, new_len[s]); });
+        scan_requests(b.S, w, [&](int s) {
+            const int old = b.kv_len[s], tail = tail_page(b, s, old);
+            return resize_request(b, s, new_len[s], old, tail, tail >= 0 ? fresh(&b.refs[tail]) : 0);
+        });
 }
 
 __global__ __launch_bounds__(kThreads) void fork_count_kernel(KvBook b, const int32_t *parent, const int32_t *child,
@@ -392,7 +411,9 @@ __global__ __launch_bounds__(kThreads) void fork_count_kernel(KvBook b, const in
     else
         scan_requests(n, w, [&](int i) {
             const Request none = {0, 0, -1, -1};
-            return w.valid[i] ? fork_request(b, parent[i], child[i]) : none;
+            if (!w.valid[i]) return none;
+            const int64_t len = b.kv_len[parent[i]];
+            return fork_request(b, child[i], len, tail_page(b, parent[i], len));
         });
 }
 
