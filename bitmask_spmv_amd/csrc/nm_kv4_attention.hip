@@ -23,6 +23,11 @@
 // not be alike, nor known to the host.  A wave finishes the rows whose blocks are all its own;
 // pieces of rows cut between waves are joined in LDS, those cut between workgroups in fp32
 // through the workspace by a second kernel, in a fixed order.
+//
+// Bound: reading the cache.  16 sequences of up to 64K tokens, 64 and 8 heads: 525 MB in 92 us, 48 of up to 8K,
+// 40 and 8 heads: 183 MB in 41 us; between the waves' first and last blocks (6 and 30, or 85 us after the launch) 6.0
+// and 6.6 TB/s, where a plain read of a large buffer reaches 6.9.  The rest is the launch, the way to the
+// first block (lengths, page table, bytes: each waits for the one before) and the join, 4.6 and 6 us.
 #include <atomic>
 
 #include "nm_device.h"
@@ -39,9 +44,9 @@ constexpr int kRows = 16;       // query rows of a tile
 // relative to that point, so that they stay at or below 1 (and O below keys times the largest value).
 constexpr float kSlack = 8.f;
 constexpr int kWaves = 4;       // waves per workgroup
-// Context up to which each row tile may be one workgroup's, which needs no second launch:
-// 8 sequences of 1000 tokens 10.4 us against 12.5, of 2000 14.1 against 13.4; where there
-// are row tiles for a quarter of the workgroups twice that: 32 of 2000 15.3 against 20.6.
+// Context up to which each row tile may be one workgroup's, which needs no second launch: 8 sequences of up to
+// 1000 tokens, 32 and 8 heads, 10.5 us against 11.8 split, of 2000 13.2 against 12.3; four times that where there are row
+// tiles for a quarter of the workgroups: 20 of up to 4000 20.2 against 20.4, 32 21.4 against 24.2, 32 of 8000 36 against 32.
 constexpr int kWholeTokens = 1024;
 constexpr int kDecodeRows = 64; // query rows of a head up to which a sequence is walked row tile by row tile
 // Row tiles of a call, one to so many waves at most, up to which prompts are walked by row tiles too: a
@@ -1154,7 +1159,7 @@ size_t decode_workspace(int groups) {
 // q_start[s] * group / rows + s on, so their number is bounded), nothing to join.
 int64_t whole_tiles(int64_t T, int64_t S, int heads, int n_kv) { return (T * (heads / n_kv) / kRows + S) * n_kv; }
 bool whole(int64_t tiles, int groups, int64_t room) {
-    return tiles <= groups && room <= (4 * tiles < groups ? kWholeTokens : 2 * kWholeTokens);
+    return tiles <= groups && room <= (4 * tiles < groups ? kWholeTokens : 4 * kWholeTokens);
 }
 
 template <int D>

@@ -286,6 +286,26 @@ def test_a_query_that_is_not_finite_spoils_its_own_row_alone(rows, lens, D):
     assert (o3 == 0).all() and (l3 == float("-inf")).all()
 
 
+def test_row_tiles_of_a_workgroup_each_over_long_contexts():
+    """Enough row tiles that none is split between workgroups, up to 60 blocks each and a few without any."""
+    say("whole tiles")
+    g = np.random.default_rng(12)
+    H, Hq, D, ps = 8, 16, 64, 256
+    lens = [3840, 1, 64, 65, 0, 3000] + [int(n) for n in g.integers(1, 3840, size=14)]
+    rows = [1, 1, 2, 1, 1, 0] + [1] * 14
+    table, kv_len, q_start, N = batch(g, rows, lens, ps)
+    assert nm.nm_kv4_attention_workspace_bytes(sum(rows), len(rows), Hq, H, D, 2, table.shape[1] * ps) == 0
+    cache = filled_cache(g, N, ps, H, D)
+    q = bf16(g.standard_normal((sum(rows), Hq, D)))
+    for window in (0, 500):
+        r = kv4.attention(q, cache, table, kv_len, q_start, ps, H, D**-0.5, window)
+        bo, bl = attention_bounds(r)
+        out, lse = nm.nm_kv4_attention(dev_bf16(bits(q)), dev(cache), dev(table), dev(kv_len), dev(q_start), H, ps, 2, window=window)
+        lse, empty = lse.cpu().numpy().astype(np.float64), np.isinf(r["lse"])
+        assert (np.abs(f64(out) - r["out"]) <= bo).all()
+        assert (lse[empty] == -np.inf).all() and (np.abs(lse - r["lse"])[~empty] <= bl[~empty]).all()
+
+
 def test_infinities_and_nan_are_stored_as_the_largest_number():
     """6 * 2^125 with their sign; the rest of their 32 channels lose against that, the next 32 do not."""
     say("store not finite")
