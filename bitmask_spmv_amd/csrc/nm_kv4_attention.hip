@@ -15,8 +15,8 @@
 //     query row, which is what the bf16 product over tokens takes; V units of 4 tokens x 8
 //     channels give the same lane its 8 tokens of 8 channels with one conversion and one
 //     byte permute per two values, nothing passes through LDS.
-// Weights are rounded to bf16 for that product (half a step: 2^-9 of each on average
-// cancelling over keys); scores, maxima, sums and O stay in fp32.
+// Weights are rounded to bf16 for that product (off by 2^-8 of each at most, either way, so
+// much of it cancels over keys); scores, maxima, sums and O stay in fp32.
 //
 // Work split.  All (sequence, key/value head, row tile, 64-token block) units of a call
 // are laid end to end, in that order, and cut into equal runs, one per wave: lengths need
@@ -24,10 +24,11 @@
 // pieces of rows cut between waves are joined in LDS, those cut between workgroups in fp32
 // through the workspace by a second kernel, in a fixed order.
 //
-// Bound: reading the cache.  16 sequences of up to 64K tokens, 64 and 8 heads: 525 MB in 92 us, 48 of up to 8K,
-// 40 and 8 heads: 183 MB in 41 us; between the waves' first and last blocks (6 and 30, or 85 us after the launch) 6.0
-// and 6.6 TB/s, where a plain read of a large buffer reaches 6.9.  The rest is the launch, the way to the
-// first block (lengths, page table, bytes: each waits for the one before) and the join, 4.6 and 6 us.
+// Bound: reading the cache.  16 sequences of up to 64K tokens, 64 and 8 heads: 525 MB in 92 us, 89 of them this
+// kernel's (5.9 TB/s); 48 of up to 8K, 40 and 8 heads: 183 MB in 41 us, 36 of them this kernel's (5.1 TB/s).  A plain read of
+// a large buffer reaches 6.9.  Until half of the waves are through, 28 us after the start of the smaller one, the
+// walk itself reads 7.6 TB/s; the rest is the way to the first block (6 us: lengths, page table and bytes, each
+// waits for the one before), the waves that had to wait for the other one of their SIMD, and the join.
 #include <atomic>
 
 #include "nm_device.h"
