@@ -62,7 +62,7 @@ struct Kv4Attention {
     float scale = 1.f;
     int64_t window = 0;  // keys a query looks back over, itself among them; 0: all
     bool whole = false;    // a workgroup to each row tile
-    bool prompts = false;  // sequences of many rows are taken by the prompt kernel
+    bool prompts = false;  // sequences of many rows are taken 128 rows at a time
 };
 
 hipError_t launch_kv4_append(const Kv4Batch &b, const Kv4Rows &k, const Kv4Rows &v, hipStream_t st);

@@ -49,9 +49,9 @@ constexpr int kWaves = 4;       // waves per workgroup
 // 1000 tokens, 32 and 8 heads, 10.5 us against 11.8 split, of 2000 13.2 against 12.3; four times that where there are row
 // tiles for a quarter of the workgroups: 20 of up to 4000 20.2 against 20.4, 32 21.4 against 24.2, 32 of 8000 36 against 32.
 constexpr int kWholeTokens = 1024;
-constexpr int kDecodeRows = 64; // query rows of a head up to which a sequence is walked row tile by row tile
+constexpr int kDecodeRows = 64; // query rows of a head up to which a sequence among others is walked by row tiles
 // Row tiles of a call, one to so many waves at most, up to which prompts are walked by row tiles too: a
-// workgroup of the prompt kernel walks all keys of its rows, so a short prompt behind a long context would keep a few
+// workgroup that takes a prompt walks all keys of its rows, so a short prompt behind a long context would keep a few
 // CUs busy for long (32 query, 8 key heads: 40 rows behind 20K tokens 416 us there and 49 in row tiles, 512 behind
 // nothing 24 and 20, 640 behind 3K 88 and 94, 1024 behind nothing 35 and 44).
 constexpr int kFewTiles = 2;
@@ -536,9 +536,10 @@ struct Join {
     }
 };
 
+// Workgroup `block` of `blocks`.
 template <int D, bool NT>
-__global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attention a, Part<D> *parts, PartTag *tags) {
-    __shared__ Shared<D> sh;
+__device__ __forceinline__ void decode(Kv4Attention &a, Part<D> *parts, PartTag *tags, Shared<D> &sh, int block,
+                                       int blocks) {
     a.b.f.dim = D;
     const Kv4Format &f = a.b.f;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -559,10 +560,10 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attenti
         behind.load(a.b, s0 + 64 + lane);
         total += lane64(units_scan(seq_from(a, group, x.q0, x.q1, x.len).units(f.n_kv, a.whole), lane), 63);
     }
-    const int64_t waves = (int64_t)gridDim.x * kWaves;
+    const int64_t waves = (int64_t)blocks * kWaves;
     const int64_t run = total < ((int64_t)1 << 31) ? (int64_t)(((uint32_t)total + (uint32_t)waves - 1) / (uint32_t)waves)
                                                    : (total + waves - 1) / waves;
-    int64_t u = a.whole ? blockIdx.x : ((int64_t)blockIdx.x * kWaves + wave) * run;
+    int64_t u = a.whole ? block : ((int64_t)block * kWaves + wave) * run;
     const int64_t stop = a.whole ? u + 1 : u + run;
     const int64_t end = stop < total ? stop : total;
     if (lane < 2) sh.tag[wave][lane].state = kNone;
@@ -683,7 +684,7 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attenti
     // Join the pieces.  Slot 0 of a wave belongs to a row that began before it, slot 1 to
     // one that begins in it and goes on behind it.
     const int row = threadIdx.x >> 4, cc = threadIdx.x & 15;
-    const int64_t me = blockIdx.x;
+    const int64_t me = block;
     PartTag out0 = {kNone}, out1 = {kNone};
     for (int first = -1; first < kWaves; ++first) {  // -1: the chain that enters this workgroup
         PartTag tag = first < 0 ? sh.tag[0][0] : sh.tag[first][1];
@@ -708,6 +709,12 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attenti
         tags[me * 2] = out0;
         tags[me * 2 + 1] = out1;
     }
+}
+
+template <int D, bool NT>
+__global__ __launch_bounds__(kWaves *kWave, 2) void kv4_decode_kernel(Kv4Attention a, Part<D> *parts, PartTag *tags) {
+    __shared__ Shared<D> sh;
+    decode<D, NT>(a, parts, tags, sh, blockIdx.x, gridDim.x);
 }
 
 // Rows cut between workgroups: the workgroup in which a row begins owns it; the pieces
@@ -810,9 +817,12 @@ __device__ __forceinline__ float halves_sum(float v) {
 }
 
 template <int D>
-__global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attention a, int tiles) {
+using Values = u32x4[2][4][D / 32][kWave];
+
+// Workgroup `block` of tiles * n_kv.
+template <int D>
+__device__ __forceinline__ void prompt(Kv4Attention &a, int tiles, Values<D> &values, int block) {
     constexpr int MT = D / 32, CH = D / 64;  // channel tiles of the values, chunks of the keys
-    __shared__ u32x4 values[2][4][MT][kWave];
     a.b.f.dim = D;
     const Kv4Format &f = a.b.f;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -822,8 +832,8 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
     // Row tile: sequence s owns the tiles from q_start[s] * group / rows + s on, which are
     // enough for it.  Later rows, which see more, go first; the heads of a tile go to
     // neighbouring workgroups, that is to different XCDs, so an XCD reads few heads.
-    const int head = blockIdx.x % f.n_kv;
-    const int vt = tiles - 1 - (int)(blockIdx.x / f.n_kv);
+    const int head = block % f.n_kv;
+    const int vt = tiles - 1 - block / f.n_kv;
     int s = 0;
     for (int n = a.b.S; n > 1;) {  // the last s whose first tile is at or before vt, 64 looks at a time
         const int step = (n + 63) >> 6, at = s + lane * step;
@@ -835,7 +845,7 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
     const int q0 = uniform_load(a.b.q_start + s), n = uniform_load(a.b.q_start + s + 1) - q0;
     const int len = uniform_load(a.b.kv_len + s);
     const int rows = n * group;  // at most 2^30, as all rows of a call together
-    if (rows <= kDecodeRows) return;
+    if (rows <= (a.b.S > 1 ? kDecodeRows : 0)) return;  // a lone sequence is all that there is
     const int r0 = (vt - (int)((uint32_t)(q0 * group) / kPromptRows) - s) * kPromptRows;
     if (r0 < 0 || r0 >= rows) return;
 
@@ -1135,6 +1145,23 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv4_prompt_kernel(Kv4Attenti
     if (hh == 0 && a.lse) a.lse[t * a.ld_lse + h] = l != 0.f ? (ref + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
+// The first `groups` workgroups walk the sequences of few rows, the others take the prompts: while the ones
+// wait for memory the others multiply.  One of the former to a CU leaves room for the latter beside them: 64 sequences of
+// up to 4000 tokens and a prompt of 2048, 32 and 8 heads, 86 us, with two to a CU 107 and in two launches
+// 106; 16 of up to 60000 and a prompt of 600, 64 and 8 heads, 122, 129 and 142.
+template <int D>
+__global__ __launch_bounds__(kWaves *kWave, 2) void kv4_mixed_kernel(Kv4Attention a, Part<D> *parts, PartTag *tags,
+                                                                     int groups, int tiles) {
+    __shared__ union {
+        Shared<D> sh;
+        Values<D> values;
+    } lds;
+    if ((int)blockIdx.x < groups)
+        decode<D, false>(a, parts, tags, lds.sh, blockIdx.x, groups);
+    else
+        prompt<D>(a, tiles, lds.values, (int)blockIdx.x - groups);
+}
+
 int device_cus() {
     static std::atomic<int> known[64];
     int dev = 0, cu = 0;
@@ -1168,14 +1195,17 @@ hipError_t launch(Kv4Attention a, int64_t max_q, void *ws, hipStream_t st) {
     const int group = a.heads / a.b.f.n_kv;
     const int groups = device_cus() * kGroupsPerCu;
     // Where no sequence has many rows, or all rows make few row tiles for the machine's waves, every sequence is
-    // walked by row tiles, split over its keys; else each goes to the kernel that its own rows ask for.
+    // walked by row tiles, split over its keys; else each is taken as its own rows ask for.
     a.prompts = max_q * group > kDecodeRows && (int64_t)a.b.T * a.heads > (int64_t)groups * kWaves * kRows / kFewTiles;
-    if (a.prompts) {
-        const int64_t tiles = (int64_t)a.b.T * group / kPromptRows + a.b.S;
-        kv4_prompt_kernel<D><<<(unsigned)(tiles * a.b.f.n_kv), kWaves * kWave, 0, st>>>(a, (int)tiles);
-    }
     Part<D> *parts = (Part<D> *)ws;
     PartTag *tags = (PartTag *)(parts + 2 * (size_t)groups);
+    if (a.prompts) {
+        const int64_t tiles = (int64_t)a.b.T * group / kPromptRows + a.b.S;
+        const int first = a.b.S > 1 ? groups / kGroupsPerCu : 0;  // a lone sequence is a prompt whatever its rows
+        kv4_mixed_kernel<D><<<(unsigned)(first + tiles * a.b.f.n_kv), kWaves * kWave, 0, st>>>(a, parts, tags, first, (int)tiles);
+        if (first) kv4_join_kernel<D><<<first, 256, 0, st>>>(a, parts, tags);
+        return hipGetLastError();
+    }
     const int64_t tiles = whole_tiles(a.b.T, a.b.S, a.heads, a.b.f.n_kv);
     a.whole = whole(tiles, groups, (int64_t)a.b.cols * a.b.f.page);
     const int grid = a.whole ? (int)tiles : groups;

@@ -32,6 +32,21 @@ def test_prompts(rows, lens, Hq, H, D):
     attention_case(sum(rows), rows, lens, Hq, H, D, 64, extra=extra(Hq))
 
 
+@pytest.mark.parametrize("rows", [0, 1, 9])
+def test_a_lone_sequence_of_fewer_rows_than_the_hint_says(rows):
+    say("lone", rows)
+    attention_case(rows, [rows], [rows + 500], 8, 2, 128, 64, max_q=300, extra=extra(8))
+
+
+@pytest.mark.parametrize("Hq,H,D", [(8, 2, 128), (5, 1, 64)])
+def test_prompts_beside_long_sequences_of_single_tokens(Hq, H, D):
+    """Both kinds in one launch, rows of the latter cut between workgroups."""
+    say("mixed", Hq, H, D)
+    rows, lens = [1, 200, 3, 1, 90, 0, 1, 8], [20000, 300, 5000, 1, 4000, 70, 0, 9000]
+    attention_case(Hq, rows, lens, Hq, H, D, 64, dirty=False, extra=extra(Hq))
+    attention_case(Hq, rows, lens, Hq, H, D, 128, window=700, dirty=False, extra=extra(Hq))
+
+
 @pytest.mark.parametrize("ps", [128, 256, 512])
 def test_page_sizes(ps):
     say("page size", ps)
