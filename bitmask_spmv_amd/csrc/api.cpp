@@ -901,9 +901,9 @@ nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int 
         const int64_t T = a.b.T, S = a.b.S;
         if (n_heads < 1 || n_heads > 1024 || n_heads % n_kv)
             return fail(NM_ERR_SHAPE, "%s: %d query heads are not a multiple of %d key/value heads", who, n_heads, n_kv);
-        if (T * (n_heads / n_kv) > kMaxDim)
-            return fail(NM_ERR_SHAPE, "%s: T=%lld rows of %d heads share a key/value head: more than 2^30", who,
-                        (long long)T, n_heads / n_kv);
+        if (T * n_heads > kMaxDim || S * n_kv > (1 << 22))  // rows and launches are numbered in 32 bits
+            return fail(NM_ERR_SHAPE, "%s: T=%lld rows of %d heads (2^30 in all) or S=%lld sequences of %d (2^22) are too many",
+                        who, (long long)T, n_heads, (long long)S, n_kv);
         if (window < 0 || max_q_len < 1)
             return fail(NM_ERR_SHAPE, "%s: window=%lld max_q_len=%lld", who, (long long)window, (long long)max_q_len);
         if (!(scale - scale == 0.f)) return fail(NM_ERR_SHAPE, "%s: scale is not finite", who);

@@ -127,8 +127,9 @@ def test_sizes_of_a_batch(L, name, bad):
     ("nm_kv4_attention", dict(ldo=100), SHAPE), ("nm_kv4_attention", dict(hdq=124), SHAPE),
     ("nm_kv4_attention", dict(hdo=129), ALIGN), ("nm_kv4_attention", dict(ld_lse=7), SHAPE),
     ("nm_kv4_attention", dict(lse=0x10002), ALIGN),
-    # rows of a key/value head are numbered in 32 bits
-    ("nm_kv4_attention", dict(T=(1 << 24) - 7, n_heads=256, n_kv=2, ldo=32768, ldq=32768, ld_lse=256), SHAPE)])
+    # rows and launches are numbered in 32 bits
+    ("nm_kv4_attention", dict(T=(1 << 24) - 7, n_heads=256, n_kv=2, ldo=32768, ldq=32768, ld_lse=256), SHAPE),
+    ("nm_kv4_attention", dict(S=1 << 20, n_heads=8, n_kv=8), SHAPE)])
 def test_rows_heads_and_scales(L, name, bad, want):
     assert call(L, name, **bad) == want
 
