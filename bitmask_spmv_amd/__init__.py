@@ -14,6 +14,7 @@ tensors that hold the raw uint32 mask words; bf16 tensors are passed as raw patt
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 
@@ -636,15 +637,18 @@ def nm_kv4_page_bytes(page_size: int, n_kv: int, head_dim: int) -> int:
     return int(lib.nm_kv4_page_bytes(int(page_size), int(n_kv), int(head_dim)))
 
 
-# The current stream's handle without the Python object around it (2 us of it), where torch has that.
+# The current stream's handle without the Python object around it (2 us of it), and the current device
+# without the check that torch is initialised (a tensor on it is at hand), where torch has them.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_Tensor, _I32, _BF16 = torch.Tensor, torch.int32, torch.bfloat16
 
 
 def _call(dev: int, fn, *args):
     """One entry point on device `dev`, on the stream that is current there."""
     stream = _raw_stream(dev)
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -654,13 +658,13 @@ def _call(dev: int, fn, *args):
 
 
 def _where(t: torch.Tensor, name: str) -> int:
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a tensor on a HIP device")
     return t.get_device()
 
 
-def _i32(t: torch.Tensor, name: str, dev: int, *shape) -> int:
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.get_device() != dev:
+def _i32(t: torch.Tensor, name: str, dev: int, shape: tuple) -> int:
+    if not isinstance(t, _Tensor) or t.dtype is not _I32 or t.get_device() != dev:
         raise TypeError(f"{name} must be an int32 tensor on cuda:{dev}")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, of shape {list(shape)} (got {list(t.shape)})")
@@ -668,22 +672,24 @@ def _i32(t: torch.Tensor, name: str, dev: int, *shape) -> int:
 
 
 def _table(t: torch.Tensor, dev: int):
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.get_device() != dev:
+    if not isinstance(t, _Tensor) or t.dtype is not _I32 or t.get_device() != dev:
         raise TypeError(f"page_table must be an int32 tensor on cuda:{dev}")
-    if t.dim() != 2 or t.stride(1) != 1:
+    stride = t.stride()
+    if len(stride) != 2 or stride[1] != 1:
         raise ValueError("page_table must be [S, columns], contiguous in its last dimension")
     S, cols = t.shape
-    return t.data_ptr(), t.stride(0) if S > 1 else cols, cols, S
+    return t.data_ptr(), stride[0] if S > 1 else cols, cols, S
 
 
 def _kv_rows(t: torch.Tensor, name: str, dev: int, shape) -> bytes:
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
+    if not isinstance(t, _Tensor) or t.dtype is not _BF16:
         raise TypeError(f"{name} must be a {torch.bfloat16} tensor")
     if t.get_device() != dev or t.shape != shape:
         raise ValueError(f"{name} must be on cuda:{dev}, of shape {list(shape)} (got {t.device}, {list(t.shape)})")
-    if len(shape) != 3:
+    stride = t.stride()
+    if len(stride) != 3:
         raise ValueError(f"{name} must be [T, heads, head_dim]")
-    ld, hd, one = t.stride()
+    ld, hd, one = stride
     if one != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
     T, H, D = shape
@@ -692,7 +698,7 @@ def _kv_rows(t: torch.Tensor, name: str, dev: int, shape) -> bytes:
 
 def _kv_batch(dev: int, cache: torch.Tensor, page_table, kv_len, q_start, page_size: int, n_kv: int, T: int, D: int):
     """(nm_kv4_batch, S, tokens a table row has room for), checked."""
-    if not isinstance(cache, torch.Tensor) or cache.dtype is not torch.uint8 or cache.get_device() != dev:
+    if not isinstance(cache, _Tensor) or cache.dtype is not torch.uint8 or cache.get_device() != dev:
         raise TypeError(f"cache must be a uint8 tensor on cuda:{dev}")
     if cache.dim() != 2 or not cache.is_contiguous():
         raise ValueError("cache must be contiguous, [num_pages, page_bytes]")
@@ -700,18 +706,30 @@ def _kv_batch(dev: int, cache: torch.Tensor, page_table, kv_len, q_start, page_s
     if nbytes != page_size * n_kv * (D + D // 16):  # nm_kv4_page_bytes, where it is not 0
         raise ValueError(f"cache pages of {page_size} tokens of {n_kv} heads of {D} cannot have {nbytes} bytes")
     tp, ld, cols, S = _table(page_table, dev)
-    return _KV4_BATCH.pack(cache.data_ptr(), N, tp, ld, _i32(kv_len, "kv_len", dev, S),
-                           _i32(q_start, "q_start", dev, S + 1), S, T, cols, page_size, n_kv, D), S, cols * page_size
+    return _KV4_BATCH.pack(cache.data_ptr(), N, tp, ld, _i32(kv_len, "kv_len", dev, (S,)),
+                           _i32(q_start, "q_start", dev, (S + 1,)), S, T, cols, page_size, n_kv, D), S, cols * page_size
 
 
-def _kv_workspace(nbytes: int, t: torch.Tensor, workspace: torch.Tensor | None):
-    """(tensor to hold on to, pointer, bytes)."""
+# Bytes that a call of some sizes on device `dev` needs: a function of them alone, asked once a size (1 us).
+@functools.lru_cache(maxsize=4096)
+def _attention_workspace(dev: int, *sizes) -> int:
+    return int(lib.nm_kv4_attention_workspace_bytes(*sizes))
+
+
+@functools.lru_cache(maxsize=4096)
+def _pages_workspace(dev: int, *sizes) -> int:
+    return int(lib.nm_kv_pages_workspace_bytes(*sizes))
+
+
+def _kv_workspace(query, dev: int, sizes: tuple, workspace: torch.Tensor | None):
+    """(tensor to hold on to, pointer, bytes).  A workspace that is given is checked by the call itself."""
     if workspace is None:
+        nbytes = query(dev, *sizes)
         if nbytes == 0:
             return None, None, 0
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
         return workspace, workspace.data_ptr(), nbytes
-    if workspace.get_device() != t.get_device() or not workspace.is_contiguous():
+    if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the same device")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
@@ -762,7 +780,7 @@ def nm_kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Ten
     elif lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != (T, Hq) or lse.stride(1) != 1:
         raise ValueError("lse must be fp32 [T, heads], contiguous in its last dimension, on q's device")
     b, S, room = _kv_batch(dev, cache, page_table, kv_len, q_start, page_size, n_kv, T, D)
-    ws, wp, wn = _kv_workspace(lib.nm_kv4_attention_workspace_bytes(T, S, Hq, n_kv, D, max_q_len, room), q, workspace)
+    ws, wp, wn = _kv_workspace(_attention_workspace, dev, (T, S, Hq, n_kv, D, max_q_len, room), workspace)
     _call(dev, lib.nm_kv4_attention, b, qr, Hq, max_q_len, D ** -0.5 if scale is None else scale, window,
           _kv_rows(out, "out", dev, shape), lse.data_ptr(), lse.stride(0) if T > 1 else Hq, wp, wn)
     return out, lse
@@ -776,8 +794,8 @@ def _kv_book(dev: int, page_table, kv_len, refcount, page_size, n_pairs, workspa
     """(nm_kv_book, S, workspace, its pointer and bytes), checked."""
     tp, ld, cols, S = _table(page_table, dev)
     N = refcount.numel()
-    b = _KV_BOOK.pack(tp, ld, _i32(kv_len, "kv_len", dev, S), S, _i32(refcount, "refcount", dev, N), N, cols, page_size)
-    return b, S, *_kv_workspace(lib.nm_kv_pages_workspace_bytes(S, n_pairs, N, cols), page_table, workspace)
+    b = _KV_BOOK.pack(tp, ld, _i32(kv_len, "kv_len", dev, (S,)), S, _i32(refcount, "refcount", dev, (N,)), N, cols, page_size)
+    return b, S, *_kv_workspace(_pages_workspace, dev, (S, n_pairs, N, cols), workspace)
 
 
 def nm_kv_resize(new_len: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, refcount: torch.Tensor,
@@ -787,8 +805,8 @@ def nm_kv_resize(new_len: torch.Tensor, page_table: torch.Tensor, kv_len: torch.
     kv_len int32 [S] and refcount int32 [num_pages].  moves int32 [S, 2] for nm_kv_copy_pages; missing int32 [1]."""
     dev = _where(page_table, "page_table")
     b, S, ws, wp, wn = _kv_book(dev, page_table, kv_len, refcount, page_size, 0, workspace)
-    _call(dev, lib.nm_kv_resize, b, _i32(new_len, "new_len", dev, S), _i32(moves, "moves", dev, S, 2),
-          _i32(missing, "missing", dev, 1), wp, wn)
+    _call(dev, lib.nm_kv_resize, b, _i32(new_len, "new_len", dev, (S,)), _i32(moves, "moves", dev, (S, 2)),
+          _i32(missing, "missing", dev, (1,)), wp, wn)
 
 
 def nm_kv_fork(parent: torch.Tensor, child: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
@@ -798,8 +816,8 @@ def nm_kv_fork(parent: torch.Tensor, child: torch.Tensor, page_table: torch.Tens
     for nm_kv_copy_pages; missing int32 [1]."""
     dev, n = _where(page_table, "page_table"), parent.numel()
     b, S, ws, wp, wn = _kv_book(dev, page_table, kv_len, refcount, page_size, n, workspace)
-    _call(dev, lib.nm_kv_fork, b, _i32(parent, "parent", dev, n), _i32(child, "child", dev, n), n,
-          _i32(moves, "moves", dev, n, 2), _i32(missing, "missing", dev, 1), wp, wn)
+    _call(dev, lib.nm_kv_fork, b, _i32(parent, "parent", dev, (n,)), _i32(child, "child", dev, (n,)), n,
+          _i32(moves, "moves", dev, (n, 2)), _i32(missing, "missing", dev, (1,)), wp, wn)
 
 
 def nm_kv_compact(page_table: torch.Tensor, kv_len: torch.Tensor, refcount: torch.Tensor, page_size: int,
@@ -807,7 +825,7 @@ def nm_kv_compact(page_table: torch.Tensor, kv_len: torch.Tensor, refcount: torc
     """Used pages into the lowest numbers.  moves int32 [max_moves, 2] for nm_kv_copy_pages; used int32 [1]."""
     dev, n = _where(page_table, "page_table"), moves.shape[0]
     b, S, ws, wp, wn = _kv_book(dev, page_table, kv_len, refcount, page_size, 0, workspace)
-    _call(dev, lib.nm_kv_compact, b, _i32(moves, "moves", dev, n, 2), n, _i32(used, "used", dev, 1), wp, wn)
+    _call(dev, lib.nm_kv_compact, b, _i32(moves, "moves", dev, (n, 2)), n, _i32(used, "used", dev, (1,)), wp, wn)
 
 
 def nm_kv_copy_pages(cache: torch.Tensor, moves: torch.Tensor) -> None:
@@ -821,4 +839,4 @@ def nm_kv_copy_pages(cache: torch.Tensor, moves: torch.Tensor) -> None:
     if cache.stride()[-2:] != (nbytes, 1):
         raise ValueError("the pages of a layer must be contiguous")
     n = moves.shape[0]
-    _call(dev, lib.nm_kv_copy_pages, cache.data_ptr(), N, nbytes, layers, stride, _i32(moves, "moves", dev, n, 2), n)
+    _call(dev, lib.nm_kv_copy_pages, cache.data_ptr(), N, nbytes, layers, stride, _i32(moves, "moves", dev, (n, 2)), n)
