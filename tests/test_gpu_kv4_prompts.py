@@ -185,3 +185,41 @@ def test_prompts_that_fill_the_machine(Hq, H, D):
         r = kv4.attention(q[t : t + 1], cache, table[s : s + 1], length, np.array([0, 1]), ps, H, D**-0.5, 0)
         bo, bl = attention_bounds(r)
         assert (np.abs(out[t] - r["out"][0]) <= bo[0]).all() and (np.abs(lse[t] - r["lse"][0]) <= bl[0]).all(), t
+
+
+def test_a_captured_batch_of_prompts_and_single_tokens():
+    """One graph; queries, lengths, rows and the page table change between its replays, each as the eager call."""
+    say("captured")
+    g = np.random.default_rng(3)
+    Hq, H, D, ps = 8, 2, 128, 64
+    T = 400 + extra(Hq)
+    plans = [([200, 1, 1, 90], [300, 9000, 64, 90]), ([1, 300, 2, 0], [700, 300, 5000, 80]), ([1, 1, 1, 1], [8000, 1, 0, 129]),
+             ([0, 0, 400, 0], [5, 5, 4000, 5])]
+    cols = 9000 // ps + 2
+    N = 160
+    cache = dev(filled_cache(g, N, ps, H, D))
+    q, table = torch.zeros((T, Hq, D), dtype=torch.bfloat16, device="cuda"), torch.zeros((4, cols), dtype=torch.int32, device="cuda")
+    kv_len, q_start = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (4, 5))
+    out, lse = torch.zeros_like(q), torch.zeros((T, Hq), device="cuda")
+    ws = torch.empty(nm.nm_kv4_attention_workspace_bytes(T, 4, Hq, H, D, 400, cols * ps), dtype=torch.uint8, device="cuda")
+    run = lambda o, e, w: nm.nm_kv4_attention(q, cache, table, kv_len, q_start, H, ps, 400, out=o, lse=e, workspace=w)  # noqa: E731
+    run(out, lse, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        run(out, lse, ws)
+    for i, (rows, lens) in enumerate(plans * 2):
+        q.copy_(torch.randn(q.shape, device="cuda"))
+        table.copy_(dev(g.integers(0, N, size=(4, cols)).astype(np.int32)))
+        kv_len.copy_(dev(np.array(lens, np.int32)))
+        q_start.copy_(dev(np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)))
+        eager = torch.full_like(q, 3.0), torch.full_like(lse, 3.0)
+        run(*eager, None)
+        out.fill_(3.0)
+        lse.fill_(3.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager[0]) and torch.equal(lse, eager[1]), f"replay {i}"
+        n = sum(rows)
+        assert torch.isfinite(out).all() and (out[n:] == 3).all() and (lse[n:] == 3).all()
