@@ -1196,9 +1196,12 @@ template <int D>
 hipError_t launch(Kv4Attention a, int64_t max_q, void *ws, hipStream_t st) {
     const int group = a.heads / a.b.f.n_kv;
     const int groups = device_cus() * kGroupsPerCu;
+    // Without a workspace (kv4_attention_workspace) nothing may be split between workgroups.
+    const int64_t row_tiles = whole_tiles(a.b.T, a.b.S, a.heads, a.b.f.n_kv);
+    a.whole = whole(row_tiles, groups, (int64_t)a.b.cols * a.b.f.page);
     // Where no sequence has many rows, or all rows make few row tiles for the machine's waves, every sequence is
     // walked by row tiles, split over its keys; else each is taken as its own rows ask for.
-    a.prompts = max_q * group > kDecodeRows && (int64_t)a.b.T * a.heads > (int64_t)groups * kWaves * kRows / kFewTiles;
+    a.prompts = !a.whole && max_q * group > kDecodeRows && (int64_t)a.b.T * a.heads > (int64_t)groups * kWaves * kRows / kFewTiles;
     Part<D> *parts = (Part<D> *)ws;
     PartTag *tags = (PartTag *)(parts + 2 * (size_t)groups);
     if (a.prompts) {
@@ -1208,9 +1211,7 @@ hipError_t launch(Kv4Attention a, int64_t max_q, void *ws, hipStream_t st) {
         if (first) kv4_join_kernel<D><<<first, 256, 0, st>>>(a, parts, tags);
         return hipGetLastError();
     }
-    const int64_t tiles = whole_tiles(a.b.T, a.b.S, a.heads, a.b.f.n_kv);
-    a.whole = whole(tiles, groups, (int64_t)a.b.cols * a.b.f.page);
-    const int grid = a.whole ? (int)tiles : groups;
+    const int grid = a.whole ? (int)row_tiles : groups;
     if (max_q * group <= kRows)
         kv4_decode_kernel<D, true><<<grid, kWaves * kWave, 0, st>>>(a, parts, tags);
     else
