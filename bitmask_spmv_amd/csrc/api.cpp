@@ -906,7 +906,8 @@ nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int 
                         who, (long long)T, n_heads, (long long)S, n_kv);
         if (window < 0 || max_q_len < 1)
             return fail(NM_ERR_SHAPE, "%s: window=%lld max_q_len=%lld", who, (long long)window, (long long)max_q_len);
-        if (!(scale - scale == 0.f)) return fail(NM_ERR_SHAPE, "%s: scale is not finite", who);
+        if (!(scale < 0x1p126f && scale > -0x1p126f))
+            return fail(NM_ERR_SHAPE, "%s: scale=%g is not below 2^126 in magnitude", who, (double)scale);
         if (T == 0) return NM_OK;  // no rows: their pointers may be NULL
         st = kv4_rows(who, "q", q, n_heads, head_dim, a.q);
         if (st == NM_OK) st = kv4_rows(who, "out", out, n_heads, head_dim, a.out);

@@ -60,6 +60,11 @@ struct Kv4Attention {
     int64_t ld_lse = 0;
     int heads = 0;
     float scale = 1.f;
+    // Scores are (2^fold q . K) times c / log2(e), c / log2(e) in [1, 2) times a scale above 1: products stay in
+    // range wherever the scores do.  Query bits: `keep` (none of them for a scale of 0), then `flip` the signs.
+    int fold = 0;
+    float c = 0.f;
+    uint32_t keep = 0, flip = 0;
     int64_t window = 0;  // keys a query looks back over, itself among them; 0: all
     bool whole = false;    // a workgroup to each row tile
     bool prompts = false;  // sequences of many rows are taken 128 rows at a time

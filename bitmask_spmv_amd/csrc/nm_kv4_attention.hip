@@ -29,6 +29,8 @@
 // a large buffer reaches 6.9.  Until half of the waves are through, 28 us after the start of the smaller one, the
 // walk itself reads 7.6 TB/s; the rest is the way to the first block (6 us: lengths, page table and bytes, each
 // waits for the one before), the waves that had to wait for the other one of their SIMD, and the join.
+#include <math.h>
+
 #include <atomic>
 
 #include "nm_device.h"
@@ -46,6 +48,7 @@ constexpr int kRows = 16;       // query rows of a tile
 // wait for memory, follow every new largest score at no cost: its weight is then 1, which bf16 holds
 // exactly (48 sequences of up to 8K tokens: 0.0019 off the 64-bit result, 0.0023 with the slack).
 constexpr float kSlack = 8.f;
+constexpr float kFar = 4096.f;  // reference (log2) up to which a rounded product of it is off by 2^-13 at most
 constexpr int kWaves = 4;       // waves per workgroup
 // Context up to which each row tile may be one workgroup's, which needs no second launch: 8 sequences of up to
 // 1000 tokens, 32 and 8 heads, 10.5 us against 11.8 split, of 2000 13.2 against 12.3; four times that where there are row
@@ -114,7 +117,8 @@ __device__ __forceinline__ uint32_t fp4_pair(uint32_t w, float s, int byte) {
 // neighbouring channels to about 13 bits below the largest of them: those of 4-bit and 6-bit
 // numbers always fit, those of 4-bit and 8-bit (E4M3) ones do not (two 8-bit pieces, at the
 // same matrix time, were measured 2^-17 of |q| |k| off).  Of a block with an infinity or NaN the
-// scales are NaN, and so is what its row gets.  `at`: the pieces' scales, a byte each.
+// scales are NaN, and so is what its row gets.  `at`: the pieces' scales, a byte each, for what is multiplied: queries
+// times 2^fold (of a score what is below 2^-127 of its key's largest channel may be lost).
 struct Pieces {
     u32x6 p[4];
     uint32_t at[4];
@@ -133,15 +137,14 @@ __device__ __forceinline__ Channels read_query(const uint16_t *from, bool real) 
     return x;
 }
 
-__device__ __forceinline__ Pieces split_query(Channels x, float scale) {
-    const uint32_t signs = scale < 0.f ? 0x80008000u : 0u;
+__device__ __forceinline__ Pieces split_query(Channels x, const Kv4Attention &a) {
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         top = max(top, max(x.w[i] & 0x7FFFu, (x.w[i] >> 16) & 0x7FFFu));
-        x.w[i] ^= signs;
+        x.w[i] = (x.w[i] & a.keep) ^ a.flip;
     }
-    const uint32_t e = max(top >> 7, 20u);  // biased exponent of the largest magnitude
+    const uint32_t e = max(top >> 7, (uint32_t)(20 - a.fold));  // biased exponent of the largest magnitude
     Pieces q;
     q.at[0] = e - 2;
     q.at[1] = e - 6;
@@ -159,7 +162,7 @@ __device__ __forceinline__ Pieces split_query(Channels x, float scale) {
         }
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) q.at[k] = e == 255u ? 255u : q.at[k];
+    for (int k = 0; k < 4; ++k) q.at[k] = e == 255u ? 255u : q.at[k] + a.fold;
     return q;
 }
 
@@ -173,8 +176,8 @@ struct Query {
 };
 
 template <int D>
-__device__ __forceinline__ Query<D> load_query(const uint16_t *row, bool real, float scale, int g) {
-    const Pieces x = split_query(read_query(row + (D == 128 ? g : (g & 1)) * 32, real), scale);
+__device__ __forceinline__ Query<D> load_query(const uint16_t *row, bool real, const Kv4Attention &a, int g) {
+    const Pieces x = split_query(read_query(row + (D == 128 ? g : (g & 1)) * 32, real), a);
     Query<D> q;
     if constexpr (D == 128) {
 #pragma unroll
@@ -384,7 +387,9 @@ __device__ __forceinline__ void scores(const Bytes<D> &x, const Query<D> &q, f32
 // What weights are relative to, as a power of two.
 __device__ __forceinline__ float reference(float m, float c) { return m == -INFINITY ? 0.f : m * c; }
 
-// Scores -> weights; O and l follow the reference.
+// Scores -> weights; O and l follow the reference.  The difference is taken before the product with c: the
+// product of a large score, rounded to be subtracted, would be off by more than a power of two (a subtraction more per
+// weight: 42.3 us against 41.9 for 48 sequences of up to 8K tokens, as in a branch for large scores).
 template <int D>
 __device__ __forceinline__ void weights(Tile<D> &t, f32x4 (&s)[4], float c) {
     float mx = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3]));
@@ -398,11 +403,11 @@ __device__ __forceinline__ void weights(Tile<D> &t, f32x4 (&s)[4], float c) {
         t.l *= keep;
         t.m = mn;
     }
-    const float mc = reference(t.m, c);
+    const float base = t.m == -INFINITY ? 0.f : t.m;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i], c, -mc));
+        for (int i = 0; i < 4; ++i) s[j][i] = __builtin_amdgcn_exp2f((s[j][i] - base) * c);
         t.l += (s[j][0] + s[j][1]) + (s[j][2] + s[j][3]);
     }
 }
@@ -547,7 +552,7 @@ __device__ __forceinline__ void decode(Kv4Attention &a, Part<D> *parts, PartTag 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int group = a.heads / f.n_kv;
     const Lane<D> ln(lane);
-    const float c = fmaxf(fabsf(a.scale), 1e-37f) * kLog2e;  // a scale of 0 leaves scores of 0
+    const float c = a.c;
     const int64_t cap = (int64_t)a.b.cols * f.page;
 
     // my run of units
@@ -616,7 +621,7 @@ __device__ __forceinline__ void decode(Kv4Attention &a, Part<D> *parts, PartTag 
         const int64_t r = (int64_t)tile * kRows + ln.col;
         const int qi = (int)r / group, t = sq.q0 + qi, h = head * group + ((int)r - qi * group);
         const bool real = r < (int64_t)sq.n * group && (uint32_t)t < (uint32_t)a.b.T;
-        const Query<D> q = load_query<D>(a.q.p + t * a.q.ld + h * a.q.hd, real, a.scale, ln.g);
+        const Query<D> q = load_query<D>(a.q.p + t * a.q.ld + h * a.q.hd, real, a, ln.g);
         // keys that my row sees: [from, upto]
         const int64_t place = (int64_t)sq.len - sq.n + qi;
         const int see_last = real ? (int)(place < cap ? place : cap - 1) : -1;
@@ -851,7 +856,7 @@ __device__ __forceinline__ void prompt(Kv4Attention &a, int tiles, Values<D> &va
     const int r0 = (vt - (int)((uint32_t)(q0 * group) / kPromptRows) - s) * kPromptRows;
     if (r0 < 0 || r0 >= rows) return;
 
-    const float c = fmaxf(fabsf(a.scale), 1e-37f) * kLog2e;
+    const float c = a.c;
     const int64_t room = (int64_t)a.b.cols * f.page;
     const int cap = len < room ? len : (int)room;  // tokens that have a place
     const int place0 = len - n;                    // of the sequence's first row
@@ -872,7 +877,7 @@ __device__ __forceinline__ void prompt(Kv4Attention &a, int tiles, Values<D> &va
     f32x16 o[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) o[i] = f32x16{};
-    float ref = -INFINITY, l = 0.f;  // what weights are relative to, a power of two, and their sum
+    float top = -INFINITY, off = 0.f, l = 0.f;  // weights are 2^((score - top) c - off); their sum
 
     // blocks that the workgroup walks, and those that need no mask for the wave
     auto place_of = [&](int r) { return place0 + (int)((uint32_t)min(r, rows - 1) / (uint32_t)group); };
@@ -923,7 +928,7 @@ __device__ __forceinline__ void prompt(Kv4Attention &a, int tiles, Values<D> &va
     PromptQuery<D> q;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-        const Pieces x = split_query(raw[k], a.scale);
+        const Pieces x = split_query(raw[k], a);
 #pragma unroll
         for (int i = 0; i < 4; ++i) q.p[k][i] = x.p[i];
         q.scales[k] = x.at[0] | x.at[1] << 8 | x.at[2] << 16 | x.at[3] << 24;
@@ -1005,23 +1010,36 @@ __device__ __forceinline__ void prompt(Kv4Attention &a, int tiles, Values<D> &va
             x = __builtin_amdgcn_fmed3f(__builtin_amdgcn_fmed3f(x, sc[i], INFINITY), sc[i + 1], INFINITY);
             y = __builtin_amdgcn_fmed3f(__builtin_amdgcn_fmed3f(y, sc[i + 2], INFINITY), sc[i + 3], INFINITY);
         }
-        return halves_max(fmaxf(x, y)) * c;
+        return halves_max(fmaxf(x, y));
     };
-    // A new reference where a score has passed the old one.  The first is the largest score itself + kSlack,
+    // A new reference where a score has passed the old one.  The first is the largest score itself and kSlack,
     // so that a lone key's weight is a power of two; the next ones lie whole powers of two from it, so that
-    // the weights w, which are rounded already and not yet multiplied, follow exactly.
-    auto raise = [&](float top, uint32_t (&w)[8]) {
-        if (__any(top > ref)) {
-            const float by = floorf(top - ref) + kSlack;
-            const float next = ref == -INFINITY ? top + kSlack : ref + by;
-            const float keep = top > ref ? __builtin_ldexpf(1.f, (int)fmaxf(-by, -1000.f)) : 1.f;
+    // the weights w, which are rounded already and not yet multiplied, follow exactly; of one so far behind
+    // that nothing remains, the largest score begins anew.
+    auto raise = [&](float x, uint32_t (&w)[8]) {
+        const float past = __builtin_fmaf(x - top, c, -off);  // NaN: neither has a key
+        if (__any(past > 0.f)) {
+            const float by = floorf(past) + kSlack;
+            const bool anew = by > 150.f, mine = past > 0.f;
+            const float keep = mine ? __builtin_ldexpf(1.f, (int)fmaxf(-by, -1000.f)) : 1.f;
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[i] *= keep;
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = pack_bf16(bf16_lo(w[i]) * keep, bf16_hi(w[i]) * keep);
             l *= keep;
-            if (top > ref) ref = next;
+            if (mine) off = anew ? kSlack : off + by;
+            if (mine && anew) top = x;
         }
+    };
+    // Scores sc to what the exponent is a product and a difference of: c times it, less the value returned.  Where a reference is
+    // far from 0 the product of a score, rounded to be subtracted, would be off by more than the weights'
+    // own rounding: there scores become differences first.
+    auto relative = [&](f32x16 &sc) {
+        const float base = top == -INFINITY ? 0.f : top, at = __builtin_fmaf(base, c, off);
+        if (__builtin_expect(!__any(fabsf(at) > kFar), 1)) return at;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sc[i] -= base;
+        return off;
     };
 
     // Tile t = 2 b + tt: between them, product by product, the values of tile t (weights w are ready), the scores
@@ -1031,7 +1049,7 @@ __device__ __forceinline__ void prompt(Kv4Attention &a, int tiles, Values<D> &va
         const u32x4 *from_lds = &values[b & 1][2 * tt][0][lane];
         hide(tt ? b + 1 : b, tt ^ 1, sc);
         raise(largest(sc), w);
-        const float mc = ref == -INFINITY ? 0.f : ref;
+        const float mc = relative(sc);
         if (tt == 0) hide_values(b + 1);
 
         constexpr int kRead = 3;  // value operands read ahead
@@ -1103,7 +1121,7 @@ __device__ __forceinline__ void prompt(Kv4Attention &a, int tiles, Values<D> &va
 #pragma unroll
             for (int k = 0; k < 8; ++k) wa[k] = 0;
             raise(largest(sa), wa);
-            const float mc = ref == -INFINITY ? 0.f : ref;
+            const float mc = relative(sa);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sa[2 * k], c, -mc));
@@ -1144,7 +1162,7 @@ __device__ __forceinline__ void prompt(Kv4Attention &a, int tiles, Values<D> &va
             }
             *reinterpret_cast<u32x4 *>(out + (8 * i + 4 * hh + j) * 8) = w;
         }
-    if (hh == 0 && a.lse) a.lse[t * a.ld_lse + h] = l != 0.f ? (ref + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    if (hh == 0 && a.lse) a.lse[t * a.ld_lse + h] = l != 0.f ? (__builtin_fmaf(top, c, off) + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
 // The first `groups` workgroups walk the sequences of few rows, the others take the prompts: while the ones
@@ -1228,7 +1246,13 @@ size_t kv4_attention_workspace(int64_t T, int64_t S, int heads, int n_kv, int di
     return dim == 128 ? decode_workspace<128>(groups) : decode_workspace<64>(groups);
 }
 
-hipError_t launch_kv4_attention(const Kv4Attention &a, int64_t max_q, void *ws, hipStream_t st) {
+hipError_t launch_kv4_attention(const Kv4Attention &given, int64_t max_q, void *ws, hipStream_t st) {
+    Kv4Attention a = given;
+    const float size = fabsf(a.scale);
+    a.fold = size > 0.f && size < 1.f ? ilogbf(size) : 0;
+    a.c = size > 0.f ? ldexpf(size, -a.fold) * kLog2e : kLog2e;
+    a.keep = size > 0.f ? ~0u : 0u;
+    a.flip = a.scale < 0.f ? 0x80008000u : 0u;
     return a.b.f.dim == 128 ? launch<128>(a, max_q, ws, st) : launch<64>(a, max_q, ws, st);
 }
 
