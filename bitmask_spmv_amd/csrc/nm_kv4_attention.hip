@@ -44,7 +44,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kBlock = 64;      // tokens a wave takes at a time
 constexpr int kRows = 16;       // query rows of a tile
 // Prompts: O is rescaled only when a score passes the largest one so far by 2^kSlack; weights are kept
-// relative to that point, so that they stay at or below 1 (and O below keys times the largest value).  Row tiles, which
+// relative to that point, so that they stay at or below 1.  Row tiles, which
 // wait for memory, follow every new largest score at no cost: its weight is then 1, which bf16 holds
 // exactly (48 sequences of up to 8K tokens: 0.0019 off the 64-bit result, 0.0023 with the slack).
 constexpr float kSlack = 8.f;
@@ -384,6 +384,11 @@ __device__ __forceinline__ void scores(const Bytes<D> &x, const Query<D> &q, f32
 #undef NM_KV4_DOT
 }
 
+// Values are multiplied as 2^-spare(keys) of what they are: weights are at most 1, so O stays below the largest
+// value, and in range whatever the values are; the factor leaves with the sum of the weights.
+__device__ __forceinline__ int spare(int keys) { return keys > 0 ? 32 - __clz(keys) : 0; }
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
 // What weights are relative to, as a power of two.
 __device__ __forceinline__ float reference(float m, float c) { return m == -INFINITY ? 0.f : m * c; }
 
@@ -412,9 +417,9 @@ __device__ __forceinline__ void weights(Tile<D> &t, f32x4 (&s)[4], float c) {
     }
 }
 
-// O += V^T P for 64 tokens.
+// O += V^T P for 64 tokens, values times `down`.
 template <int D>
-__device__ __forceinline__ void add_values(Tile<D> &t, const Bytes<D> &x, const f32x4 (&p)[4], int col) {
+__device__ __forceinline__ void add_values(Tile<D> &t, const Bytes<D> &x, const f32x4 (&p)[4], float down, int col) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         union { uint32_t w[4]; bf16x8 h; } b;
@@ -428,7 +433,7 @@ __device__ __forceinline__ void add_values(Tile<D> &t, const Bytes<D> &x, const 
         for (int e = 0; e < 8; ++e) {
             w[e] = x.v[2 * s + (e >> 2)][e & 3];
             if (D == 64) w[e] >>= (col & 1) * 16;
-            f[e] = scale_field(x.vs[2 * s + (e >> 2)], e & 3);
+            f[e] = scale_field(x.vs[2 * s + (e >> 2)], e & 3) * down;
         }
 #pragma unroll
         for (int by = 0; by < D / 32; ++by) {
@@ -450,8 +455,8 @@ __device__ __forceinline__ void add_values(Tile<D> &t, const Bytes<D> &x, const 
 // Lane's channel of o[mt][i]: (D/4) g + (D/16) i + mt.
 template <int D>
 __device__ __forceinline__ void store_row(const Kv4Attention &a, int t, int h, int g, const float *o, float m, float l,
-                                          bool with_lse) {
-    const float inv = l != 0.f ? 1.f / l : 0.f;
+                                          float up, bool with_lse) {
+    const float inv = l != 0.f ? up / l : 0.f;
     uint16_t *p = a.out.p + t * a.out.ld + h * a.out.hd + g * (D / 4);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
@@ -477,6 +482,7 @@ enum : int { kNone = 0, kEnds = 1, kThrough = 2 };  // the item's last block is 
 struct PartTag {
     int state;                  // kNone, kEnds, kThrough
     int q0, head, tile, rows;   // the sequence's first row, the row tile and its rows
+    int spare;                  // O is 2^-spare of what it is
 };
 
 template <int D>
@@ -535,7 +541,7 @@ struct Join {
         const int r = tag.tile * kRows + row;
         const int t = tag.q0 + r / group, h = tag.head * group + r % group;
         if ((uint32_t)t >= (uint32_t)a.b.T) return;
-        const float inv = l != 0.f ? 1.f / l : 0.f;
+        const float inv = l != 0.f ? pow2(tag.spare) / l : 0.f;
         uint32_t *p = reinterpret_cast<uint32_t *>(a.out.p + t * a.out.ld + h * a.out.hd + c * N);
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) p[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
@@ -632,6 +638,8 @@ __device__ __forceinline__ void decode(Kv4Attention &a, Part<D> *parts, PartTag 
         const int64_t some = (int64_t)sq.len - sq.n - a.window + 1;
         const int any_first = a.window > 0 && some > 0 ? (int)some : 0;
         const int any_last = (int)((int64_t)sq.len < cap ? (int64_t)sq.len : cap) - 1;
+        const int bits = spare(any_last + 1);
+        const float down = pow2(-bits);
 
         Tile<D> tl;
         clear(tl);
@@ -651,7 +659,7 @@ __device__ __forceinline__ void decode(Kv4Attention &a, Part<D> *parts, PartTag 
                     }
             }
             weights(tl, sc, c);
-            add_values(tl, x, sc, ln.col);
+            add_values(tl, x, sc, down, ln.col);
         };
         // Behind the last block the loads, which are not branched around, go to the cache's first
         // bytes for all waves: a block more of each run's own would be a tenth more traffic at 10 blocks a run (48
@@ -677,13 +685,13 @@ __device__ __forceinline__ void decode(Kv4Attention &a, Part<D> *parts, PartTag 
 #pragma unroll
                 for (int m = 0; m < D / 16; ++m) o[(D / 16) * i + m] = tl.o[m][i];
             const float l = cross_rows_sum(tl.l);
-            if (real) store_row<D>(a, t, h, ln.g, o, reference(tl.m, c), l, ln.g == 0);
+            if (real) store_row<D>(a, t, h, ln.g, o, reference(tl.m, c), l, pow2(bits), ln.g == 0);
         } else {
             const int slot = begins ? 1 : 0;
             keep_part(sh.part[wave][slot], tl, c, ln);
             const int64_t left = (int64_t)sq.n * group - (int64_t)tile * kRows;
             if (lane == 0)
-                sh.tag[wave][slot] = {ends ? kEnds : kThrough, sq.q0, head, tile, (int)(left < kRows ? left : kRows)};
+                sh.tag[wave][slot] = {ends ? kEnds : kThrough, sq.q0, head, tile, (int)(left < kRows ? left : kRows), bits};
         }
     }
     __syncthreads();
@@ -865,6 +873,7 @@ __device__ __forceinline__ void prompt(Kv4Attention &a, int tiles, Values<D> &va
     auto first_of = [&](int place) { return window && place >= window ? place - window + 1 : 0; };
     auto last_of = [&](int place) { return place < cap ? place : cap - 1; };
     const int any_from = first_of(place0), any_upto = cap - 1;
+    const float down = pow2(-spare(cap));
 
     const int w0 = r0 + wave * kPromptTile;  // the wave's first row
     const int r = w0 + col;
@@ -947,7 +956,7 @@ __device__ __forceinline__ void prompt(Kv4Attention &a, int tiles, Values<D> &va
     };
     // token e of the eight, byte byte0 + by of its word; then the channels 2 (byte0 + by) and the next of all of them
     auto convert = [&](int by, int e) {
-        return fp4_pair(vx[e >> 2][e & 3] >> (8 * byte0), scale_field(vs[e >> 2], e & 3), by);
+        return fp4_pair(vx[e >> 2][e & 3] >> (8 * byte0), scale_field(vs[e >> 2], e & 3) * down, by);
     };
     auto put_values = [&](int by, const u32x4 &even, const u32x4 &odd, u32x4 (*to)[MT][kWave]) {
         if constexpr (D == 128) {
@@ -1144,7 +1153,7 @@ __device__ __forceinline__ void prompt(Kv4Attention &a, int tiles, Values<D> &va
     }
     l = halves_sum(l);
     if (!real) return;
-    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? pow2(spare(cap)) / l : 0.f;
     uint16_t *out = a.out.p + t * a.out.ld + h * a.out.hd;
     // the lane's rows m = 8 i + 4 hh + j of every channel tile
 #pragma unroll

@@ -1,5 +1,5 @@
-"""Attention over the 4-bit cache at the ends of what numbers hold: the largest keys that nm_kv4_append
-stores, scores of any size below 2^125, scales of any size.  Calls of few rows (row tiles) and the kernel
+"""Attention over the 4-bit cache at the ends of what numbers hold: the largest and smallest keys and values that
+nm_kv4_append stores, scores of any size below 2^125, scales of any size.  Calls of few rows (row tiles) and the kernel
 that takes prompts."""
 from __future__ import annotations
 
@@ -33,6 +33,49 @@ def scale_bytes(cache, H, ps, D, values):
     x = cache.reshape(len(cache), H, -1)
     at = ps * D + (ps * D // 32 if values else 0)
     return x[:, :, at : at + ps * D // 32]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", WAYS)
+@pytest.mark.parametrize("n", [81, 700, 5000])
+@pytest.mark.parametrize("equal", [False, True])
+def test_values_near_the_largest_number(D, rows, n, equal):
+    """Values of one sign up to 6 * 2^125: their weighted mean is a number whatever their count.  With queries of 0
+    the weights are all alike."""
+    say("largest values", D, rows, n, equal)
+    g = np.random.default_rng(n + rows)
+    H, Hq, ps = 1, 4, 64
+    table, kv_len, q_start, N = batch(g, [rows], [n], ps)
+    cache = filled_cache(g, N, ps, H, D, 118, 126)
+    cache.reshape(N, H, -1)[:, :, ps * D // 2 : ps * D] &= 0x77
+    scale_bytes(cache, H, ps, D, True)[:] = g.integers(250, 253, size=(N, H, ps * D // 32), dtype=np.uint8)
+    q = queries(np.zeros((rows, Hq, D)) if equal else bf16(g.standard_normal((rows, Hq, D))), rows)
+    r = kv4.attention(q, cache, table, kv_len, q_start, ps, H, D**-0.5, 0)
+    held_to(*run_attention(q, cache, table, kv_len, q_start, H, ps, rows), r, f"D{D} rows {rows} n {n}")
+
+
+@pytest.mark.parametrize("rows", WAYS)
+@pytest.mark.parametrize("n", [81, 3000])
+def test_values_near_the_smallest_number(rows, n):
+    """Values of 2^-112 to 6 * 2^-111 among thousands of others: weights times values are not normal numbers.
+
+    A weight is between 2^-8 and 1 for the largest score, times 2^-13 at most for 3000 keys (room for their sum); an
+    fp32 sum of what is below 2^-126 is kept in steps of 2^-149.  n products are then off by half a step each, that is
+    n * 2^-150 over weights that sum to at least 2^-21: n * 2^-129."""
+    say("smallest values", rows, n)
+    g = np.random.default_rng(n)
+    H, Hq, D, ps = 1, 4, 128, 64
+    table, kv_len, q_start, N = batch(g, [rows], [n], ps)
+    cache = filled_cache(g, N, ps, H, D, 118, 126)
+    scale_bytes(cache, H, ps, D, True)[:] = 16
+    q = queries(bf16(g.standard_normal((rows, Hq, D))), rows)
+    r = kv4.attention(q, cache, table, kv_len, q_start, ps, H, D**-0.5, 0)
+    out, lse = run_attention(q, cache, table, kv_len, q_start, H, ps, rows)
+    held_to(out, lse, r, "smallest values")
+    ro, ra = r["out"][:rows], r["absum"][:rows]
+    delta = 2.0**-20 * r["srow"] + 140 * 2.0**-24 * r["smax"] + 2.0**-22
+    rel = (2.0**-8 + 2 * delta + 2.0**-23 * (n + 64))[:rows, :, None]
+    assert (np.abs(out[:rows] - ro) <= 2.0**-8 * np.abs(ro) + 1.01 * rel * ra + n * 2.0**-129).all()
 
 
 @pytest.mark.parametrize("D", [64, 128])
