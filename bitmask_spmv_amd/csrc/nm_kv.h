@@ -3,6 +3,7 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -59,15 +60,21 @@ struct Kv4Attention {
     float *lse = nullptr;
     int64_t ld_lse = 0;
     int heads = 0;
-    float scale = 1.f;
     // Scores are (2^fold q . K) times c / log2(e), c / log2(e) in [1, 2) times a scale above 1: products stay in
-    // range wherever the scores do.  Query bits: `keep` (none of them for a scale of 0), then `flip` the signs.
-    int fold = 0;
+    // range wherever the scores do.
     float c = 0.f;
-    uint32_t keep = 0, flip = 0;
+    int16_t fold = 0;
+    bool minus = false, zero = false;  // a scale below 0, of 0
     int64_t window = 0;  // keys a query looks back over, itself among them; 0: all
     bool whole = false;    // a workgroup to each row tile
     bool prompts = false;  // sequences of many rows are taken 128 rows at a time
+    void set_scale(float scale) {
+        const float size = fabsf(scale);
+        minus = scale < 0.f;
+        zero = scale == 0.f;
+        fold = size > 0.f && size < 1.f ? (int16_t)ilogbf(size) : 0;
+        c = (zero ? 1.f : ldexpf(size, -fold)) * 1.4426950408889634f;
+    }
 };
 
 hipError_t launch_kv4_append(const Kv4Batch &b, const Kv4Rows &k, const Kv4Rows &v, hipStream_t st);

@@ -29,8 +29,6 @@
 // a large buffer reaches 6.9.  Until half of the waves are through, 28 us after the start of the smaller one, the
 // walk itself reads 7.6 TB/s; the rest is the way to the first block (6 us: lengths, page table and bytes, each
 // waits for the one before), the waves that had to wait for the other one of their SIMD, and the join.
-#include <math.h>
-
 #include <atomic>
 
 #include "nm_device.h"
@@ -39,7 +37,6 @@
 namespace nmk {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kBlock = 64;      // tokens a wave takes at a time
 constexpr int kRows = 16;       // query rows of a tile
@@ -138,11 +135,12 @@ __device__ __forceinline__ Channels read_query(const uint16_t *from, bool real) 
 }
 
 __device__ __forceinline__ Pieces split_query(Channels x, const Kv4Attention &a) {
+    const uint32_t keep = a.zero ? 0u : ~0u, flip = a.minus ? 0x80008000u : 0u;
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         top = max(top, max(x.w[i] & 0x7FFFu, (x.w[i] >> 16) & 0x7FFFu));
-        x.w[i] = (x.w[i] & a.keep) ^ a.flip;
+        x.w[i] = (x.w[i] & keep) ^ flip;
     }
     const uint32_t e = max(top >> 7, (uint32_t)(20 - a.fold));  // biased exponent of the largest magnitude
     Pieces q;
@@ -1255,13 +1253,7 @@ size_t kv4_attention_workspace(int64_t T, int64_t S, int heads, int n_kv, int di
     return dim == 128 ? decode_workspace<128>(groups) : decode_workspace<64>(groups);
 }
 
-hipError_t launch_kv4_attention(const Kv4Attention &given, int64_t max_q, void *ws, hipStream_t st) {
-    Kv4Attention a = given;
-    const float size = fabsf(a.scale);
-    a.fold = size > 0.f && size < 1.f ? ilogbf(size) : 0;
-    a.c = size > 0.f ? ldexpf(size, -a.fold) * kLog2e : kLog2e;
-    a.keep = size > 0.f ? ~0u : 0u;
-    a.flip = a.scale < 0.f ? 0x80008000u : 0u;
+hipError_t launch_kv4_attention(const Kv4Attention &a, int64_t max_q, void *ws, hipStream_t st) {
     return a.b.f.dim == 128 ? launch<128>(a, max_q, ws, st) : launch<64>(a, max_q, ws, st);
 }
 
