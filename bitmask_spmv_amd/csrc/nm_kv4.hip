@@ -29,6 +29,24 @@ __device__ __forceinline__ int find_seq(const int32_t *q_start, int S, int t, in
     return lo;
 }
 
+// The same for a lane's row t < q_start[S], from the sequence s of the wave's first row t0.  Most rows are of s as well, or of
+// the sequence as far behind it as the row is (single tokens): both are looked at at once.  Else in steps that
+// double, and back: a few looks however many sequences without rows lie between.
+__device__ __forceinline__ int seq_of_row(const int32_t *q_start, int S, int s, int t0, int t) {
+    const int guess = min(s + (t - t0), S - 1);
+    const int next = q_start[s + 1], from = q_start[guess], end = q_start[guess + 1];
+    if (t < next) return s;
+    if (from <= t && t < end) return guess;
+    int step = 1;
+    while (step < S - s && q_start[s + step] <= t) {
+        s += step;
+        step *= 2;
+    }
+    for (; step > 0; step >>= 1)
+        if (step < S - s && q_start[s + step] <= t) s += step;
+    return s;
+}
+
 // Where row t is kept: the head-0 block of its page and its token within the page; null
 // where the sequence has no place or no valid page for it.
 __device__ __forceinline__ uint8_t *place_of(const Kv4Batch &b, int s, int t, int &tok) {
@@ -107,9 +125,9 @@ __global__ __launch_bounds__(kThreads) void kv4_rows_kernel(Kv4Batch b, Kv4Rows 
             }
     };
     if (WRITE) load(h0);
-    int s = find_seq(b.q_start, b.S, t0, lane);
+    const int s0 = find_seq(b.q_start, b.S, t0, lane);
     if (t >= b.T || t >= b.q_start[b.S]) return;
-    while (s + 1 < b.S && b.q_start[s + 1] <= t) ++s;
+    const int s = seq_of_row(b.q_start, b.S, s0, t0, t);
     int tok = 0;
     uint8_t *page = place_of(b, s, t, tok);
     if (WRITE && !page) return;  // all lanes of a row leave together

@@ -1,0 +1,71 @@
+"""Batches of the 4-bit cache that are far from the usual ones."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv4
+from tests.gpu_util import bf16_as_f64, dev_bf16, host_bf16, say
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - CPU container
+    pytest.skip("needs a HIP GPU", allow_module_level=True)
+
+import bitmask_spmv_amd as nm  # noqa: E402
+from tests.kv4_util import bf16, bits  # noqa: E402
+from tests.test_gpu_kv4 import dev  # noqa: E402
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("S,used", [(1000, [0, 999]), (1000, [0, 1, 63, 64, 65, 500, 998]), (130, [128, 129]), (4097, [7, 4000, 4096])])
+def test_rows_of_sequences_far_apart(D, S, used):
+    """A wave's rows belong to sequences with many without rows between them."""
+    say("far apart", D, S, used)
+    g = np.random.default_rng(S)
+    H, ps = 2, 64
+    n = np.zeros(S, dtype=np.int64)
+    n[used] = g.integers(1, 4, size=len(used))
+    q_start = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+    kv_len = (n + g.integers(0, 60, size=S)).astype(np.int32)
+    table = np.full((S, 1), -1, np.int32)
+    table[used, 0] = g.permutation(len(used) + 2)[: len(used)]
+    T = int(q_start[-1])
+    k, v = (bf16(g.standard_normal((T, H, D))) for _ in range(2))
+    cache = g.integers(0, 250, size=(len(used) + 2, kv4.page_bytes(ps, H, D)), dtype=np.uint8)
+    cd, args = dev(cache), (dev(table), dev(kv_len), dev(q_start), ps)
+    nm.nm_kv4_append(dev_bf16(bits(k)), dev_bf16(bits(v)), cd, *args)
+    kv4.append(cache, k, v, table, kv_len, q_start, ps)
+    assert (cd.cpu().numpy() == cache).all()
+    ko, vo = (torch.full((T, H, D), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    nm.nm_kv4_unpack(cd, *args, ko, vo)
+    kr, vr = kv4.rows_of(cache, table, kv_len, q_start, ps, H, D, T)
+    assert (bf16_as_f64(host_bf16(ko)) == kr).all() and (bf16_as_f64(host_bf16(vo)) == vr).all()
+
+
+def test_two_rows_at_the_ends_of_a_million_slots():
+    """The search for a row's sequence takes a few looks, not one for each of the slots between two rows of a
+    wave: 10 ms are a thousand times what the call takes, and a tenth of a million reads one after the other."""
+    say("a million slots")
+    S, H, D, ps = 1 << 20, 2, 128, 64
+    q_start = torch.ones(S + 1, dtype=torch.int32, device="cuda")
+    q_start[0], q_start[-1] = 0, 2
+    kv_len = torch.full((S,), 1, dtype=torch.int32, device="cuda")
+    table = torch.zeros((S, 1), dtype=torch.int32, device="cuda")
+    table[-1] = 1
+    x = torch.randn((2, H, D), device="cuda").to(torch.bfloat16)
+    cache = torch.zeros((2, kv4.page_bytes(ps, H, D)), dtype=torch.uint8, device="cuda")
+    a, b = torch.empty_like(x), torch.empty_like(x)
+    t0, t1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    for again in range(2):
+        torch.cuda.synchronize()
+        t0.record()
+        nm.nm_kv4_append(x, x, cache, table, kv_len, q_start, ps)
+        nm.nm_kv4_unpack(cache, table, kv_len, q_start, ps, a, b)
+        t1.record()
+        torch.cuda.synchronize()
+    want = kv4.dequantize(*kv4.quantize(bf16_as_f64(host_bf16(x))))
+    assert (bf16_as_f64(host_bf16(a)) == want).all() and (bf16_as_f64(host_bf16(b)) == want).all()
+    assert int(cache.any(1).sum()) == 2
+    assert t0.elapsed_time(t1) < 10, f"{t0.elapsed_time(t1)} ms"
