@@ -710,10 +710,14 @@ def _kv_batch(dev: int, cache: torch.Tensor, page_table, kv_len, q_start, page_s
                            _i32(q_start, "q_start", dev, (S + 1,)), S, T, cols, page_size, n_kv, D), S, cols * page_size
 
 
-# Bytes that a call of some sizes on device `dev` needs: a function of them alone, asked once a size (1 us).
+# Bytes that a call of some sizes on device `dev` needs: a function of them alone, asked once a size (1 us), with
+# that device the current one (attention's depends on its compute units).
 @functools.lru_cache(maxsize=4096)
 def _attention_workspace(dev: int, *sizes) -> int:
-    return int(lib.nm_kv4_attention_workspace_bytes(*sizes))
+    if dev == _current_device():
+        return int(lib.nm_kv4_attention_workspace_bytes(*sizes))
+    with torch.cuda.device(dev):
+        return int(lib.nm_kv4_attention_workspace_bytes(*sizes))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -759,7 +763,7 @@ def nm_kv4_unpack(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.T
 
 def nm_kv4_attention_workspace_bytes(T: int, S: int, n_heads: int, n_kv: int, head_dim: int, max_q_len: int,
                                      room: int) -> int:
-    """room: tokens that a row of the page table has room for (columns * page_size)."""
+    """For calls on the current device.  room: tokens that a row of the page table has room for (columns * page_size)."""
     return int(lib.nm_kv4_attention_workspace_bytes(T, S, n_heads, n_kv, head_dim, max_q_len, room))
 
 

@@ -1,6 +1,8 @@
 """Arguments of the 4-bit cache at the ends of their ranges (no GPU needed)."""
 from __future__ import annotations
 
+import contextlib
+
 import pytest
 
 from tests.test_abi_kv4_host import L, SHAPE, call  # noqa: F401
@@ -9,3 +11,32 @@ from tests.test_abi_kv4_host import L, SHAPE, call  # noqa: F401
 @pytest.mark.parametrize("scale", [2.0**126, -(2.0**126), 3.0e38])
 def test_a_scale_whose_scores_pass_fp32_is_refused(L, scale):  # noqa: F811
     assert call(L, "nm_kv4_attention", scale=scale) == SHAPE
+
+
+def test_workspace_sizes_are_asked_on_the_device_of_the_call(monkeypatch):
+    """Two devices of different size: what a call on the second needs is not what the current one would."""
+    import bitmask_spmv_amd as nm
+
+    at = [0]
+
+    class Library:
+        def nm_kv4_attention_workspace_bytes(self, *sizes):
+            return 1000 + at[0]
+
+    @contextlib.contextmanager
+    def device(d):
+        before, at[0] = at[0], d
+        yield
+        at[0] = before
+
+    monkeypatch.setattr(nm, "lib", Library())
+    monkeypatch.setattr(nm, "_current_device", lambda: at[0])
+    monkeypatch.setattr(nm.torch.cuda, "device", device)
+    nm._attention_workspace.cache_clear()
+    try:
+        sizes = (5, 3, 8, 2, 128, 1, 4096)
+        for d in (1, 0, 1):
+            assert nm._attention_workspace(d, *sizes) == 1000 + d
+            assert at == [0]
+    finally:
+        nm._attention_workspace.cache_clear()
