@@ -923,7 +923,7 @@ nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int 
         a.heads = n_heads;
         a.set_scale(scale);
         a.window = std::min(window, (int64_t)1 << 40);  // longer than any sequence
-        hipError_t e = nmk::launch_kv4_attention(a, max_q_len, workspace, (hipStream_t)hip_stream);
+        hipError_t e = nmk::launch_kv4_attention(a, std::min(max_q_len, T), workspace, (hipStream_t)hip_stream);
         return e == hipSuccess ? NM_OK : hip_fail(who, e);
     } catch (...) {
         return fail(NM_ERR_HIP, "nm_kv4_attention: internal error");

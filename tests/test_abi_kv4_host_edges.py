@@ -2,15 +2,23 @@
 from __future__ import annotations
 
 import contextlib
+import os
 
 import pytest
 
-from tests.test_abi_kv4_host import L, SHAPE, call  # noqa: F401
+from tests.test_abi_kv4_host import HIP, L, SHAPE, call  # noqa: F401
 
 
 @pytest.mark.parametrize("scale", [2.0**126, -(2.0**126), 3.0e38])
 def test_a_scale_whose_scores_pass_fp32_is_refused(L, scale):  # noqa: F811
     assert call(L, "nm_kv4_attention", scale=scale) == SHAPE
+
+
+@pytest.mark.skipif(os.path.exists("/dev/kfd"), reason="would be launched, with addresses that are none")
+def test_any_hint_reaches_the_launch(L):  # noqa: F811
+    """As many rows as the type holds: with no device to launch on, that is all that is wrong."""
+    for hint in ((1 << 63) - 1, 1 << 61, 1 << 40):
+        assert call(L, "nm_kv4_attention", max_q_len=hint) == HIP
 
 
 def test_workspace_sizes_are_asked_on_the_device_of_the_call(monkeypatch):

@@ -15,7 +15,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
 
 import bitmask_spmv_amd as nm  # noqa: E402
 from tests.kv4_util import bf16, bits  # noqa: E402
-from tests.test_gpu_kv4 import dev  # noqa: E402
+from tests.test_gpu_kv4 import attention_case, dev  # noqa: E402
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -69,3 +69,9 @@ def test_two_rows_at_the_ends_of_a_million_slots():
     assert (bf16_as_f64(host_bf16(a)) == want).all() and (bf16_as_f64(host_bf16(b)) == want).all()
     assert int(cache.any(1).sum()) == 2
     assert t0.elapsed_time(t1) < 10, f"{t0.elapsed_time(t1)} ms"
+
+
+@pytest.mark.parametrize("hint", [1 << 40, 1 << 61, (1 << 63) - 1])
+def test_a_hint_of_any_size(hint):
+    say("hint", hint)
+    attention_case(5, [3, 1], [70, 33], 8, 2, 128, 64, max_q=hint)
