@@ -795,7 +795,8 @@ static bool kv_page_size_ok(int p) { return p == 64 || p == 128 || p == 256 || p
 
 // Checks of a ragged batch over a cache, shared by append, unpack and attention.
 static nm_status kv4_batch(const char *who, const nm_kv4_batch *p, nmk::Kv4Batch &b) {
-    if (!p || !p->cache || !p->page_table || !p->kv_len || !p->q_start) return fail(NM_ERR_NULL, "%s: NULL pointer", who);
+    if (!p || !p->cache || !p->q_start || (p->S != 0 && (!p->page_table || !p->kv_len)))  // of no sequences: no arrays
+        return fail(NM_ERR_NULL, "%s: NULL pointer", who);
     if (p->head_dim != 64 && p->head_dim != 128)
         return fail(NM_ERR_SHAPE, "%s: head_dim=%d is not 64 or 128", who, p->head_dim);
     if (!kv_page_size_ok(p->page_size))

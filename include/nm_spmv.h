@@ -419,7 +419,8 @@ nm_status nm_stream_read(const void *buf, size_t bytes, uint32_t *sink, size_t s
  * as zeros (unpack) and is left out (attention).  Rows from q_start[S] to T are not touched.
  * Token arrays (nm_kv4_rows) are bf16 [T][heads][D] with element strides ld (token) and hd
  * (head), both multiples of 8, the base 16-byte aligned.  T <= 2^24, S <= 2^20, n_kv <= 256;
- * T = 0 is allowed (the rows' pointers may then be NULL).  The cache is 16-byte aligned.
+ * T = 0 is allowed (the rows' pointers may then be NULL), and S = 0 with it (page_table and kv_len may
+ * then be NULL).  The cache is 16-byte aligned.
  *
  * nm_kv4_append -- stores rows of k and v.  Per block of 32 channels, with E the biased
  * exponent of the largest magnitude a and m its significand in [1, 2):

@@ -6,12 +6,19 @@ import os
 
 import pytest
 
-from tests.test_abi_kv4_host import HIP, L, SHAPE, call  # noqa: F401
+from tests.test_abi_kv4_host import HIP, L, OK, SHAPE, call  # noqa: F401
 
 
 @pytest.mark.parametrize("scale", [2.0**126, -(2.0**126), 3.0e38])
 def test_a_scale_whose_scores_pass_fp32_is_refused(L, scale):  # noqa: F811
     assert call(L, "nm_kv4_attention", scale=scale) == SHAPE
+
+
+def test_no_sequences_have_no_arrays(L):  # noqa: F811
+    """An array of no elements may have no address: the table's and the lengths' of no sequences."""
+    for name in ("nm_kv4_append", "nm_kv4_unpack", "nm_kv4_attention"):
+        assert call(L, name, S=0, T=0, page_table=None, kv_len=None) == OK, name
+        assert call(L, name, S=0, T=1, page_table=None, kv_len=None) == SHAPE, name
 
 
 @pytest.mark.skipif(os.path.exists("/dev/kfd"), reason="would be launched, with addresses that are none")

@@ -75,3 +75,14 @@ def test_two_rows_at_the_ends_of_a_million_slots():
 def test_a_hint_of_any_size(hint):
     say("hint", hint)
     attention_case(5, [3, 1], [70, 33], 8, 2, 128, 64, max_q=hint)
+
+
+def test_no_sequences():
+    say("no sequences")
+    cache = torch.zeros((2, kv4.page_bytes(64, 1, 64)), dtype=torch.uint8, device="cuda")
+    table, kv_len, q_start = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in ((0, 1), 0, 1))
+    x = torch.empty((0, 1, 64), dtype=torch.bfloat16, device="cuda")
+    nm.nm_kv4_append(x, x, cache, table, kv_len, q_start, 64)
+    nm.nm_kv4_unpack(cache, table, kv_len, q_start, 64, x, x)
+    out, lse = nm.nm_kv4_attention(x, cache, table, kv_len, q_start, 1, 64, 1)
+    assert out.shape == (0, 1, 64) and lse.shape == (0, 1) and int(cache.sum()) == 0
