@@ -426,8 +426,10 @@ nm_status nm_stream_read(const void *buf, size_t bytes, uint32_t *sink, size_t s
  * exponent of the largest magnitude a and m its significand in [1, 2):
  *     e = min(max(E - 2 + (m > 1.75), 16), 252);
  * values are rounded to the nearest E2M1 multiple of 2^(e - 127), ties to the even code,
- * magnitudes above 6 to 6; an infinity or NaN is kept as 6 * 2^125 with its sign.  Two rows of one call at the same place (a page shared by two
- * sequences: see nm_kv_resize) leave one of the two there, token by token and head by head.
+ * magnitudes above 6 to 6; an infinity or NaN is kept as 6 * 2^125 with its sign.
+ * Two rows of one call for the same place (two sequences that write into a page they share:
+ * nm_kv_resize gives each a page of its own first) leave there values of the one and scales of the
+ * other, as it happens: finite numbers, in that place alone.
  *
  * nm_kv4_unpack -- the same rows of the cache as bf16 (exact).
  *

@@ -86,3 +86,28 @@ def test_no_sequences():
     nm.nm_kv4_unpack(cache, table, kv_len, q_start, 64, x, x)
     out, lse = nm.nm_kv4_attention(x, cache, table, kv_len, q_start, 1, 64, 1)
     assert out.shape == (0, 1, 64) and lse.shape == (0, 1) and int(cache.sum()) == 0
+
+
+@pytest.mark.parametrize("rows", [2, 64, 3000])
+def test_the_same_place_twice_stays_within_that_place(rows):
+    """Rows of many sequences that share a page, all for one token of it: what ends up there is finite, and nothing else changes."""
+    say("same place", rows)
+    H, D, ps = 3, 128, 64
+    g = np.random.default_rng(rows)
+    x = bf16(g.standard_normal((rows, H, D)) * np.exp(4 * g.standard_normal((rows, 1, 1))))
+    table = torch.ones((rows, 1), dtype=torch.int32, device="cuda")
+    kv_len = torch.full((rows,), 21, dtype=torch.int32, device="cuda")
+    q_start = torch.arange(rows + 1, dtype=torch.int32, device="cuda")
+    before = g.integers(0, 250, size=(3, kv4.page_bytes(ps, H, D)), dtype=np.uint8)
+    cd, xd = dev(before), dev_bf16(bits(x))
+    nm.nm_kv4_append(xd, xd, cd, table, kv_len, q_start, ps)
+    after = cd.cpu().numpy()
+    mine = np.zeros((H, before.shape[1] // H), dtype=bool)
+    for values in (False, True):
+        at, sc = kv4.places(ps, D, values)
+        mine[:, at[20]] = mine[:, sc[20]] = True
+    mine = mine.reshape(-1)
+    assert (after[[0, 2]] == before[[0, 2]]).all() and (after[1, ~mine] == before[1, ~mine]).all()
+    one = [table[:1], kv_len[:1], q_start[:2]]
+    for y in nm.nm_kv4_unpack(cd, *one, ps, *(torch.empty_like(xd[:1]) for _ in range(2))):
+        assert torch.isfinite(y).all()
