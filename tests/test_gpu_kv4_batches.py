@@ -14,7 +14,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
     pytest.skip("needs a HIP GPU", allow_module_level=True)
 
 import bitmask_spmv_amd as nm  # noqa: E402
-from tests.kv4_util import bf16, bits  # noqa: E402
+from tests.kv4_util import attention_bounds, bf16, bits, filled_cache  # noqa: E402
 from tests.test_gpu_kv4 import attention_case, dev  # noqa: E402
 
 
@@ -111,3 +111,31 @@ def test_the_same_place_twice_stays_within_that_place(rows):
     one = [table[:1], kv_len[:1], q_start[:2]]
     for y in nm.nm_kv4_unpack(cd, *one, ps, *(torch.empty_like(xd[:1]) for _ in range(2))):
         assert torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("window", [0, 30000])
+def test_long_runs_of_row_tiles(window):
+    """Over 60 blocks to a wave, so that it reads the page table again within its run; whole rows, pieces, and
+    short sequences between them in one run.  Some rows against the plain definition."""
+    say("long runs", window)
+    g = np.random.default_rng(31)
+    Hq, H, D, ps, N = 32, 4, 64, 64, 50
+    rows, lens = [60, 1, 2, 0, 8, 40], [65536, 70, 6000, 9, 50001, 30011]
+    tiles = [-(-r * Hq // H // 16) for r in rows]
+    units = H * sum(t * -(-n // 64) for t, n in zip(tiles, lens))
+    assert window or units > 62 * 8 * torch.cuda.get_device_properties(0).multi_processor_count  # 8 waves to a CU
+    cols = 65536 // ps
+    table = g.integers(0, N, size=(len(rows), cols)).astype(np.int32)  # a small pool, its pages many times in a row
+    kv_len, q_start = np.array(lens, np.int32), np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    cache = filled_cache(g, N, ps, H, D)
+    T = int(q_start[-1])
+    q = bf16(g.standard_normal((T, Hq, D)))
+    out, lse = nm.nm_kv4_attention(dev_bf16(bits(q)), dev(cache), dev(table), dev(kv_len), dev(q_start), H, ps, 1, window=window)
+    out, lse = bf16_as_f64(host_bf16(out)), lse.double().cpu().numpy()
+    assert np.isfinite(out).all() and np.isfinite(lse).all()
+    for t in (0, 17, 59, 60, 61, 62, 63, 66, 70, 71, 90, T - 1):
+        s = int(np.searchsorted(q_start, t, side="right")) - 1
+        length = kv_len[s : s + 1] - (q_start[s + 1] - 1 - t)  # the sequence as that row sees it
+        r = kv4.attention(q[t : t + 1], cache, table[s : s + 1], length, np.array([0, 1]), ps, H, D**-0.5, window)
+        bo, bl = attention_bounds(r)
+        assert (np.abs(out[t] - r["out"][0]) <= bo[0]).all() and (np.abs(lse[t] - r["lse"][0]) <= bl[0]).all(), t
