@@ -438,17 +438,19 @@ nm_status nm_stream_read(const void *buf, size_t bytes, uint32_t *sink, size_t s
  *     s_j = scale * sum_c q_c K_jc,  out = sum_j exp(s_j - lse) V_j,  lse = log sum_j exp(s_j).
  * A row without keys gives out = 0 and lse = -infinity.  lse (fp32 [T][ld_lse]) may be NULL.  out
  * must not overlap q.  Scores, maxima, sums and outputs are kept in fp32, the result is rounded
- * once to bf16.  max_q_len >= 1 is a hint (the largest number of rows of a sequence) that the
- * choice of kernels goes by; a wrong one costs time only.  Cached values must be finite in the
- * places that are looked at (nm_kv4_append stores no others); what masked places, other pages and
- * the rest of a page hold does not matter.  A query with an infinity or NaN among its channels
- * gives NaN, in its own row and head alone.  |scale| < 2^126, and |scale| sum_c |q_c K_jc| < 2^125
- * for the keys a row sees, whatever q and K are by themselves (a larger one may give that row and
- * head infinities or NaN).  T * n_heads <= 2^30, S * n_kv <= 2^22, kv_len < 2^31 - 1024.
- * Workspace: nm_kv4_attention_workspace_bytes, asked with the device of the call as the current
- * one (the size depends on its compute units), 16-byte aligned (room = table_cols * page_size:
- * contexts that all fit in 1024 tokens, for instance, may need none); calls that may overlap in
- * time need workspaces of their own.
+ * once to bf16.  Of a query what is below 2^-20 of the largest of 32 channels may be lost, and the
+ * weights exp(s_j - max) are rounded to bf16 for the product with the values (2^-8 of each at
+ * most; lse is of the unrounded ones).  max_q_len >= 1 is a hint (the largest number of rows of a
+ * sequence) that the choice of kernels goes by; a wrong one costs time only.  Cached values must
+ * be finite in the places that are looked at (nm_kv4_append stores no others); what masked places,
+ * other pages and the rest of a page hold does not matter.  A query with an infinity or NaN among
+ * its channels gives NaN, in its own row and head alone.  |scale| < 2^126, and
+ * |scale| sum_c |q_c K_jc| < 2^125 for the keys a row sees, whatever q and K are by themselves (a
+ * larger one may give that row and head infinities or NaN).  T * n_heads <= 2^30,
+ * S * n_kv <= 2^22, kv_len < 2^31 - 1024. Workspace: nm_kv4_attention_workspace_bytes, asked with
+ * the device of the call as the current one (the size depends on its compute units), 16-byte
+ * aligned (room = table_cols * page_size: contexts that all fit in 1024 tokens, for instance, may
+ * need none); calls that may overlap in time need workspaces of their own.
  */
 typedef struct {
     uint8_t *cache;            /* [num_pages][page_bytes]; written by nm_kv4_append only */
@@ -478,7 +480,8 @@ nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int 
  * sequence's last page are -1), kv_len and a reference count per page: how many sequences
  * hold it, 0 = free.  One table serves the caches of all layers.  Free pages are
  * handed out lowest number first, in the order of the requests, so a result depends on the
- * state and the arguments alone.  S * table_cols and num_pages <= 2^30, pairs <= 2^16, moves <= 2^29.  Workspace for all
+ * state and the arguments alone.  S * table_cols and num_pages <= 2^30, pairs <= 2^16, moves <= 2^29;
+ * none of them 0 (nm_kv_copy_pages takes an empty list).  Workspace for all
  * three: nm_kv_pages_workspace_bytes(S, n_pairs, num_pages, table_cols), 16-byte aligned (n_pairs
  * 0 where there is no fork; small pools need none).
  *
