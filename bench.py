@@ -176,6 +176,8 @@ def parse():
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--cpu-seconds", type=float, default=10.0,
                     help="wall time of the oracle sample on all host cores (half of it again on one core)")
+    ap.add_argument("--details", metavar="FILE", default=None,
+                    help="write every figure of the run to FILE as JSON (the printed line holds the main ones)")
     ap.add_argument("--skip-check", action="store_true", help="skip the oracle spot check")
     ap.add_argument("--no-meta-formats", action="store_true",
                     help="skip the bitmask vs uint8-offset vs int32-index comparison table")
@@ -498,6 +500,22 @@ def target_check(per, patterns):
                 row["pct_reachable_by_plain_read"] = d["stream_read"]["pct_peak"] >= TARGET_PCT
             out[f"{label} {N}:{M}"] = row
     return out
+
+
+def headline(out):
+    """What is printed of a run's figures: a line of a few KB, short enough to be read whole out of the end of a log.
+    Launches as {label: {pattern: [us, % of peak, speedup over dense]}}, other workloads as their steps; the
+    tables behind them are on stderr and in --details."""
+    line = {k: v for k, v in out.items() if k not in ("metadata_formats", "unstructured_50", "solver")}
+    line["per_layer"] = {label: {p: [e["us"], e["pct_peak"], e.get("speedup_vs_dense")] for p, e in d.items() if ":" in p}
+                         for label, d in out["per_layer"].items()}
+    rows = out["per_layer_target"]["launches"]
+    line["per_layer_target"] = {"criterion": out["per_layer_target"]["criterion"], "launches": len(rows),
+                                "met": sum(r["pct_ok"] and r["speedup_ok"] for r in rows.values())}
+    if out["configs"]:
+        line["configs"] = {name: {B: {k: e["step"][k] for k in ("ms", "GBs", "pct_hbm_peak", "speedup_vs_dense")}
+                                  for B, e in cfg["by_batch"].items()} for name, cfg in out["configs"].items()}
+    return line
 
 
 def measure_other(c, name, L, batches, steps, warmup, seed, check):
@@ -912,7 +930,10 @@ def main():
         "roofline": roofline,
         "cpu_baseline": cpu,
     }
-    print(json.dumps(out), flush=True)
+    if args.details:
+        with open(args.details, "w") as f:
+            json.dump(out, f)
+    print(json.dumps(headline(out)), flush=True)
 
 
 COPY_BYTES = 256 << 20
