@@ -24,8 +24,8 @@
 // pieces of rows cut between waves are joined in LDS, those cut between workgroups in fp32
 // through the workspace by a second kernel, in a fixed order.
 //
-// Bound: reading the cache.  16 sequences of up to 64K tokens, 64 and 8 heads: 525 MB in 92 us, 89 of them this
-// kernel's (5.9 TB/s); 48 of up to 8K, 40 and 8 heads: 183 MB in 41 us, 36 of them this kernel's (5.1 TB/s).  A plain read of
+// Bound: reading the cache.  16 sequences of up to 64K tokens, 64 and 8 heads: 525 MB, 93 us a call among others (traced alone
+// this kernel takes 90, 5.8 TB/s, and the join 6); 48 of up to 8K, 40 and 8 heads: 183 MB, 42 us (39 and 5).  A plain read of
 // a large buffer reaches 6.9.  Until half of the waves are through, 28 us after the start of the smaller one, the
 // walk itself reads 7.6 TB/s; the rest is the way to the first block (6 us: lengths, page table and bytes, each
 // waits for the one before), the waves that had to wait for the other one of their SIMD, and the join.
@@ -392,7 +392,7 @@ __device__ __forceinline__ float reference(float m, float c) { return m == -INFI
 
 // Scores -> weights; O and l follow the reference.  The difference is taken before the product with c: the
 // product of a large score, rounded to be subtracted, would be off by more than a power of two (a subtraction more per
-// weight: 42.3 us against 41.9 for 48 sequences of up to 8K tokens, as in a branch for large scores).
+// weight: 42.3 us against 41.9 for 48 sequences of up to 8K tokens; in a branch for large scores, as in prompts, 42.2).
 template <int D>
 __device__ __forceinline__ void weights(Tile<D> &t, f32x4 (&s)[4], float c) {
     float mx = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3]));
@@ -803,8 +803,8 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attention a, const Par
 // softmax a block took 2500 together).  So the walk is a pipeline over tiles of 32 tokens, one step
 // of which has the products of three of them: see `step`.  A block takes 3760 cycles against 4110 for
 // scores, softmax and values one after the other; the clock falls by 4 % (2.14 GHz: the
-// card's power is the bound), so 3 prompts of up to 4K rows behind 2K take 464 us against 475, 455 GFLOP
-// at 980 TFLOP/s.
+// card's power is the bound), so 3 prompts of up to 4K rows behind 2K, 455 GFLOP, took 464 us against 475 on one card when the two were
+// compared, and take 480 to 490 now by card (930 to 950 TFLOP/s).
 constexpr int kPromptTile = 32;                       // rows of a wave
 constexpr int kPromptRows = kWaves * kPromptTile;     // rows of a workgroup
 
@@ -885,6 +885,10 @@ __device__ __forceinline__ void prompt(Kv4Attention &a, int tiles, Values<D> &va
 #pragma unroll
     for (int i = 0; i < MT; ++i) o[i] = f32x16{};
     float top = -INFINITY, off = 0.f, l = 0.f;  // weights are 2^((score - top) c - off); their sum
+    // what follows from top and off: the score that asks for new ones, what is taken from scores times c, and
+    // whether that is far from 0 for a row of the wave
+    float limit = -INFINITY, less = 0.f;
+    bool far = false;
 
     // blocks that the workgroup walks, and those that need no mask for the wave
     auto place_of = [&](int r) { return place0 + (int)((uint32_t)min(r, rows - 1) / (uint32_t)group); };
@@ -1024,8 +1028,8 @@ __device__ __forceinline__ void prompt(Kv4Attention &a, int tiles, Values<D> &va
     // the weights w, which are rounded already and not yet multiplied, follow exactly; of one so far behind
     // that nothing remains, the largest score begins anew.
     auto raise = [&](float x, uint32_t (&w)[8]) {
-        const float past = __builtin_fmaf(x - top, c, -off);  // NaN: neither has a key
-        if (__any(past > 0.f)) {
+        if (__any(x > limit)) {
+            const float past = __builtin_fmaf(x - top, c, -off);  // NaN: neither has a key
             const float by = floorf(past) + kSlack;
             const bool anew = by > 150.f, mine = past > 0.f;
             const float keep = mine ? __builtin_ldexpf(1.f, (int)fmaxf(-by, -1000.f)) : 1.f;
@@ -1036,17 +1040,21 @@ __device__ __forceinline__ void prompt(Kv4Attention &a, int tiles, Values<D> &va
             l *= keep;
             if (mine) off = anew ? kSlack : off + by;
             if (mine && anew) top = x;
+            less = __builtin_fmaf(top == -INFINITY ? 0.f : top, c, off);
+            far = __any(fabsf(less) > kFar);
+            if (far) less = off;
+            limit = __builtin_fmaf(off, __builtin_amdgcn_rcpf(c), top);  // not above its exact value:
+            if (top != -INFINITY) limit = __builtin_fmaf(fabsf(limit), -0x1p-21f, limit);
         }
     };
-    // Scores sc to what the exponent is a product and a difference of: c times it, less the value returned.  Where a reference is
-    // far from 0 the product of a score, rounded to be subtracted, would be off by more than the weights'
-    // own rounding: there scores become differences first.
+    // Where a reference is far from 0 the product of a score, rounded to be subtracted, would be off by more than the
+    // weights' own rounding: there scores become differences first.
     auto relative = [&](f32x16 &sc) {
-        const float base = top == -INFINITY ? 0.f : top, at = __builtin_fmaf(base, c, off);
-        if (__builtin_expect(!__any(fabsf(at) > kFar), 1)) return at;
+        if (__builtin_expect(far, 0)) {
+            const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sc[i] -= base;
-        return off;
+            for (int i = 0; i < 16; ++i) sc[i] -= base;
+        }
     };
 
     // Tile t = 2 b + tt: between them, product by product, the values of tile t (weights w are ready), the scores
@@ -1056,7 +1064,8 @@ __device__ __forceinline__ void prompt(Kv4Attention &a, int tiles, Values<D> &va
         const u32x4 *from_lds = &values[b & 1][2 * tt][0][lane];
         hide(tt ? b + 1 : b, tt ^ 1, sc);
         raise(largest(sc), w);
-        const float mc = relative(sc);
+        relative(sc);
+        const float mc = less;
         if (tt == 0) hide_values(b + 1);
 
         constexpr int kRead = 3;  // value operands read ahead
@@ -1128,7 +1137,8 @@ __device__ __forceinline__ void prompt(Kv4Attention &a, int tiles, Values<D> &va
 #pragma unroll
             for (int k = 0; k < 8; ++k) wa[k] = 0;
             raise(largest(sa), wa);
-            const float mc = relative(sa);
+            relative(sa);
+            const float mc = less;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sa[2 * k], c, -mc));

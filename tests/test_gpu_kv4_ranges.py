@@ -57,11 +57,9 @@ def test_values_near_the_largest_number(D, rows, n, equal):
 @pytest.mark.parametrize("rows", WAYS)
 @pytest.mark.parametrize("n", [81, 3000])
 def test_values_near_the_smallest_number(rows, n):
-    """Values of 2^-112 to 6 * 2^-111 among thousands of others: weights times values are not normal numbers.
-
-    A weight is between 2^-8 and 1 for the largest score, times 2^-13 at most for 3000 keys (room for their sum); an
-    fp32 sum of what is below 2^-126 is kept in steps of 2^-149.  n products are then off by half a step each, that is
-    n * 2^-150 over weights that sum to at least 2^-21: n * 2^-129."""
+    """Values of 2^-112 to 6 * 2^-111 among thousands of others, multiplied as 2^-12 of what they are: weights times values
+    are not normal numbers.  An fp32 sum of what is below 2^-126 is kept in steps of 2^-149: n products are off by half a
+    step each, n * 2^-150, times 2^12 and over weights that sum to at least 2^-8 that is n * 2^-130."""
     say("smallest values", rows, n)
     g = np.random.default_rng(n)
     H, Hq, D, ps = 1, 4, 128, 64
