@@ -804,7 +804,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attention a, const Par
 // of which has the products of three of them: see `step`.  A block takes 3760 cycles against 4110 for
 // scores, softmax and values one after the other; the clock falls by 4 % (2.14 GHz: the
 // card's power is the bound), so 3 prompts of up to 4K rows behind 2K, 455 GFLOP, took 464 us against 475 on one card when the two were
-// compared, and take 480 to 490 now by card (930 to 950 TFLOP/s).
+// compared; with all that keeps sums and scores in range 476 to 502 by card (905 to 955 TFLOP/s).
 constexpr int kPromptTile = 32;                       // rows of a wave
 constexpr int kPromptRows = kWaves * kPromptTile;     // rows of a workgroup
 
