@@ -156,3 +156,21 @@ def test_scales_of_any_size(rows, scale, up_q, up_k):
     q = queries(bf16(np.ldexp(g.standard_normal((rows, Hq, D)), up_q)), rows)
     r = kv4.attention(q, cache, table, kv_len, q_start, ps, H, float(np.float32(scale)), 0)
     held_to(*run_attention(q, cache, table, kv_len, q_start, H, ps, rows, scale=scale), r, f"scale {scale}")
+
+
+@pytest.mark.parametrize("rows", WAYS)
+@pytest.mark.parametrize("scale", [0.0, 2.0**-140, -(2.0**-100), 2.0**60])
+def test_a_query_that_is_not_finite_at_any_scale(rows, scale):
+    """NaN in its own row and head, also where the scale leaves nothing of the others."""
+    say("not finite", rows, scale)
+    g = np.random.default_rng(rows)
+    H, Hq, D, ps, n = 1, 4, 64, 64, 300
+    table, kv_len, q_start, N = batch(g, [rows], [n], ps)
+    cache = filled_cache(g, N, ps, H, D)
+    q = queries(bf16(g.standard_normal((rows, Hq, D))), rows)
+    q[0, 1, 5], q[rows - 1, 2, 40], q[rows // 2, 0, 63] = np.inf, np.nan, -np.inf
+    spoilt = ~np.isfinite(q[:rows]).all(-1)
+    out, lse = run_attention(q, cache, table, kv_len, q_start, H, ps, rows, scale=scale)
+    out, lse = out[:rows], lse[:rows]
+    assert np.isnan(out[spoilt]).all() and np.isnan(lse[spoilt]).all()
+    assert np.isfinite(out[~spoilt]).all() and np.isfinite(lse[~spoilt]).all()
