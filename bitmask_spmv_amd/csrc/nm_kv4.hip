@@ -5,61 +5,12 @@
 // E the biased exponent of the largest magnitude: that magnitude lands in (3.5, 7], where
 // rounding to nearest (6 the largest) is off by at most one unit of the scale.  The ends
 // 16 and 252 keep every stored value a normal, finite bf16.
-#include "nm_device.h"
-#include "nm_kv.h"
+#include "nm_kv_rows.h"
 
 namespace nmk {
 namespace {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
-// Sequence that row t belongs to: the last s with q_start[s] <= t.  Called by a whole wave
-// with one t: 64 lanes look at 64 places at once, so 4096 sequences take two looks.
-__device__ __forceinline__ int find_seq(const int32_t *q_start, int S, int t, int lane) {
-    int lo = 0, n = S;  // the answer is in [lo, lo + n)
-    while (n > 1) {
-        const int step = (n + 63) >> 6;
-        const int at = lo + lane * step;
-        const bool yes = lane * step < n && q_start[at] <= t;
-        const uint64_t m = __ballot(yes);
-        const int last = m ? 63 - __clzll((long long)m) : 0;
-        lo += last * step;
-        n = min(step, S - lo);
-    }
-    return lo;
-}
-
-// The same for a lane's row t < q_start[S], from the sequence s of the wave's first row t0.  Most rows are of s as well, or of
-// the sequence as far behind it as the row is (single tokens): both are looked at at once.  Else in steps that
-// double, and back: a few looks however many sequences without rows lie between.
-__device__ __forceinline__ int seq_of_row(const int32_t *q_start, int S, int s, int t0, int t) {
-    const int guess = min(s + (t - t0), S - 1);
-    const int next = q_start[s + 1], from = q_start[guess], end = q_start[guess + 1];
-    if (t < next) return s;
-    if (from <= t && t < end) return guess;
-    int step = 1;
-    while (step < S - s && q_start[s + step] <= t) {
-        s += step;
-        step *= 2;
-    }
-    for (; step > 0; step >>= 1)
-        if (step < S - s && q_start[s + step] <= t) s += step;
-    return s;
-}
-
-// Where row t is kept: the head-0 block of its page and its token within the page; null
-// where the sequence has no place or no valid page for it.
-__device__ __forceinline__ uint8_t *place_of(const Kv4Batch &b, int s, int t, int &tok) {
-    const int q0 = b.q_start[s], q1 = b.q_start[s + 1];
-    const int64_t pos = (int64_t)b.kv_len[s] - q1 + t;
-    if (t < q0 || t >= q1 || pos < 0) return nullptr;
-    const int64_t col = pos / b.f.page;
-    tok = (int)(pos - col * b.f.page);
-    if (col >= b.cols) return nullptr;
-    const int page = b.table[(int64_t)s * b.ld_table + col];
-    if (page < 0 || page >= b.num_pages) return nullptr;
-    return b.cache + (int64_t)page * b.f.page_bytes();
-}
 
 __device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
 
