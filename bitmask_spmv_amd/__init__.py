@@ -33,7 +33,8 @@ __all__ = [
     "NM_EPI_SWIGLU", "NM_KERNEL_WORD", "NM_KERNEL_TILE", "NM_KERNEL_WORD_HALF_ROWS", "NM_KERNEL_WORD_STRIPS",
     "nm_spmv_noalloc", "nm_kv4_page_bytes", "nm_kv4_append", "nm_kv4_unpack", "nm_kv4_attention",
     "nm_kv4_attention_workspace_bytes", "nm_kv_pages_workspace_bytes", "nm_kv_resize", "nm_kv_fork",
-    "nm_kv_compact", "nm_kv_copy_pages",
+    "nm_kv_compact", "nm_kv_copy_pages", "nm_kv8_page_bytes", "nm_kv8_append", "nm_kv8_unpack", "nm_kv8_select",
+    "nm_kv8_attention", "nm_kv8_attention_workspace_bytes",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnmspmv.so")
@@ -127,8 +128,15 @@ def _load() -> ctypes.CDLL:
     L.nm_kv_fork.argtypes = [d, p, p, i64, p, p, p, sz, p]
     L.nm_kv_compact.argtypes = [d, p, i64, p, p, sz, p]
     L.nm_kv_copy_pages.argtypes = [p, i64, i64, i64, i64, p, i64, p]
+    L.nm_kv8_page_bytes.argtypes, L.nm_kv8_page_bytes.restype = [i32, i32, i32], i64
+    L.nm_kv8_append.argtypes = [d, d, d, d, d, i32, d, p]
+    L.nm_kv8_unpack.argtypes = [d, d, d, p]
+    L.nm_kv8_select.argtypes = [d, d, i32, i32, i32, i32, p, i64, p]
+    L.nm_kv8_attention_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i64, i64, i32]
+    L.nm_kv8_attention_workspace_bytes.restype = sz
+    L.nm_kv8_attention.argtypes = [d, d, i32, i64, f32, i64, p, i64, i32, d, p, i64, p, sz, p]
     for f in (L.nm_kv4_append, L.nm_kv4_unpack, L.nm_kv4_attention, L.nm_kv_resize, L.nm_kv_fork, L.nm_kv_compact,
-              L.nm_kv_copy_pages):
+              L.nm_kv_copy_pages, L.nm_kv8_append, L.nm_kv8_unpack, L.nm_kv8_select, L.nm_kv8_attention):
         f.restype = i32
     for f in (L.nm_col_norm, L.nm_prune_pack, L.nm_spmv, L.dense_gemv, L.nm_unpack, L.nm_spmv_multi,
               L.dense_gemv_multi):
@@ -622,7 +630,7 @@ def nm_spmv_multi_plan(rows, K: int, B: int) -> dict:
     return _plan_dict(pl)
 
 
-# ---- the 4-bit key/value cache (format, places and rules: include/nm_spmv.h) ----
+# ---- the 4-bit and the 8-bit key/value cache (formats, places and rules: include/nm_spmv.h) ----
 #
 # These run once a token and layer, some for a few microseconds: descriptors are packed in one
 # go (native alignment, the C structs' field order), devices compared by number.
@@ -630,6 +638,7 @@ def nm_spmv_multi_plan(rows, K: int, B: int) -> dict:
 _KV4_BATCH = struct.Struct("@PqPqPPqq4i")  # nm_kv4_batch
 _KV4_ROWS = struct.Struct("@Pqq")          # nm_kv4_rows
 _KV_BOOK = struct.Struct("@PqPqPq2i")      # nm_kv_book
+_KV8_ROTATION = struct.Struct("@Pqq2i")    # nm_kv8_rotation
 
 
 def nm_kv4_page_bytes(page_size: int, n_kv: int, head_dim: int) -> int:
@@ -696,14 +705,23 @@ def _kv_rows(t: torch.Tensor, name: str, dev: int, shape) -> bytes:
     return _KV4_ROWS.pack(t.data_ptr(), ld if T > 1 else H * D, hd if H > 1 else D)
 
 
-def _kv_batch(dev: int, cache: torch.Tensor, page_table, kv_len, q_start, page_size: int, n_kv: int, T: int, D: int):
+def _kv4_page(page_size: int, n_kv: int, D: int) -> int:  # nm_kv4_page_bytes, where it is not 0
+    return page_size * n_kv * (D + D // 16)
+
+
+def _kv8_page(page_size: int, n_kv: int, D: int) -> int:  # nm_kv8_page_bytes, where it is not 0
+    return -(-n_kv * (page_size // 64) * (130 * D + 4) // 128) * 128
+
+
+def _kv_batch(dev: int, cache: torch.Tensor, page_table, kv_len, q_start, page_size: int, n_kv: int, T: int, D: int,
+              page=_kv4_page):
     """(nm_kv4_batch, S, tokens a table row has room for), checked."""
     if not isinstance(cache, _Tensor) or cache.dtype is not torch.uint8 or cache.get_device() != dev:
         raise TypeError(f"cache must be a uint8 tensor on cuda:{dev}")
     if cache.dim() != 2 or not cache.is_contiguous():
         raise ValueError("cache must be contiguous, [num_pages, page_bytes]")
     N, nbytes = cache.shape
-    if nbytes != page_size * n_kv * (D + D // 16):  # nm_kv4_page_bytes, where it is not 0
+    if nbytes != page(page_size, n_kv, D):
         raise ValueError(f"cache pages of {page_size} tokens of {n_kv} heads of {D} cannot have {nbytes} bytes")
     tp, ld, cols, S = _table(page_table, dev)
     return _KV4_BATCH.pack(cache.data_ptr(), N, tp, ld, _i32(kv_len, "kv_len", dev, (S,)),
@@ -786,6 +804,132 @@ def nm_kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Ten
     b, S, room = _kv_batch(dev, cache, page_table, kv_len, q_start, page_size, n_kv, T, D)
     ws, wp, wn = _kv_workspace(_attention_workspace, dev, (T, S, Hq, n_kv, D, max_q_len, room), workspace)
     _call(dev, lib.nm_kv4_attention, b, qr, Hq, max_q_len, D ** -0.5 if scale is None else scale, window,
+          _kv_rows(out, "out", dev, shape), lse.data_ptr(), lse.stride(0) if T > 1 else Hq, wp, wn)
+    return out, lse
+
+
+def nm_kv8_page_bytes(page_size: int, n_kv: int, head_dim: int) -> int:
+    """Bytes of one page of page_size tokens (64, 128, 256 or 512) of n_kv heads of 64 or 128 channels."""
+    return int(lib.nm_kv8_page_bytes(int(page_size), int(n_kv), int(head_dim)))
+
+
+def _kv8_rotation(t: torch.Tensor, interleaved: bool, dev: int) -> bytes:
+    if not isinstance(t, _Tensor) or t.dtype is not torch.float32 or t.get_device() != dev:
+        raise TypeError(f"rotation must be an fp32 tensor on cuda:{dev}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != 2 or stride[2] != 1 or stride[1] != 2:
+        raise ValueError(f"rotation must be [positions, pairs, 2], contiguous in its last two dimensions (got {list(shape)})")
+    R = 2 * shape[1]
+    return _KV8_ROTATION.pack(t.data_ptr(), stride[0] if shape[0] > 1 else R, shape[0], R, bool(interleaved))
+
+
+def nm_kv8_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
+                  kv_len: torch.Tensor, q_start: torch.Tensor, page_size: int, rotation: torch.Tensor | None = None,
+                  interleaved: bool = False, q: torch.Tensor | None = None, q_out: torch.Tensor | None = None):
+    """Rows k, v bf16 [T, n_kv, D] -> cache uint8 [num_pages, page_bytes], at the last places of the
+    sequences: page_table int32 [S, columns], kv_len int32 [S] (new rows included), q_start int32 [S + 1].
+    rotation: cosine and sine fp32 [positions, pairs, 2] of every place that the table has room for, by which keys are
+    rotated on the way, pairs half the rotated channels apart or side by side (interleaved), and queries q bf16
+    [T, heads, D] too -> q_out (new unless given; q itself will do)."""
+    dev, shape = _where(k, "k"), k.shape
+    kr, vr = _kv_rows(k, "k", dev, shape), _kv_rows(v, "v", dev, shape)
+    T, H, D = shape
+    b, _, _ = _kv_batch(dev, cache, page_table, kv_len, q_start, page_size, H, T, D, _kv8_page)
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        _call(dev, lib.nm_kv8_append, b, kr, vr, None if rotation is None else _kv8_rotation(rotation, interleaved, dev), None, 0, None)
+        return None
+    if rotation is None:
+        raise ValueError("q without a rotation")
+    if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D:
+        raise ValueError(f"q must be [{T}, heads, {D}] (got {list(q.shape)})")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    _call(dev, lib.nm_kv8_append, b, kr, vr, _kv8_rotation(rotation, interleaved, dev), _kv_rows(q, "q", dev, q.shape),
+          q.shape[1], _kv_rows(q_out, "q_out", dev, q.shape))
+    return q_out
+
+
+def nm_kv8_unpack(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, q_start: torch.Tensor,
+                  page_size: int, k_out: torch.Tensor, v_out: torch.Tensor):
+    """The rows that nm_kv8_append with the same arguments stores, as the cache holds them -> k_out, v_out bf16
+    [T, n_kv, D]."""
+    dev, shape = _where(k_out, "k_out"), k_out.shape
+    kr, vr = _kv_rows(k_out, "k_out", dev, shape), _kv_rows(v_out, "v_out", dev, shape)
+    T, H, D = shape
+    b, _, _ = _kv_batch(dev, cache, page_table, kv_len, q_start, page_size, H, T, D, _kv8_page)
+    _call(dev, lib.nm_kv8_unpack, b, kr, vr)
+    return k_out, v_out
+
+
+def _kv8_selected(t: torch.Tensor, T: int, H: int, dev: int):
+    """(pointer, entries from a row to the next, blocks of a row), checked."""
+    if not isinstance(t, _Tensor) or t.dtype is not _I32 or t.get_device() != dev:
+        raise TypeError(f"selected must be an int32 tensor on cuda:{dev}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != T or shape[1] != H or stride[2] != 1 or (H > 1 and stride[1] != shape[2]):
+        raise ValueError(f"selected must be [{T}, {H}, top], contiguous in its last two dimensions (got {list(shape)})")
+    return t.data_ptr(), stride[0] if T > 1 else H * shape[2], shape[2]
+
+
+def nm_kv8_select(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
+                  q_start: torch.Tensor, n_kv: int, page_size: int, top: int, first: int = 1, last: int = 1,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """For each row of q bf16 [T, heads, D] and key/value head the `top` blocks of 64 places whose bound on the heads' sum of
+    scores is largest, the `first` and the `last` blocks of the row's keys in any case -> int32 [T, n_kv, top] in increasing
+    order, -1 behind the last (rows behind the last sequence are left as they are)."""
+    dev, shape = _where(q, "q"), q.shape
+    qr = _kv_rows(q, "q", dev, shape)
+    T, Hq, D = shape
+    b, _, _ = _kv_batch(dev, cache, page_table, kv_len, q_start, page_size, n_kv, T, D, _kv8_page)
+    if out is None:
+        out = torch.empty((T, n_kv, top), dtype=torch.int32, device=q.device)
+    elif out.dim() == 3 and out.shape[2] != top:
+        raise ValueError(f"out must have room for {top} blocks (got {list(out.shape)})")
+    ptr, ld, _ = _kv8_selected(out, T, n_kv, dev)
+    _call(dev, lib.nm_kv8_select, b, qr, Hq, top, first, last, ptr, ld)
+    return out
+
+
+def nm_kv8_attention_workspace_bytes(T: int, S: int, n_heads: int, n_kv: int, head_dim: int, max_q_len: int,
+                                     room: int, top: int = 0) -> int:
+    """For calls on the current device.  room: tokens that a row of the page table has room for (columns * page_size);
+    top: selected blocks of a row, 0 without them."""
+    return int(lib.nm_kv8_attention_workspace_bytes(T, S, n_heads, n_kv, head_dim, max_q_len, room, top))
+
+
+@functools.lru_cache(maxsize=4096)
+def _kv8_workspace(dev: int, *sizes) -> int:
+    if dev == _current_device():
+        return int(lib.nm_kv8_attention_workspace_bytes(*sizes))
+    with torch.cuda.device(dev):
+        return int(lib.nm_kv8_attention_workspace_bytes(*sizes))
+
+
+def nm_kv8_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
+                     q_start: torch.Tensor, n_kv: int, page_size: int, max_q_len: int, scale: float | None = None,
+                     window: int = 0, selected: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Causal attention of rows q bf16 [T, heads, D] over the cached keys and values of their sequences ->
+    (out bf16 [T, heads, D], lse fp32 [T, heads]).  scale: 1 / sqrt(D) unless given.  window: keys a row looks
+    back over, itself among them (0: all).  selected int32 [T, n_kv, top]: blocks of 64 places that a row looks at
+    (nm_kv8_select; below 0: none), all unless given.  max_q_len: a hint, the most rows of one sequence."""
+    dev, shape = _where(q, "q"), q.shape
+    qr = _kv_rows(q, "q", dev, shape)
+    T, Hq, D = shape
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    elif lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != (T, Hq) or lse.stride(1) != 1:
+        raise ValueError("lse must be fp32 [T, heads], contiguous in its last dimension, on q's device")
+    b, S, room = _kv_batch(dev, cache, page_table, kv_len, q_start, page_size, n_kv, T, D, _kv8_page)
+    sp, sl, top = (None, 0, 0) if selected is None else _kv8_selected(selected, T, n_kv, dev)
+    if selected is not None and top < 1:
+        raise ValueError("selected has no blocks")
+    ws, wp, wn = _kv_workspace(_kv8_workspace, dev, (T, S, Hq, n_kv, D, max_q_len, room, top), workspace)
+    _call(dev, lib.nm_kv8_attention, b, qr, Hq, max_q_len, D ** -0.5 if scale is None else scale, window, sp, sl, top,
           _kv_rows(out, "out", dev, shape), lse.data_ptr(), lse.stride(0) if T > 1 else Hq, wp, wn)
     return out, lse
 

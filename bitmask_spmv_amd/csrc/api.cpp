@@ -789,12 +789,14 @@ nm_status nm_stream_read(const void *buf, size_t bytes, uint32_t *sink, size_t s
     }
 }
 
-// ---- the 4-bit key/value cache ----
+// ---- the 4-bit and the 8-bit key/value cache ----
 
 static bool kv_page_size_ok(int p) { return p == 64 || p == 128 || p == 256 || p == 512; }
 
 // Checks of a ragged batch over a cache, shared by append, unpack and attention.
-static nm_status kv4_batch(const char *who, const nm_kv4_batch *p, nmk::Kv4Batch &b) {
+extern "C++" {
+template <class F>
+static nm_status kv_batch(const char *who, const nm_kv4_batch *p, nmk::KvBatch<F> &b) {
     if (!p || !p->cache || !p->q_start || (p->S != 0 && (!p->page_table || !p->kv_len)))  // of no sequences: no arrays
         return fail(NM_ERR_NULL, "%s: NULL pointer", who);
     if (p->head_dim != 64 && p->head_dim != 128)
@@ -825,9 +827,10 @@ static nm_status kv4_batch(const char *who, const nm_kv4_batch *p, nmk::Kv4Batch
     b.T = (int)p->T;
     return NM_OK;
 }
+}
 
-static nm_status kv4_rows(const char *who, const char *name, const nm_kv4_rows *p, int heads, int dim,
-                          nmk::Kv4Rows &r) {
+static nm_status kv_rows(const char *who, const char *name, const nm_kv4_rows *p, int heads, int dim,
+                         nmk::KvRows &r) {
     if (!p || !p->p) return fail(NM_ERR_NULL, "%s: %s is NULL", who, name);
     if (p->ld < dim || (heads > 1 && p->hd < dim) || p->ld > kMaxDim || p->hd > kMaxDim || p->hd < 0)
         return fail(NM_ERR_SHAPE, "%s: %s strides %lld (token) and %lld (head) for heads of %d", who, name,
@@ -853,10 +856,10 @@ static nm_status kv4_move_rows(const char *who, const nm_kv4_batch *batch, const
                                bool write, void *hip_stream) {
     nmk::Kv4Batch b;
     nmk::Kv4Rows kr, vr;
-    nm_status st = kv4_batch(who, batch, b);
+    nm_status st = kv_batch(who, batch, b);
     if (st != NM_OK || b.T == 0) return st;  // no rows: their pointers may be NULL
-    st = kv4_rows(who, "k", k, b.f.n_kv, b.f.dim, kr);
-    if (st == NM_OK) st = kv4_rows(who, "v", v, b.f.n_kv, b.f.dim, vr);
+    st = kv_rows(who, "k", k, b.f.n_kv, b.f.dim, kr);
+    if (st == NM_OK) st = kv_rows(who, "v", v, b.f.n_kv, b.f.dim, vr);
     if (st != NM_OK) return st;
     hipError_t e = write ? nmk::launch_kv4_append(b, kr, vr, (hipStream_t)hip_stream)
                          : nmk::launch_kv4_unpack(b, kr, vr, (hipStream_t)hip_stream);
@@ -896,7 +899,7 @@ nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int 
         g_err[0] = 0;
         const char *who = "nm_kv4_attention";
         nmk::Kv4Attention a;
-        nm_status st = kv4_batch(who, batch, a.b);
+        nm_status st = kv_batch(who, batch, a.b);
         if (st != NM_OK) return st;
         const int n_kv = a.b.f.n_kv, head_dim = a.b.f.dim;
         const int64_t T = a.b.T, S = a.b.S;
@@ -910,8 +913,8 @@ nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int 
         if (!(scale < 0x1p126f && scale > -0x1p126f))
             return fail(NM_ERR_SHAPE, "%s: scale=%g is not below 2^126 in magnitude", who, (double)scale);
         if (T == 0) return NM_OK;  // no rows: their pointers may be NULL
-        st = kv4_rows(who, "q", q, n_heads, head_dim, a.q);
-        if (st == NM_OK) st = kv4_rows(who, "out", out, n_heads, head_dim, a.out);
+        st = kv_rows(who, "q", q, n_heads, head_dim, a.q);
+        if (st == NM_OK) st = kv_rows(who, "out", out, n_heads, head_dim, a.out);
         if (st != NM_OK) return st;
         if (lse && ld_lse < n_heads) return fail(NM_ERR_SHAPE, "%s: ld_lse=%lld", who, (long long)ld_lse);
         if (!aligned(lse, 4)) return fail(NM_ERR_ALIGN, "%s: lse needs 4-byte alignment", who);
@@ -928,6 +931,196 @@ nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int 
         return e == hipSuccess ? NM_OK : hip_fail(who, e);
     } catch (...) {
         return fail(NM_ERR_HIP, "nm_kv4_attention: internal error");
+    }
+}
+
+int64_t nm_kv8_page_bytes(int page_size, int n_kv, int head_dim) {
+    if (!kv_page_size_ok(page_size) || n_kv < 1 || n_kv > 256 || (head_dim != 64 && head_dim != 128)) return 0;
+    nmk::Kv8Format f;
+    f.page = page_size;
+    f.n_kv = n_kv;
+    f.dim = head_dim;
+    return f.page_bytes();
+}
+
+// Append and unpack take a workgroup to each block of 64 tokens and head: launches are numbered in 32 bits.
+static nm_status kv8_move_sizes(const char *who, const nmk::Kv8Batch &b) {
+    if ((int64_t)b.T * b.f.n_kv > (1 << 28) || (int64_t)b.S * b.f.n_kv > (1 << 21))
+        return fail(NM_ERR_SHAPE, "%s: T=%d rows (2^28 in all) or S=%d sequences (2^21) of %d heads are too many", who, b.T, b.S,
+                    b.f.n_kv);
+    return NM_OK;
+}
+
+static nm_status query_heads(const char *who, int n_heads, int n_kv) {
+    if (n_heads < 1 || n_heads > 1024 || n_heads % n_kv)
+        return fail(NM_ERR_SHAPE, "%s: %d query heads are not a multiple of %d key/value heads", who, n_heads, n_kv);
+    return NM_OK;
+}
+
+nm_status nm_kv8_append(const nm_kv8_batch *batch, const nm_kv8_rows *k, const nm_kv8_rows *v,
+                        const nm_kv8_rotation *rotation, const nm_kv8_rows *q, int n_heads, const nm_kv8_rows *q_out,
+                        void *hip_stream) {
+    try {
+        g_err[0] = 0;
+        const char *who = "nm_kv8_append";
+        nmk::Kv8Batch b;
+        nmk::KvRows kr, vr, qr, qo;
+        nmk::KvRotation r;
+        nm_status st = kv_batch(who, batch, b);
+        if (st == NM_OK) st = kv8_move_sizes(who, b);
+        if (st != NM_OK) return st;
+        if (rotation) {
+            const int64_t room = (int64_t)b.cols * b.f.page;
+            if (!rotation->cos_sin) return fail(NM_ERR_NULL, "%s: cos_sin is NULL", who);
+            if (rotation->rotary_dim < 16 || rotation->rotary_dim > b.f.dim || rotation->rotary_dim % 16)
+                return fail(NM_ERR_SHAPE, "%s: %d rotated channels of %d are not a multiple of 16", who, rotation->rotary_dim,
+                            b.f.dim);
+            if (rotation->positions < room)
+                return fail(NM_ERR_SHAPE, "%s: angles of %lld places, the page table has room for %lld", who,
+                            (long long)rotation->positions, (long long)room);
+            if (rotation->ld < rotation->rotary_dim || rotation->ld > kMaxDim)
+                return fail(NM_ERR_SHAPE, "%s: %lld numbers from a place's angles to the next", who, (long long)rotation->ld);
+            if (rotation->ld % 4 || !aligned(rotation->cos_sin, 16))
+                return fail(NM_ERR_ALIGN, "%s: cos_sin needs 16-byte alignment, its row stride a multiple of 4", who);
+            r.cos_sin = rotation->cos_sin;
+            r.ld = rotation->ld;
+            r.dim = rotation->rotary_dim;
+            r.interleaved = rotation->interleaved != 0;
+        }
+        if (q || q_out) {
+            if (!q || !q_out) return fail(NM_ERR_NULL, "%s: one of q and q_out is NULL", who);
+            if (!rotation) return fail(NM_ERR_NULL, "%s: queries without a rotation", who);
+            st = query_heads(who, n_heads, b.f.n_kv);
+            if (st != NM_OK) return st;
+        }
+        if (b.T == 0) return NM_OK;  // no rows: their pointers may be NULL
+        st = kv_rows(who, "k", k, b.f.n_kv, b.f.dim, kr);
+        if (st == NM_OK) st = kv_rows(who, "v", v, b.f.n_kv, b.f.dim, vr);
+        if (st == NM_OK && q) st = kv_rows(who, "q", q, n_heads, b.f.dim, qr);
+        if (st == NM_OK && q) st = kv_rows(who, "q_out", q_out, n_heads, b.f.dim, qo);
+        if (st != NM_OK) return st;
+        hipError_t e = nmk::launch_kv8_append(b, kr, vr, r, qr, n_heads, qo, (hipStream_t)hip_stream);
+        return e == hipSuccess ? NM_OK : hip_fail(who, e);
+    } catch (...) {
+        return fail(NM_ERR_HIP, "nm_kv8_append: internal error");
+    }
+}
+
+nm_status nm_kv8_unpack(const nm_kv8_batch *batch, const nm_kv8_rows *k, const nm_kv8_rows *v, void *hip_stream) {
+    try {
+        g_err[0] = 0;
+        const char *who = "nm_kv8_unpack";
+        nmk::Kv8Batch b;
+        nmk::KvRows kr, vr;
+        nm_status st = kv_batch(who, batch, b);
+        if (st == NM_OK) st = kv8_move_sizes(who, b);
+        if (st != NM_OK || b.T == 0) return st;  // no rows: their pointers may be NULL
+        st = kv_rows(who, "k", k, b.f.n_kv, b.f.dim, kr);
+        if (st == NM_OK) st = kv_rows(who, "v", v, b.f.n_kv, b.f.dim, vr);
+        if (st != NM_OK) return st;
+        hipError_t e = nmk::launch_kv8_unpack(b, kr, vr, (hipStream_t)hip_stream);
+        return e == hipSuccess ? NM_OK : hip_fail(who, e);
+    } catch (...) {
+        return fail(NM_ERR_HIP, "nm_kv8_unpack: internal error");
+    }
+}
+
+nm_status nm_kv8_select(const nm_kv8_batch *batch, const nm_kv8_rows *q, int n_heads, int top, int first, int last,
+                        int32_t *selected, int64_t ld_selected, void *hip_stream) {
+    try {
+        g_err[0] = 0;
+        const char *who = "nm_kv8_select";
+        nmk::Kv8Select a;
+        nm_status st = kv_batch(who, batch, a.b);
+        if (st == NM_OK) st = query_heads(who, n_heads, a.b.f.n_kv);
+        if (st != NM_OK) return st;
+        const int64_t blocks = (int64_t)a.b.cols * (a.b.f.page / 64);
+        if (top < 1 || top > nmk::kMaxSelectBlocks || first < 0 || last < 0 || (int64_t)first + last > top)
+            return fail(NM_ERR_SHAPE, "%s: top=%d blocks (1 to %d), the first %d and the last %d among them", who, top,
+                        nmk::kMaxSelectBlocks, first, last);
+        if (blocks > nmk::kMaxSelectBlocks)
+            return fail(NM_ERR_SHAPE, "%s: a row of the page table holds %lld blocks, more than %d", who, (long long)blocks,
+                        nmk::kMaxSelectBlocks);
+        if ((int64_t)a.b.T * a.b.f.n_kv > (1 << 21))
+            return fail(NM_ERR_SHAPE, "%s: T=%d rows of %d heads are more than 2^21", who, a.b.T, a.b.f.n_kv);
+        if (a.b.T == 0) return NM_OK;  // no rows: their pointers may be NULL
+        st = kv_rows(who, "q", q, n_heads, a.b.f.dim, a.q);
+        if (st != NM_OK) return st;
+        if (!selected) return fail(NM_ERR_NULL, "%s: selected is NULL", who);
+        if (!aligned(selected, 4)) return fail(NM_ERR_ALIGN, "%s: selected needs 4-byte alignment", who);
+        if (ld_selected < (int64_t)a.b.f.n_kv * top)
+            return fail(NM_ERR_SHAPE, "%s: ld_selected=%lld", who, (long long)ld_selected);
+        a.heads = n_heads;
+        a.top = top;
+        a.first = first;
+        a.last = last;
+        a.out = selected;
+        a.ld_out = ld_selected;
+        hipError_t e = nmk::launch_kv8_select(a, (hipStream_t)hip_stream);
+        return e == hipSuccess ? NM_OK : hip_fail(who, e);
+    } catch (...) {
+        return fail(NM_ERR_HIP, "nm_kv8_select: internal error");
+    }
+}
+
+size_t nm_kv8_attention_workspace_bytes(int64_t T, int64_t S, int n_heads, int n_kv, int head_dim, int64_t max_q_len,
+                                        int64_t room, int top) {
+    if (T < 0 || T > (1 << 24) || S < 0 || S > (1 << 20) || n_kv < 1 || n_kv > 256 || n_heads < 1 || n_heads > 1024 ||
+        n_heads % n_kv || (head_dim != 64 && head_dim != 128) || max_q_len < 1 || room < 1 || top < 0)
+        return 0;
+    return nmk::kv8_attention_workspace(T, S, n_heads, n_kv, head_dim, room, top);
+}
+
+nm_status nm_kv8_attention(const nm_kv8_batch *batch, const nm_kv8_rows *q, int n_heads, int64_t max_q_len, float scale,
+                           int64_t window, const int32_t *selected, int64_t ld_selected, int top, const nm_kv8_rows *out,
+                           float *lse, int64_t ld_lse, void *workspace, size_t workspace_bytes, void *hip_stream) {
+    try {
+        g_err[0] = 0;
+        const char *who = "nm_kv8_attention";
+        nmk::Kv8Attention a;
+        nm_status st = kv_batch(who, batch, a.b);
+        if (st != NM_OK) return st;
+        const int n_kv = a.b.f.n_kv, head_dim = a.b.f.dim;
+        st = query_heads(who, n_heads, n_kv);
+        if (st != NM_OK) return st;
+        const int64_t T = a.b.T, S = a.b.S;
+        if (T * n_heads > kMaxDim || S * n_kv > (1 << 22))  // rows and launches are numbered in 32 bits
+            return fail(NM_ERR_SHAPE, "%s: T=%lld rows of %d heads (2^30 in all) or S=%lld sequences of %d (2^22) are too many",
+                        who, (long long)T, n_heads, (long long)S, n_kv);
+        if (window < 0 || max_q_len < 1)
+            return fail(NM_ERR_SHAPE, "%s: window=%lld max_q_len=%lld", who, (long long)window, (long long)max_q_len);
+        if (!(scale == 0.f || (fabsf(scale) >= 0x1p-60f && fabsf(scale) <= 0x1p60f)))
+            return fail(NM_ERR_SHAPE, "%s: scale=%g is neither 0 nor between 2^-60 and 2^60 in magnitude", who, (double)scale);
+        if (selected) {
+            if (top < 1 || top > (1 << 20) || ld_selected < (int64_t)n_kv * top)
+                return fail(NM_ERR_SHAPE, "%s: top=%d selected blocks, ld_selected=%lld", who, top, (long long)ld_selected);
+            if (T * n_heads > (1 << 23))
+                return fail(NM_ERR_SHAPE, "%s: T=%lld rows of %d heads are more than 2^23 with selected blocks", who, (long long)T,
+                            n_heads);
+            if (!aligned(selected, 4)) return fail(NM_ERR_ALIGN, "%s: selected needs 4-byte alignment", who);
+            a.selected = selected;
+            a.ld_selected = ld_selected;
+            a.top = top;
+        }
+        if (T == 0) return NM_OK;  // no rows: their pointers may be NULL
+        st = kv_rows(who, "q", q, n_heads, head_dim, a.q);
+        if (st == NM_OK) st = kv_rows(who, "out", out, n_heads, head_dim, a.out);
+        if (st != NM_OK) return st;
+        if (lse && ld_lse < n_heads) return fail(NM_ERR_SHAPE, "%s: ld_lse=%lld", who, (long long)ld_lse);
+        if (!aligned(lse, 4)) return fail(NM_ERR_ALIGN, "%s: lse needs 4-byte alignment", who);
+        const size_t need = nmk::kv8_attention_workspace(T, S, n_heads, n_kv, head_dim, (int64_t)a.b.cols * a.b.f.page, a.top);
+        if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+            return fail(NM_ERR_WORKSPACE, "%s: 16-byte aligned workspace of %zu bytes required, %zu given", who, need,
+                        workspace ? workspace_bytes : (size_t)0);
+        a.lse = lse;
+        a.ld_lse = ld_lse;
+        a.heads = n_heads;
+        a.set_scale(scale);
+        a.window = std::min(window, (int64_t)1 << 40);  // longer than any sequence
+        hipError_t e = nmk::launch_kv8_attention(a, std::min(max_q_len, T), workspace, (hipStream_t)hip_stream);
+        return e == hipSuccess ? NM_OK : hip_fail(who, e);
+    } catch (...) {
+        return fail(NM_ERR_HIP, "nm_kv8_attention: internal error");
     }
 }
 

@@ -1,0 +1,806 @@
+// nm_kv8_attention.hip -- attention over the 8-bit key/value cache, over all keys or over blocks of 64 that each row selects.
+//
+// For query row i of a sequence (place p = kv_len - rows + i) and head h:
+//     s_j = scale * sum_c q_c K_jc,  m = max_j s_j,  l = sum_j exp(s_j - m),
+//     o_c = sum_j exp(s_j - m) V_jc / l,  lse = m + log l,
+// over the keys j <= p, and j > p - window where there is a window, and j in the row's selected blocks where there are some.
+//
+// Row tiles.  The query rows of one key/value head (its query heads times the sequence's new tokens; with selected blocks
+// times one token) form tiles of 16.  A wave takes one tile and walks blocks of 64 tokens:
+//   S^T [64 x 16] = K [64 x D] . Q^T and O^T [D x 16] += V^T [D x 64] . P^T, both on the bf16 matrix instruction.  E4M3
+//     numbers times a power of two are bf16 numbers, so keys and values are converted exactly, two an instruction, in the
+//     order the page has them: K units are 16 channels of a token, V units 16 tokens of a channel, and S^T leaves a lane the
+//     weights of just those tokens.  Nothing passes through LDS.  The scaled matrix instruction would take the bytes as they lie, but
+//     it aligns the products of 8 neighbouring channels to 13 bits below the largest, too few for two E4M3 factors; the
+//     conversions (128 a block and lane) hide behind the reads.
+// Weights are rounded to bf16 for the second product (2^-8 of each at most, either way); scores, maxima, sums and O stay in fp32.
+//
+// Work split.  As the 4-bit kernels: all (sequence, key/value head, row tile, 64-token block) units of a call laid end to end and
+// cut into equal runs, one a wave; pieces of rows cut between waves are joined in LDS, between workgroups by a second kernel, in
+// a fixed order.  Selected blocks make the same units, so many to every row.
+#include "nm_kv_attention.h"
+#include "nm_kv_rows.h"
+
+namespace nmk {
+namespace {
+
+constexpr float kSlack = 8.f;   // prompts: O is rescaled only when a score passes the largest one so far by 2^kSlack
+constexpr float kFar = 4096.f;  // reference (log2) up to which a rounded product of it is off by 2^-13 at most
+constexpr int kWholeTokens = 1024;  // context up to which each row tile may be one workgroup's, which needs no second launch
+constexpr int kFewTiles = 2;        // row tiles of a call, one to so many waves at most, up to which prompts are walked by row tiles too
+constexpr int kGroupsPerCu = 2;     // resident workgroups: 8 waves a CU
+
+__device__ __forceinline__ uint32_t fp8_pair(uint32_t w, float s, bool high) {
+    union { bf16x2 h; uint32_t u; } c;
+    c.h = high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true) : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false);
+    return c.u;
+}
+
+union Operand {  // eight bf16 numbers of a lane
+    u32x4 u;
+    uint32_t w[4];
+    bf16x8 h;
+};
+
+// Eight E4M3 numbers times s.
+__device__ __forceinline__ Operand eight(uint32_t a, uint32_t b, float s) {
+    Operand x;
+    x.w[0] = fp8_pair(a, s, false);
+    x.w[1] = fp8_pair(a, s, true);
+    x.w[2] = fp8_pair(b, s, false);
+    x.w[3] = fp8_pair(b, s, true);
+    return x;
+}
+
+// Eight channels of a query with the sign of the scale; zeros for a row that is none.  An infinity becomes NaN: a product with it could
+// look like a key that is not seen.
+__device__ __forceinline__ Operand read_query(const uint16_t *from, bool real, const Kv8Attention &a) {
+    const uint32_t flip = a.minus ? 0x80008000u : 0u;
+    Operand x;
+    x.u = real ? *reinterpret_cast<const u32x4 *>(from) : (u32x4){0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t none = ((x.w[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;  // exponents of all ones
+        x.w[i] = a.zero ? (none >> 15) * 0x7FC0u : (x.w[i] ^ flip) | none >> 9;
+    }
+    return x;
+}
+
+// Where the blocks of one head lie: lane i holds the address and the scales of a block and its number, so that a walk reads the page table
+// once for kAhead blocks.  Without a valid page the address is that of page 0, so that loads need no branch, and
+// the block's bit in `valid` is clear.
+struct Blocks {
+    static constexpr int kAhead = 60;  // of 64: a walk looks up to three blocks ahead
+    uint32_t lo, hi, scales;
+    int block;
+    uint64_t valid;
+    __device__ void load(const Kv8Batch &b, const int32_t *row, int head, int mine) {
+        block = mine;
+        const int per = b.f.blocks(), col = block >= 0 ? block / per : 0;
+        int page = block >= 0 && col < b.cols ? row[col] : -1;
+        const bool ok = page >= 0 && page < b.num_pages;
+        if (!ok) page = 0;
+        valid = __ballot(ok);
+        const uint32_t at = (uint32_t)(head * per + (ok ? block & (per - 1) : 0));
+        const uint8_t *p = b.cache + (uint64_t)page * (uint64_t)b.f.page_bytes();
+        scales = *reinterpret_cast<const uint32_t *>(p + b.f.scales_at() + at * 4);
+        const uint64_t k = (uint64_t)(uintptr_t)p + (uint64_t)at * (uint32_t)b.f.block_bytes();
+        lo = (uint32_t)k;
+        hi = (uint32_t)(k >> 32);
+    }
+    __device__ const uint8_t *at(int i) const {
+        const uint32_t l = __builtin_amdgcn_readlane((int)lo, i), h = __builtin_amdgcn_readlane((int)hi, i);
+        return (const uint8_t *)(uintptr_t)((uint64_t)h << 32 | l);
+    }
+    __device__ float k_scale(int i) const { return __uint_as_float((__builtin_amdgcn_readlane((int)scales, i) & 255u) << 23); }
+    __device__ float v_scale(int i) const { return __uint_as_float((__builtin_amdgcn_readlane((int)scales, i) & 0xFF00u) << 15); }
+    __device__ int number(int i) const { return __builtin_amdgcn_readlane(block, i); }
+    __device__ bool ok(int i) const { return (valid >> i) & 1; }
+};
+
+// The cache bytes of 64 tokens of one head that a lane multiplies.
+template <int D>
+struct Bytes {
+    u32x4 k[D / 16], v[D / 16];
+};
+
+// Lane (col, g): K units g + 4 u of tokens 16 j + col, V units g of channels 16 c + col.
+template <int D>
+struct Lane {
+    int col, g;
+    uint32_t k_off, v_off;
+    __device__ Lane(int lane) {
+        col = lane & 15;
+        g = lane >> 4;
+        k_off = (g * 64 + col) * 16;
+        v_off = 64 * D + (g * D + col) * 16;
+    }
+};
+
+template <int D, bool NT>
+__device__ __forceinline__ void load_block(Bytes<D> &x, const uint8_t *k, const Lane<D> &ln) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) x.k[i] = load_cache<NT, u32x4>(k + ln.k_off + (i >> 2) * 4096 + (i & 3) * 256);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) x.v[i] = load_cache<NT, u32x4>(k + ln.v_off + i * 256);
+}
+
+// Scores of 64 tokens: s[j][i] is token 16 j + 4 g + i of the column's row.
+template <int D>
+__device__ __forceinline__ void scores(const Bytes<D> &x, const Operand (&q)[D / 32], float scale, f32x4 (&s)[4]) {
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const u32x4 &w = x.k[u * 4 + j];
+                const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+                s[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(eight(w[2 * e], w[2 * e + 1], scale).h, q[2 * u + e].h,
+                                                               u + e ? s[j] : zero, 0, 0, 0);
+            }
+}
+
+// O += V^T P for 64 tokens: lane's row i of tile c is channel 16 c + 4 g + i.
+template <int D>
+__device__ __forceinline__ void add_values(Tile<D> &t, const Bytes<D> &x, const f32x4 (&p)[4], float scale) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        Operand b;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            b.w[2 * j] = pack_bf16(p[2 * s + j][0], p[2 * s + j][1]);
+            b.w[2 * j + 1] = pack_bf16(p[2 * s + j][2], p[2 * s + j][3]);
+        }
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+            t.o[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(eight(x.v[c][2 * s], x.v[c][2 * s + 1], scale).h, b.h, t.o[c], 0, 0, 0);
+    }
+}
+
+// Of four tokens from `tok` on, a byte each, those in [from, upto].
+__device__ __forceinline__ uint32_t seen_bytes(int tok, int from, int upto) {
+    const int lo = min(max(from - tok, 0), 4), hi = min(max(upto + 1 - tok, 0), 4);
+    const uint32_t below_hi = hi == 4 ? ~0u : (1u << (8 * hi)) - 1, below_lo = lo == 4 ? ~0u : (1u << (8 * lo)) - 1;
+    return below_hi & ~below_lo;
+}
+
+template <int D>
+__device__ __forceinline__ void store_row(const Kv8Attention &a, int t, int h, int g, const Tile<D> &tl, float m, float l) {
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    uint16_t *p = a.out.p + t * a.out.ld + h * a.out.hd + 4 * g;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+        uint2 w;
+        w.x = pack_bf16(tl.o[c][0] * inv, tl.o[c][1] * inv);
+        w.y = pack_bf16(tl.o[c][2] * inv, tl.o[c][3] * inv);
+        *reinterpret_cast<uint2 *>(p + 16 * c) = w;
+    }
+    if (g == 0 && a.lse) a.lse[t * a.ld_lse + h] = l != 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+}
+
+template <int D>
+__device__ __forceinline__ void keep_part(Part<D> &p, const Tile<D> &t, float c, const Lane<D> &ln) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) *reinterpret_cast<f32x4 *>(&p.o[ln.col][16 * i + 4 * ln.g]) = t.o[i];
+    const float l = cross_rows_sum(t.l);
+    if (ln.g == 0) {
+        p.m[ln.col] = t.m == -INFINITY ? -INFINITY : reference(t.m, c);
+        p.l[ln.col] = l;
+    }
+}
+
+// A row tile: rows r0 .. of the n * group of a sequence's (or of one token's) rows, and the keys they look at.
+struct Rows {
+    int s, q0, head, tile, rows;  // sequence, token row of row 0, key/value head, tile of 16 and its rows
+    int place;                    // of row 0's token
+    int see_end;                  // places below it hold keys
+    int last;                     // place of the last token among the rows that masks are asked for
+};
+
+// Blocks b0 .. b1 of the tile's list: all from block `first` on, or a row's selected ones.
+template <int D, bool NT, bool SEL>
+__device__ __forceinline__ void walk(const Kv8Attention &a, const Rows &r, int first, int b0, int b1, bool begins, bool ends, const Lane<D> &ln,
+                                     int lane, int wave, Shared<D> &sh) {
+    const int group = a.heads / a.b.f.n_kv;
+    const int32_t *row = a.b.table + (int64_t)r.s * a.b.ld_table;
+    const int32_t *list = SEL ? a.selected + (int64_t)r.q0 * a.ld_selected + (int64_t)r.head * a.top : nullptr;
+    Blocks lies;
+    int held = b0;
+    auto look = [&] {
+        if constexpr (SEL) {
+            const int i = held + lane;
+            const int b = i < b1 ? list[i] : -1;
+            lies.load(a.b, row, r.head, b <= r.place >> 6 ? b : -1);  // behind its own: none
+        } else {
+            lies.load(a.b, row, r.head, first + held + lane);
+        }
+    };
+    look();
+    Bytes<D> x0, x1;
+    load_block<D, NT>(x0, lies.at(0), ln);
+
+    // queries of my column
+    const int in = r.tile * kRows + ln.col;
+    const int qi = SEL ? 0 : in / group, t = r.q0 + qi, h = r.head * group + (in - qi * group);
+    const bool real = ln.col < r.rows && (uint32_t)t < (uint32_t)a.b.T;
+    Operand q[D / 32];
+    const uint16_t *from = a.q.p + t * a.q.ld + h * a.q.hd;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) q[i] = read_query(from + 64 * (i >> 1) + 16 * ln.g + 8 * (i & 1), real, a);
+    // keys that my row sees: [see_first, see_last]; that every row sees, and that any of them sees
+    const int place = r.place + qi;
+    auto first_of = [&](int p) { return a.window > 0 && p >= a.window ? (int)(p - a.window + 1) : 0; };
+    const int see_last = real ? min(place, r.see_end - 1) : -1, see_first = first_of(place);
+    const int all_first = first_of(r.last), all_last = min(r.place, r.see_end - 1);
+    const int any_first = first_of(r.place), any_last = min(r.last, r.see_end - 1);
+
+    Tile<D> tl;
+    clear(tl);
+    auto add = [&](Bytes<D> &x, int i, int b) {
+        const int j0 = (SEL ? lies.number(i) : first + b) * kBlock;
+        f32x4 sc[4];
+        scores<D>(x, q, lies.k_scale(i), sc);
+        if (j0 < all_first || j0 + (kBlock - 1) > all_last) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int tok = j0 + 16 * j + 4 * ln.g + e;
+                    if (tok > see_last || tok < see_first) sc[j][e] = -INFINITY;
+                }
+                // a weight of 0 times what an unseen place holds must be 0
+                const uint32_t keep = seen_bytes(j0 + 16 * j + 4 * ln.g, any_first, any_last);
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) x.v[c][j] &= keep;
+            }
+        }
+        weights(tl, sc, a.c);
+        add_values<D>(tl, x, sc, lies.v_scale(i));
+    };
+    // Behind the last block the loads, which are not branched around, go to the cache's first bytes for all waves.
+    for (int b = b0; b < b1; b += 2) {
+        if (b - held == Blocks::kAhead) {
+            held = b;
+            look();
+        }
+        const int i = b - held;
+        load_block<D, NT>(x1, b + 1 < b1 ? lies.at(i + 1) : a.b.cache, ln);
+        if (lies.ok(i)) add(x0, i, b);
+        if (b + 1 >= b1) break;
+        load_block<D, NT>(x0, b + 2 < b1 ? lies.at(i + 2) : a.b.cache, ln);
+        if (lies.ok(i + 1)) add(x1, i + 1, b + 1);
+    }
+
+    if (begins && ends) {
+        const float l = cross_rows_sum(tl.l);
+        if (real) store_row<D>(a, t, h, ln.g, tl, reference(tl.m, a.c), l);
+    } else {
+        const int slot = begins ? 1 : 0;
+        keep_part(sh.part[wave][slot], tl, a.c, ln);
+        if (lane == 0) sh.tag[wave][slot] = {ends ? kEnds : kThrough, r.q0, r.head, r.tile, r.rows, 0};
+    }
+}
+
+// Workgroup `block` of `blocks`: its waves' runs of the units of all sequences.
+template <int D, bool NT>
+__device__ __forceinline__ void decode(Kv8Attention &a, Part<D> *parts, PartTag *tags, Shared<D> &sh, int block, int blocks) {
+    a.b.f.dim = D;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int group = a.heads / a.b.f.n_kv, n_kv = a.b.f.n_kv;
+    const Lane<D> ln(lane);
+    const int64_t cap = (int64_t)a.b.cols * a.b.f.page;
+
+    // my run of units
+    SeqLane sl, behind;
+    sl.load(a.b, lane);
+    int64_t w = seq_from(a, group, sl.q0, sl.q1, sl.len).units(n_kv, a.whole);
+    int64_t upto = units_scan(w, lane);
+    int64_t total = lane64(upto, 63);
+    for (int s0 = 64; s0 < a.b.S; s0 += 64) {
+        if (s0 == 64) behind.load(a.b, s0 + lane);
+        const SeqLane x = behind;
+        behind.load(a.b, s0 + 64 + lane);
+        total += lane64(units_scan(seq_from(a, group, x.q0, x.q1, x.len).units(n_kv, a.whole), lane), 63);
+    }
+    const int64_t waves = (int64_t)blocks * kWaves;
+    const int64_t run = total < ((int64_t)1 << 31) ? (int64_t)(((uint32_t)total + (uint32_t)waves - 1) / (uint32_t)waves)
+                                                   : (total + waves - 1) / waves;
+    int64_t u = a.whole ? block : ((int64_t)block * kWaves + wave) * run;
+    const int64_t stop = a.whole ? u + 1 : u + run;
+    const int64_t end = stop < total ? stop : total;
+    if (lane < 2) sh.tag[wave][lane].state = kNone;
+
+    int s0 = 0;        // the 64 sequences that the lanes hold
+    int64_t base = 0;  // units before them
+    while (u < end) {
+        // the sequence that unit u is in
+        const uint64_t past = __ballot(base + upto > u);
+        if (!past) {
+            base += lane64(upto, 63);
+            s0 += 64;
+            sl.load(a.b, s0 + lane);
+            w = seq_from(a, group, sl.q0, sl.q1, sl.len).units(n_kv, a.whole);
+            upto = units_scan(w, lane);
+            continue;
+        }
+        const int at = __builtin_ctzll(past);
+        const Seq sq = seq_from(a, group, __builtin_amdgcn_readlane(sl.q0, at), __builtin_amdgcn_readlane(sl.q1, at),
+                                __builtin_amdgcn_readlane(sl.len, at));
+        const int64_t in = u - base - lane64(upto - w, at);
+        int item, b0, b1;
+        if (a.whole) {  // a unit is a row tile, a quarter of its blocks is mine (the last waves may have none)
+            const int mine = (sq.blocks + kWaves - 1) / kWaves;
+            item = (int)in;
+            b0 = wave * mine;
+            b1 = b0 + mine < sq.blocks ? b0 + mine : sq.blocks;
+            u = end;
+            if (b0 >= b1) break;
+        } else {
+            item = in < ((int64_t)1 << 31) ? (int)((uint32_t)in / (uint32_t)sq.blocks) : (int)(in / sq.blocks);
+            b0 = (int)(in - (int64_t)item * sq.blocks);
+            const int64_t room = end - u;
+            b1 = (int)(room < sq.blocks - b0 ? b0 + room : sq.blocks);
+            u += b1 - b0;
+        }
+        const int head = item / sq.tiles, tile = item - head * sq.tiles;
+        const int64_t left = (int64_t)sq.n * group - (int64_t)tile * kRows;
+        const Rows r = {s0 + at, sq.q0, head, tile, (int)(left < kRows ? left : kRows), sq.len - sq.n,
+                        (int)(sq.len < cap ? sq.len : cap), sq.len - 1};
+        walk<D, NT, false>(a, r, sq.first, b0, b1, b0 == 0, b1 == sq.blocks, ln, lane, wave, sh);
+    }
+    __syncthreads();
+    join_pieces<D>(a, parts, tags, sh, block);
+}
+
+template <int D, bool NT>
+__global__ __launch_bounds__(kWaves *kWave, 2) void kv8_decode_kernel(Kv8Attention a, Part<D> *parts, PartTag *tags) {
+    __shared__ Shared<D> sh;
+    decode<D, NT>(a, parts, tags, sh, blockIdx.x, gridDim.x);
+}
+
+// Selected blocks: items are (token, key/value head, tile of 16 of its rows), units the `top` blocks of each.  With a.whole an
+// item is a workgroup's, each wave takes a quarter of the blocks that the row has; else units are cut into runs.
+template <int D>
+__global__ __launch_bounds__(kWaves *kWave, 2) void kv8_selected_kernel(Kv8Attention a, Part<D> *parts, PartTag *tags) {
+    __shared__ Shared<D> sh;
+    a.b.f.dim = D;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n_kv = a.b.f.n_kv, group = a.heads / n_kv, subs = (group + kRows - 1) / kRows;
+    const Lane<D> ln(lane);
+    const int64_t cap = (int64_t)a.b.cols * a.b.f.page;
+    const int64_t items = (int64_t)a.b.T * n_kv * subs;
+    const int64_t total = a.whole ? items : items * a.top;
+    const int64_t waves = (int64_t)gridDim.x * kWaves, run = (total + waves - 1) / waves;
+    int64_t u = a.whole ? blockIdx.x : ((int64_t)blockIdx.x * kWaves + wave) * run;
+    const int64_t stop = a.whole ? u + 1 : u + run;
+    const int64_t end = stop < total ? stop : total;
+    if (lane < 2) sh.tag[wave][lane].state = kNone;
+    const int rows_end = uniform_load(a.b.q_start + a.b.S);
+    while (u < end) {
+        const int64_t item = a.whole ? u : u / a.top;
+        int b0 = a.whole ? 0 : (int)(u - item * a.top), b1, blocks = a.top;
+        const int th = (int)(item / subs), tile = (int)(item - (int64_t)th * subs);
+        const int t = th / n_kv, head = th - t * n_kv;
+        if (a.whole) {
+            u = end;
+            const int32_t *list = a.selected + (int64_t)t * a.ld_selected + (int64_t)head * a.top;
+            blocks = 1;  // up to the last one that is named
+            for (int i = 0; i < a.top; i += 64) {
+                const uint64_t some = __ballot(i + lane < a.top && list[min(i + lane, a.top - 1)] >= 0);
+                if (some) blocks = i + 64 - __clzll((long long)some);
+            }
+            const int mine = (blocks + kWaves - 1) / kWaves;
+            b0 = wave * mine;
+            b1 = min(b0 + mine, blocks);
+            if (b0 >= b1) break;
+        } else {
+            b1 = (int)(end - u < a.top - b0 ? b0 + (end - u) : a.top);
+            u += b1 - b0;
+        }
+        if (t >= rows_end) continue;
+        const int s = find_seq(a.b.q_start, a.b.S, t, lane);
+        const int q0 = uniform_load(a.b.q_start + s), q1 = uniform_load(a.b.q_start + s + 1), len = uniform_load(a.b.kv_len + s);
+        if (t < q0 || t >= q1) continue;
+        const int place = len - q1 + t;
+        const Rows r = {s, t, head, tile, min(kRows, group - tile * kRows), place, (int)(len < cap ? len : cap), place};
+        walk<D, true, true>(a, r, 0, b0, b1, b0 == 0, b1 == blocks, ln, lane, wave, sh);
+    }
+    __syncthreads();
+    join_pieces<D>(a, parts, tags, sh, blockIdx.x);
+}
+
+template <int D>
+__global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Attention a, const Part<D> *parts, const PartTag *tags) {
+    join_groups<D>(a, parts, tags);
+}
+
+// ---- prompts ----
+//
+// Many rows of a sequence: a workgroup takes kPromptRows rows of one key/value head, 32 a wave, and walks the blocks of 64 tokens that
+// the last of them sees, in 32 x 32 tiles.  Values are converted once for the 128 rows: a thread has the 16 + 16 tokens of one
+// channel that one lane half of a score tile has, and leaves them in LDS in the operand order of the product (two buffers, one
+// barrier a block).  Keys, which would need as much LDS bandwidth again, go from the page to each wave, which converts
+// its own.  The walk is a pipeline over tiles of 32 tokens, one step of which has the products of three of them, so that
+// matrix and vector instructions alternate within a wave: see `step`.
+constexpr int kPromptTile = 32;                       // rows of a wave
+constexpr int kPromptRows = kWaves * kPromptTile;     // rows of a workgroup
+
+// Lane (col, hh) = (lane % 32, lane / 32): column col is a query row, token rows of the scores are
+// 8 (i / 4) + 4 hh + i % 4 of a tile of 32, channel rows of O 32 mt + 8 (i / 4) + 4 hh + i % 4.
+template <int D>
+using Values = u32x4[2][4][D / 32][kWave];
+
+// Workgroup `block` of tiles * n_kv.
+template <int D>
+__device__ __forceinline__ void prompt(Kv8Attention &a, int tiles, Values<D> &values, int block) {
+    constexpr int MT = D / 32, KU = D / 32;  // channel tiles of the values, K units of a lane
+    a.b.f.dim = D;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 31, hh = lane >> 5;
+    const int group = a.heads / a.b.f.n_kv;
+
+    // Row tile: sequence s owns the tiles from q_start[s] * group / rows + s on, which are
+    // enough for it.  Later rows, which see more, go first; the heads of a tile go to
+    // neighbouring workgroups, that is to different XCDs, so an XCD reads few heads.
+    const int head = block % a.b.f.n_kv;
+    const int vt = tiles - 1 - block / a.b.f.n_kv;
+    int s = 0;
+    for (int n = a.b.S; n > 1;) {  // the last s whose first tile is at or before vt, 64 looks at a time
+        const int step = (n + 63) >> 6, at = s + lane * step;
+        const bool yes = lane * step < n && (uint32_t)(a.b.q_start[at] * group) / kPromptRows + at <= (uint32_t)vt;
+        const uint64_t m = __ballot(yes);
+        s += (m ? 63 - __clzll((long long)m) : 0) * step;
+        n = min(step, a.b.S - s);
+    }
+    const int q0 = uniform_load(a.b.q_start + s), n = uniform_load(a.b.q_start + s + 1) - q0;
+    const int len = uniform_load(a.b.kv_len + s);
+    const int rows = n * group;  // at most 2^30, as all rows of a call together
+    if (rows <= (a.b.S > 1 ? kDecodeRows : 0)) return;  // a lone sequence is all that there is
+    const int r0 = (vt - (int)((uint32_t)(q0 * group) / kPromptRows) - s) * kPromptRows;
+    if (r0 < 0 || r0 >= rows) return;
+
+    const float c = a.c;
+    const int64_t room = (int64_t)a.b.cols * a.b.f.page;
+    const int cap = len < room ? len : (int)room;  // tokens that have a place
+    const int place0 = len - n;                    // of the sequence's first row
+    // The first and the last key that a row at some place sees; the same for places at the end of the keys.
+    const int window = a.window > 0 && a.window < len ? (int)a.window : 0;
+    auto first_of = [&](int place) { return window && place >= window ? place - window + 1 : 0; };
+    auto last_of = [&](int place) { return place < cap ? place : cap - 1; };
+    const int any_from = first_of(place0), any_upto = cap - 1;
+
+    const int w0 = r0 + wave * kPromptTile;  // the wave's first row
+    const int r = w0 + col;
+    const int qi = (int)((uint32_t)r / (uint32_t)group), t = q0 + qi, h = head * group + (r - qi * group);
+    const bool real = r < rows && (uint32_t)t < (uint32_t)a.b.T;
+    Operand q[2 * KU];  // product 2 i + e: channels 32 i + 16 hh + 8 e ..
+#pragma unroll
+    for (int i = 0; i < 2 * KU; ++i) q[i] = read_query(a.q.p + t * a.q.ld + h * a.q.hd + 32 * (i >> 1) + 16 * hh + 8 * (i & 1), real, a);
+    const int upto = real ? last_of(place0 + qi) : -1, from = first_of(place0 + qi);
+    f32x16 o[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) o[i] = f32x16{};
+    float top = -INFINITY, off = 0.f, l = 0.f;  // weights are 2^((score - top) c - off); their sum
+    // what follows from top and off: the score that asks for new ones, what is taken from scores times c, and
+    // whether that is far from 0 for a row of the wave
+    float limit = -INFINITY, less = 0.f;
+    bool far = false;
+
+    // blocks that the workgroup walks, and those that need no mask for the wave
+    auto place_of = [&](int r) { return place0 + (int)((uint32_t)min(r, rows - 1) / (uint32_t)group); };
+    const int b_first = first_of(place_of(r0)) / kBlock;
+    const int see_last = last_of(place_of(r0 + kPromptRows - 1));
+    const int b_end = see_last >= 0 ? see_last / kBlock + 1 : 0;
+    const int w_all = last_of(place_of(w0)), w_all_from = first_of(place_of(w0 + kPromptTile - 1));
+
+    const int32_t *row = a.b.table + (int64_t)s * a.b.ld_table;
+    Blocks lies;
+    int held = b_first;  // first of the blocks whose places are held
+    lies.load(a.b, row, head, held + lane);
+
+    // keys: token 32 tt + col, units 2 i + hh
+    const uint32_t k_off = (hh * 64 + col) * 16;
+    u32x4 kx[2][KU];
+    float kscale[2];
+    auto load_keys = [&](int b, int tt) {
+        const uint8_t *kp = lies.at(b - held);
+        kscale[tt] = lies.k_scale(b - held);
+#pragma unroll
+        for (int i = 0; i < KU; ++i) kx[tt][i] = load_cache<false, u32x4>(kp + k_off + (tt * 512 + i * 2048));
+    };
+
+    // this thread's share of a block's values: channel vc of the lane half vh, tokens 16 j + 4 vh + {0..3, 8..11} for kShare of
+    // the four j, from vj on
+    constexpr int kShare = D / 32;
+    const int vc = (D == 128 ? wave * 32 : (wave & 1) * 32) + col, vh = hh, vj = D == 128 ? 0 : (wave >> 1) * 2;
+    const uint32_t v_off = 64 * D + (vh * D + vc) * 16 + vj * 4;
+    uint32_t vx[2][kShare];  // units vh and vh + 2
+    float vscale = 1.f;
+    auto load_values = [&](int b) {
+        const uint8_t *vp = lies.at(b - held) + v_off;
+        vscale = lies.v_scale(b - held);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if constexpr (D == 128) {
+                const u32x4 w = load_cache<false, u32x4>(vp + i * 32 * D);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) vx[i][j] = w[j];
+            } else {
+                typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+                const u32x2 w = load_cache<false, u32x2>(vp + i * 32 * D);
+                vx[i][0] = w[0];
+                vx[i][1] = w[1];
+            }
+        }
+    };
+    load_keys(b_first, 0);
+    load_keys(b_first, 1);
+    load_values(b_first);
+    // a weight of 0 times what an unseen place holds must be 0
+    auto hide_values = [&](int b) {
+        const int j0 = b * kBlock;
+        const bool page = lies.ok(b - held);
+        if (j0 < any_from || j0 + kBlock - 1 > any_upto || !page) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < kShare; ++j)
+                    vx[i][j] &= page ? seen_bytes(j0 + 16 * (vj + j) + 8 * i + 4 * vh, any_from, any_upto) : 0u;
+        }
+    };
+    auto operand = [&](int j) {
+        Operand x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x.w[k] = fp8_pair(vx[k >> 1][j], vscale, k & 1);
+        return x;
+    };
+    auto put_values = [&](int j, const Operand &x, u32x4 (*to)[MT][kWave]) { to[vj + j][vc >> 5][vh * 32 + (vc & 31)] = x.u; };
+
+    // Products of the scores: number i of a 32-token tile's 2 KU.
+    auto dot = [&](int tt, int i, f32x16 &acc) {
+        const f32x16 zero = {};
+        const u32x4 &w = kx[tt][i >> 1];
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(eight(w[2 * (i & 1)], w[2 * (i & 1) + 1], kscale[tt]).h, q[i].h, i ? acc : zero, 0, 0, 0);
+    };
+    constexpr int kDots = 2 * KU, kSums = 2 * MT;  // matrix products of a 32-token tile: scores, values
+    auto sum = [&](int i, const u32x4 &v, const uint32_t (&w)[8]) {
+        Operand x, y;
+        x.u = v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y.w[e] = w[4 * (i / MT) + e];
+        o[i % MT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x.h, y.h, o[i % MT], 0, 0, 0);
+    };
+    // Scores of tile tt of block b: unseen ones to -infinity.
+    auto hide = [&](int b, int tt, f32x16 &sc) {
+        const int j0 = b * kBlock + 32 * tt;
+        const bool page = lies.ok(b - held);
+        if (j0 < w_all_from || j0 + 31 > w_all || !page) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int tok = j0 + 8 * (i >> 2) + 4 * hh + (i & 3);
+                if (tok > upto || tok < from || !page) sc[i] = -INFINITY;
+            }
+        }
+    };
+    auto largest = [&](const f32x16 &sc) {
+        float x = __builtin_amdgcn_fmed3f(sc[0], sc[1], INFINITY), y = __builtin_amdgcn_fmed3f(sc[2], sc[3], INFINITY);
+#pragma unroll
+        for (int i = 4; i < 16; i += 4) {
+            x = __builtin_amdgcn_fmed3f(__builtin_amdgcn_fmed3f(x, sc[i], INFINITY), sc[i + 1], INFINITY);
+            y = __builtin_amdgcn_fmed3f(__builtin_amdgcn_fmed3f(y, sc[i + 2], INFINITY), sc[i + 3], INFINITY);
+        }
+        return halves_max(fmaxf(x, y));
+    };
+    // A new reference where a score has passed the old one.  The first is the largest score itself and kSlack,
+    // so that a lone key's weight is a power of two; the next ones lie whole powers of two from it, so that
+    // the weights w, which are rounded already and not yet multiplied, follow exactly; of one so far behind
+    // that nothing remains, the largest score begins anew.
+    auto raise = [&](float x, uint32_t (&w)[8]) {
+        if (__any(x > limit)) {
+            const float past = __builtin_fmaf(x - top, c, -off);  // NaN: neither has a key
+            const float by = floorf(past) + kSlack;
+            const bool anew = by > 150.f, mine = past > 0.f;
+            const float keep = mine ? __builtin_ldexpf(1.f, (int)fmaxf(-by, -1000.f)) : 1.f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) o[i] *= keep;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = pack_bf16(bf16_lo(w[i]) * keep, bf16_hi(w[i]) * keep);
+            l *= keep;
+            if (mine) off = anew ? kSlack : off + by;
+            if (mine && anew) top = x;
+            less = __builtin_fmaf(top == -INFINITY ? 0.f : top, c, off);
+            far = __any(fabsf(less) > kFar);
+            if (far) less = off;
+            limit = __builtin_fmaf(off, __builtin_amdgcn_rcpf(c), top);  // not above its exact value:
+            if (top != -INFINITY) limit = __builtin_fmaf(fabsf(limit), -0x1p-21f, limit);
+        }
+    };
+    // Where a reference is far from 0 the product of a score, rounded to be subtracted, would be off by more than the
+    // weights' own rounding: there scores become differences first.
+    auto relative = [&](f32x16 &sc) {
+        if (__builtin_expect(far, 0)) {
+            const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sc[i] -= base;
+        }
+    };
+
+    // Tile t = 2 b + tt: between them, product by product, the values of tile t (weights w are ready), the scores
+    // of tile t + 2 (into n), the softmax of tile t + 1 (scores sc to weights wn) and half of the conversion of
+    // block b + 1.
+    auto step = [&](int b, int tt, uint32_t (&w)[8], uint32_t (&wn)[8], f32x16 &sc, f32x16 &n) {
+        const u32x4 *from_lds = &values[b & 1][2 * tt][0][lane];
+        hide(tt ? b + 1 : b, tt ^ 1, sc);
+        raise(largest(sc), w);
+        relative(sc);
+        const float mc = less;
+        if (tt == 0) hide_values(b + 1);
+
+        constexpr int kRead = 3;  // value operands read ahead
+        u32x4 v[kRead];
+#pragma unroll
+        for (int i = 0; i < kRead - 1; ++i) v[i] = from_lds[i * kWave];
+        constexpr int kMine = kShare / 2;  // operands converted in a step
+        Operand cv[kMine];
+        float part = 0.f;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (k + kRead - 1 < kSums) v[(k + kRead - 1) % kRead] = from_lds[(k + kRead - 1) * kWave];
+            if (k < kSums) sum(k, v[k % kRead], w);
+            if (k < kDots) dot(tt, k, n);
+            const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[2 * k], c, -mc));
+            const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[2 * k + 1], c, -mc));
+            wn[k] = pack_bf16(e0, e1);
+            part += e0 + e1;
+            if (k < 4 * kMine) cv[k / 4].w[k % 4] = fp8_pair(vx[k % 4 / 2][kMine * tt + k / 4], vscale, k & 1);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 7, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 9, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // this step's work: not to be put off to where it is used
+        asm volatile("" : "+v"(n));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) asm volatile("" : "+v"(wn[k]));
+        l += part;
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) put_values(kMine * tt + j, cv[j], values[(b + 1) & 1]);
+        if (tt == 1) load_values(b + 2);
+        load_keys(b + 2, tt);
+    };
+
+    if (b_first < b_end) {
+        // fill the pipeline: values of the first block, scores of its two tiles, weights of the first
+        uint32_t wa[8], wb[8];
+        f32x16 sa, sb;
+        hide_values(b_first);
+#pragma unroll
+        for (int j = 0; j < kShare; ++j) put_values(j, operand(j), values[b_first & 1]);
+        load_values(b_first + 1);
+#pragma unroll
+        for (int i = 0; i < kDots; ++i) dot(0, i, sa);
+#pragma unroll
+        for (int i = 0; i < kDots; ++i) dot(1, i, sb);
+        load_keys(b_first + 1, 0);
+        load_keys(b_first + 1, 1);
+        hide(b_first, 0, sa);
+        {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) wa[k] = 0;
+            raise(largest(sa), wa);
+            relative(sa);
+            const float mc = less;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sa[2 * k], c, -mc));
+                const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sa[2 * k + 1], c, -mc));
+                wa[k] = pack_bf16(e0, e1);
+                l += e0 + e1;
+            }
+        }
+        __syncthreads();
+        int b = b_first;
+        do {
+            if (b - held == Blocks::kAhead) {
+                held = b;
+                lies.load(a.b, row, head, held + lane);
+            }
+            step(b, 0, wa, wb, sb, sa);
+            step(b, 1, wb, wa, sa, sb);
+            __syncthreads();
+        } while (++b < b_end);
+    }
+    l = halves_sum(l);
+    if (!real) return;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    uint16_t *out = a.out.p + t * a.out.ld + h * a.out.hd + 4 * hh;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint2 w;
+            w.x = pack_bf16(o[mt][4 * i] * inv, o[mt][4 * i + 1] * inv);
+            w.y = pack_bf16(o[mt][4 * i + 2] * inv, o[mt][4 * i + 3] * inv);
+            *reinterpret_cast<uint2 *>(out + 32 * mt + 8 * i) = w;
+        }
+    if (hh == 0 && a.lse) a.lse[t * a.ld_lse + h] = l != 0.f ? (__builtin_fmaf(top, c, off) + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+}
+
+// The first `groups` workgroups walk the sequences of few rows, the others take the prompts: while the ones
+// wait for memory the others multiply.
+template <int D>
+__global__ __launch_bounds__(kWaves *kWave, 2) void kv8_mixed_kernel(Kv8Attention a, Part<D> *parts, PartTag *tags,
+                                                                     int groups, int tiles) {
+    __shared__ union {
+        Shared<D> sh;
+        Values<D> values;
+    } lds;
+    if ((int)blockIdx.x < groups)
+        decode<D, false>(a, parts, tags, lds.sh, blockIdx.x, groups);
+    else
+        prompt<D>(a, tiles, lds.values, (int)blockIdx.x - groups);
+}
+
+// Few and short: a workgroup to each row tile (sequence s has none but its own of
+// q_start[s] * group / rows + s on, so their number is bounded), nothing to join.
+int64_t whole_tiles(int64_t T, int64_t S, int heads, int n_kv) { return (T * (heads / n_kv) / kRows + S) * n_kv; }
+bool whole(int64_t tiles, int groups, int64_t room) {
+    return tiles <= groups && room <= (4 * tiles < groups ? kWholeTokens : 4 * kWholeTokens);
+}
+
+// The same of selected blocks: their number is known.
+int64_t selected_items(int64_t T, int heads, int n_kv) { return T * n_kv * ((heads / n_kv + kRows - 1) / kRows); }
+bool selected_whole(int64_t items, int groups, int top) { return 2 * items >= groups || top <= 2 * kWaves; }
+
+template <int D>
+hipError_t launch(Kv8Attention a, int64_t max_q, void *ws, hipStream_t st) {
+    const int group = a.heads / a.b.f.n_kv;
+    const int groups = device_cus() * kGroupsPerCu;
+    Part<D> *parts = (Part<D> *)ws;
+    PartTag *tags = (PartTag *)(parts + 2 * (size_t)groups);
+    // Without a workspace (kv8_attention_workspace) nothing may be split between workgroups.
+    if (a.selected) {
+        const int64_t items = selected_items(a.b.T, a.heads, a.b.f.n_kv);
+        a.whole = selected_whole(items, groups, a.top);
+        kv8_selected_kernel<D><<<(unsigned)(a.whole ? items : groups), kWaves * kWave, 0, st>>>(a, parts, tags);
+        if (!a.whole) kv8_join_kernel<D><<<groups, 256, 0, st>>>(a, parts, tags);
+        return hipGetLastError();
+    }
+    const int64_t row_tiles = whole_tiles(a.b.T, a.b.S, a.heads, a.b.f.n_kv);
+    a.whole = whole(row_tiles, groups, (int64_t)a.b.cols * a.b.f.page);
+    // Where no sequence has many rows, or all rows make few row tiles for the machine's waves, every sequence is
+    // walked by row tiles, split over its keys; else each is taken as its own rows ask for.
+    a.prompts = !a.whole && max_q * group > kDecodeRows && (int64_t)a.b.T * a.heads > (int64_t)groups * kWaves * kRows / kFewTiles;
+    if (a.prompts) {
+        const int64_t tiles = (int64_t)a.b.T * group / kPromptRows + a.b.S;
+        const int first = a.b.S > 1 ? groups / kGroupsPerCu : 0;  // a lone sequence is a prompt whatever its rows
+        kv8_mixed_kernel<D><<<(unsigned)(first + tiles * a.b.f.n_kv), kWaves * kWave, 0, st>>>(a, parts, tags, first, (int)tiles);
+        if (first) kv8_join_kernel<D><<<first, 256, 0, st>>>(a, parts, tags);
+        return hipGetLastError();
+    }
+    const int grid = a.whole ? (int)row_tiles : groups;
+    if (max_q * group <= kRows)
+        kv8_decode_kernel<D, true><<<grid, kWaves * kWave, 0, st>>>(a, parts, tags);
+    else
+        kv8_decode_kernel<D, false><<<grid, kWaves * kWave, 0, st>>>(a, parts, tags);
+    if (!a.whole) kv8_join_kernel<D><<<groups, 256, 0, st>>>(a, parts, tags);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t kv8_attention_workspace(int64_t T, int64_t S, int heads, int n_kv, int dim, int64_t room, int top) {
+    const int groups = device_cus() * kGroupsPerCu;
+    if (top > 0 ? selected_whole(selected_items(T, heads, n_kv), groups, top) : whole(whole_tiles(T, S, heads, n_kv), groups, room)) return 0;
+    return dim == 128 ? decode_workspace<128>(groups) : decode_workspace<64>(groups);
+}
+
+hipError_t launch_kv8_attention(const Kv8Attention &a, int64_t max_q, void *ws, hipStream_t st) {
+    return a.b.f.dim == 128 ? launch<128>(a, max_q, ws, st) : launch<64>(a, max_q, ws, st);
+}
+
+}  // namespace nmk

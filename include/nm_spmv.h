@@ -476,6 +476,75 @@ nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int 
                            size_t workspace_bytes, void *hip_stream);
 
 /*
+ * The 8-bit key/value cache: the same step for models that lose by 4 bits, with what stands next to it in a decoder
+ * layer, the rotation of keys and queries by their places, and a choice of the blocks that a row looks at.
+ *
+ * Format.  uint8 [num_pages][page_bytes], page_bytes = nm_kv8_page_bytes(page_size, n_kv, head_dim)
+ * (D = head_dim 64 or 128; page_size 64, 128, 256 or 512 tokens; 8.14 bits per value).  A page has B = page_size / 64
+ * blocks of 64 tokens for each head:
+ *     values [n_kv][B]{ K [D/16][64][16] | V [4][D][16] } | bounds [n_kv][B][2][D] | scales [n_kv][B][4]
+ * bytes, and bytes up to a multiple of 128.  Values are OCP E4M3 numbers (no infinities; 0x7F and 0xFF are NaN); scale bytes 0
+ * and 1 are E8M0 numbers e for the keys and the values of one block: x = e4m3 * 2^(e - 127) (bytes 2 and 3: 0).  K unit
+ * [u][t] is channels 16u..16u+15 of token t of the block; V unit [g][c] is channel c of tokens 16j + 4g + i, at byte 4j + i.
+ * Bounds are the largest and the smallest key of the block in each channel, E4M3 at the keys' scale.
+ *
+ * A ragged batch and its token arrays are as above (nm_kv8_batch, nm_kv8_rows), and so are places that hold nothing: not
+ * written, read as zeros, left out.
+ *
+ * nm_kv8_append -- stores rows of k and v, after a rotation if there is one.  With (c, s) the cosine and sine of a row's place and
+ * pair of channels (x, y): (x c - y s, y c + x s), in fp64 for keys and rounded to E4M3 from there, in fp32 for queries and
+ * rounded to bf16.  Pair i is channels (i, i + rotary_dim / 2), or (2i, 2i + 1) where interleaved; channels from rotary_dim on stay.
+ * cos_sin: fp32 [positions][ld] of cosine and sine in turn, 16-byte aligned, ld a multiple of 4, positions >= table_cols *
+ * page_size; rotary_dim a multiple of 16.  q (n_heads heads) is rotated into q_out (q itself, or memory that does not
+ * overlap it); both NULL: keys alone.  A row of q whose place is below 0 or behind the table's last column is left as it is in q_out.
+ * The new tokens of a block need e = min(max(E - 8 + (m > 1.75), 63), 182), E the biased exponent of their largest magnitude and m
+ * its significand in [1, 2).  A block without earlier tokens takes that; one with earlier tokens of its sequence the larger of that and
+ * what it has, and where it grows, its earlier tokens and bounds are rounded again to the new scale.  Values are rounded to the nearest
+ * E4M3 multiple, ties to the even code, magnitudes above 448 (of numbers above 448 * 2^55) to 448.  Bounds of a block without earlier
+ * tokens are those of the new ones, else they widen.  (Tokens that a shorter length took back keep their part in scale and bounds until
+ * the block begins anew.)  A key that is an infinity or NaN after the rotation is kept as NaN and counts as 0 for scale and
+ * bounds; a value that is one is kept as 0, and the key of its token and head as NaN in channel 0: a row that sees the token gets NaN,
+ * no other row does.  T * n_kv <= 2^28, S * n_kv <= 2^21.  Blocks are read and written whole: a page that two sequences of a batch
+ * share must not be written by both (nm_kv_resize gives each a page of its own first).
+ *
+ * nm_kv8_unpack -- the same rows of the cache as bf16 (exact).
+ *
+ * nm_kv8_attention -- as nm_kv4_attention, with these differences.  Scores are those of the bf16 queries and the cached keys, kept in
+ * fp32; weights are rounded to bf16 for the product with the values.  Keys may be NaN (see above), values not.  scale is 0 or between
+ * 2^-60 and 2^60 in magnitude; sum_c |q_c K_jc| and |scale| times it < 2^125 for the keys a row sees.
+ * selected (int32 [T][n_kv][top], ld_selected entries from a row to the next) may be NULL; else a row looks, for the heads of each
+ * key/value head, at the keys of its `top` blocks selected[t][h][..] alone (block b: places 64 b .. 64 b + 63), as far as j <= p and the
+ * window go.  Entries below 0, behind the row's own block or without a page are left out; one that is named twice counts
+ * twice.  T * n_heads <= 2^23 then.  Workspace: nm_kv8_attention_workspace_bytes (top 0: no selected blocks).
+ *
+ * nm_kv8_select -- writes selected[t][h][..] for the rows of the sequences: of the blocks b <= p / 64 that have a page the first
+ * `first` and the last `last`, and those with the largest
+ *     score_b = sum_g sum_c max(q_gc most_bc, q_gc least_bc)
+ * over the query heads g of the key/value head h, most and least the block's bounds, a bound on its keys' sum of scores; of equal ones
+ * the lowest; `top` in all, in increasing order, -1 behind the last.  Scores are formed in fp64.  A row with an infinity or NaN among the
+ * queries of h takes the lowest.  first + last <= top <= 2^14, table_cols * page_size <= 2^20, T * n_kv <= 2^21.
+ */
+typedef nm_kv4_batch nm_kv8_batch;
+typedef nm_kv4_rows nm_kv8_rows;
+typedef struct {
+    const float *cos_sin; /* [positions][ld] */
+    int64_t ld, positions;
+    int rotary_dim, interleaved;
+} nm_kv8_rotation;
+int64_t nm_kv8_page_bytes(int page_size, int n_kv, int head_dim); /* 0 for sizes that are refused */
+nm_status nm_kv8_append(const nm_kv8_batch *batch, const nm_kv8_rows *k, const nm_kv8_rows *v,
+                        const nm_kv8_rotation *rotation, const nm_kv8_rows *q, int n_heads, const nm_kv8_rows *q_out,
+                        void *hip_stream);
+nm_status nm_kv8_unpack(const nm_kv8_batch *batch, const nm_kv8_rows *k, const nm_kv8_rows *v, void *hip_stream);
+nm_status nm_kv8_select(const nm_kv8_batch *batch, const nm_kv8_rows *q, int n_heads, int top, int first, int last,
+                        int32_t *selected, int64_t ld_selected, void *hip_stream);
+size_t nm_kv8_attention_workspace_bytes(int64_t T, int64_t S, int n_heads, int n_kv, int head_dim, int64_t max_q_len,
+                                        int64_t room, int top);
+nm_status nm_kv8_attention(const nm_kv8_batch *batch, const nm_kv8_rows *q, int n_heads, int64_t max_q_len, float scale,
+                           int64_t window, const int32_t *selected, int64_t ld_selected, int top, const nm_kv8_rows *out,
+                           float *lse, int64_t ld_lse, void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/*
  * Keeping the pages of a cache.  The state (nm_kv_book) is the page table (entries behind a
  * sequence's last page are -1), kv_len and a reference count per page: how many sequences
  * hold it, 0 = free.  One table serves the caches of all layers.  Free pages are
