@@ -222,9 +222,12 @@ def run(s):
 
         batch = s["cache"], s["table"], s["kv_len"], s["q_start"]
         if case["op"] == "append":
-            nm.nm_kv8_append(s["k"], s["v"], *batch, page, rotation=s["rotation"], interleaved=case["interleaved"], q=s["q"], q_out=s["q_out"])
+            if s["rotation"] is None:  # queries stay as they are
+                nm.nm_kv8_append(s["k"], s["v"], *batch, page)
+            else:
+                nm.nm_kv8_append(s["k"], s["v"], *batch, page, rotation=s["rotation"], interleaved=case["interleaved"], q=s["q"], q_out=s["q_out"])
             nm.nm_kv8_unpack(*batch, page, s["k_out"], s["v_out"])
-            return s["k_out"], s["v_out"], s["q_out"]
+            return s["k_out"], s["v_out"], s["q"] if s["rotation"] is None else s["q_out"]
         if case["op"] == "attention":
             return nm.nm_kv8_attention(s["q"], *batch, H, page, case["q"], window=case["window"], out=s["out"], lse=s["lse"])
         nm.nm_kv8_select(s["q"], *batch, H, page, case["top"], first=case["first"], last=case["last"], out=s["selected"])
