@@ -29,6 +29,7 @@ constexpr float kFar = 4096.f;  // reference (log2) up to which a rounded produc
 constexpr int kWholeTokens = 1024;  // context up to which each row tile may be one workgroup's, which needs no second launch
 constexpr int kFewTiles = 2;        // row tiles of a call, one to so many waves at most, up to which prompts are walked by row tiles too
 constexpr int kGroupsPerCu = 2;     // resident workgroups: 8 waves a CU
+constexpr int kJoinBlocks = 4;      // blocks that a wave walks in the time of a second launch
 
 __device__ __forceinline__ uint32_t fp8_pair(uint32_t w, float s, bool high) {
     union { bf16x2 h; uint32_t u; } c;
@@ -199,19 +200,17 @@ struct Rows {
 };
 
 // Blocks b0 .. b1 of the tile's list: all from block `first` on, or a row's selected ones.
-template <int D, bool NT, bool SEL>
+template <int D, bool NT, bool SEL, class L>
 __device__ __forceinline__ void walk(const Kv8Attention &a, const Rows &r, int first, int b0, int b1, bool begins, bool ends, const Lane<D> &ln,
-                                     int lane, int wave, Shared<D> &sh) {
+                                     int lane, int wave, Shared<D> *sh, L &&listed) {
     const int group = a.heads / a.b.f.n_kv;
     const int32_t *row = a.b.table + (int64_t)r.s * a.b.ld_table;
-    const int32_t *list = SEL ? a.selected + (int64_t)r.q0 * a.ld_selected + (int64_t)r.head * a.top : nullptr;
     Blocks lies;
     int held = b0;
     auto look = [&] {
         if constexpr (SEL) {
-            const int i = held + lane;
-            const int b = i < b1 ? list[i] : -1;
-            lies.load(a.b, row, r.head, b <= r.place >> 6 ? b : -1);  // behind its own: none
+            const int b = listed(held + lane);
+            lies.load(a.b, row, r.head, held + lane < b1 && b <= r.place >> 6 ? b : -1);  // behind its own: none
         } else {
             lies.load(a.b, row, r.head, first + held + lane);
         }
@@ -277,8 +276,8 @@ __device__ __forceinline__ void walk(const Kv8Attention &a, const Rows &r, int f
         if (real) store_row<D>(a, t, h, ln.g, tl, reference(tl.m, a.c), l);
     } else {
         const int slot = begins ? 1 : 0;
-        keep_part(sh.part[wave][slot], tl, a.c, ln);
-        if (lane == 0) sh.tag[wave][slot] = {ends ? kEnds : kThrough, r.q0, r.head, r.tile, r.rows, 0};
+        keep_part(sh->part[wave][slot], tl, a.c, ln);
+        if (lane == 0) sh->tag[wave][slot] = {ends ? kEnds : kThrough, r.q0, r.head, r.tile, r.rows, 0};
     }
 }
 
@@ -347,7 +346,7 @@ __device__ __forceinline__ void decode(Kv8Attention &a, Part<D> *parts, PartTag 
         const int64_t left = (int64_t)sq.n * group - (int64_t)tile * kRows;
         const Rows r = {s0 + at, sq.q0, head, tile, (int)(left < kRows ? left : kRows), sq.len - sq.n,
                         (int)(sq.len < cap ? sq.len : cap), sq.len - 1};
-        walk<D, NT, false>(a, r, sq.first, b0, b1, b0 == 0, b1 == sq.blocks, ln, lane, wave, sh);
+        walk<D, NT, false>(a, r, sq.first, b0, b1, b0 == 0, b1 == sq.blocks, ln, lane, wave, &sh, [](int) { return 0; });
     }
     __syncthreads();
     join_pieces<D>(a, parts, tags, sh, block);
@@ -359,55 +358,77 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv8_decode_kernel(Kv8Attenti
     decode<D, NT>(a, parts, tags, sh, blockIdx.x, gridDim.x);
 }
 
-// Selected blocks: items are (token, key/value head, tile of 16 of its rows), units the `top` blocks of each.  With a.whole an
-// item is a workgroup's, each wave takes a quarter of the blocks that the row has; else units are cut into runs.
-template <int D>
+// Selected blocks: items are (key/value head, token, tile of 16 of its rows), units the `top` blocks of each.  kItem: an item is a
+// workgroup's, each wave takes a quarter of the blocks that the row has.  kWave1: a wave's.  kRuns: units are cut into runs.
+// With kWave1 workgroups that go to one XCD take neighbouring items, tokens of few heads, whose blocks its L2 holds.
+enum : int { kItem = 0, kWave1 = 1, kRuns = 2 };
+constexpr int kXcds = 8;
+
+__device__ __forceinline__ int by_xcd(int block, int blocks) {
+    const int per = blocks / kXcds, rest = blocks % kXcds, xcd = block % kXcds;
+    return xcd * per + min(xcd, rest) + block / kXcds;
+}
+
+template <int D, int MODE>
 __global__ __launch_bounds__(kWaves *kWave, 2) void kv8_selected_kernel(Kv8Attention a, Part<D> *parts, PartTag *tags) {
-    __shared__ Shared<D> sh;
+    __shared__ Shared<D> shared;
+    Shared<D> *sh = MODE == kWave1 ? nullptr : &shared;
     a.b.f.dim = D;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n_kv = a.b.f.n_kv, group = a.heads / n_kv, subs = (group + kRows - 1) / kRows;
     const Lane<D> ln(lane);
     const int64_t cap = (int64_t)a.b.cols * a.b.f.page;
     const int64_t items = (int64_t)a.b.T * n_kv * subs;
-    const int64_t total = a.whole ? items : items * a.top;
-    const int64_t waves = (int64_t)gridDim.x * kWaves, run = (total + waves - 1) / waves;
-    int64_t u = a.whole ? blockIdx.x : ((int64_t)blockIdx.x * kWaves + wave) * run;
-    const int64_t stop = a.whole ? u + 1 : u + run;
-    const int64_t end = stop < total ? stop : total;
-    if (lane < 2) sh.tag[wave][lane].state = kNone;
-    const int rows_end = uniform_load(a.b.q_start + a.b.S);
+    const int me = MODE == kWave1 ? by_xcd(blockIdx.x, gridDim.x) : (int)blockIdx.x;
+    int64_t u, end;
+    if (MODE == kRuns) {
+        const int64_t total = items * a.top, waves = (int64_t)gridDim.x * kWaves, run = (total + waves - 1) / waves;
+        u = ((int64_t)me * kWaves + wave) * run;
+        end = u + run < total ? u + run : total;
+    } else {
+        u = MODE == kItem ? me : (int64_t)me * kWaves + wave;
+        end = u < items ? u + 1 : u;
+    }
+    if (MODE != kWave1 && lane < 2) sh->tag[wave][lane].state = kNone;
     while (u < end) {
-        const int64_t item = a.whole ? u : u / a.top;
-        int b0 = a.whole ? 0 : (int)(u - item * a.top), b1, blocks = a.top;
-        const int th = (int)(item / subs), tile = (int)(item - (int64_t)th * subs);
-        const int t = th / n_kv, head = th - t * n_kv;
-        if (a.whole) {
-            u = end;
-            const int32_t *list = a.selected + (int64_t)t * a.ld_selected + (int64_t)head * a.top;
-            blocks = 1;  // up to the last one that is named
-            for (int i = 0; i < a.top; i += 64) {
-                const uint64_t some = __ballot(i + lane < a.top && list[min(i + lane, a.top - 1)] >= 0);
-                if (some) blocks = i + 64 - __clzll((long long)some);
-            }
-            const int mine = (blocks + kWaves - 1) / kWaves;
-            b0 = wave * mine;
-            b1 = min(b0 + mine, blocks);
-            if (b0 >= b1) break;
-        } else {
+        const int64_t item = MODE == kRuns ? u / a.top : u;
+        const int ht = (int)(item / subs), tile = (int)(item - (int64_t)ht * subs);
+        const int head = ht / a.b.T, t = ht - head * a.b.T;
+        const int32_t *list = a.selected + (int64_t)t * a.ld_selected + (int64_t)head * a.top;
+        int b0 = 0, b1, blocks = a.top;
+        if (MODE == kRuns) {
+            b0 = (int)(u - item * a.top);
             b1 = (int)(end - u < a.top - b0 ? b0 + (end - u) : a.top);
             u += b1 - b0;
+        } else {
+            u = end;
         }
-        if (t >= rows_end) continue;
-        const int s = find_seq(a.b.q_start, a.b.S, t, lane);
-        const int q0 = uniform_load(a.b.q_start + s), q1 = uniform_load(a.b.q_start + s + 1), len = uniform_load(a.b.kv_len + s);
-        if (t < q0 || t >= q1) continue;
-        const int place = len - q1 + t;
-        const Rows r = {s, t, head, tile, min(kRows, group - tile * kRows), place, (int)(len < cap ? len : cap), place};
-        walk<D, true, true>(a, r, 0, b0, b1, b0 == 0, b1 == blocks, ln, lane, wave, sh);
+        const int entry = list[min(b0 + lane, a.top - 1)];
+        const RowSeq seq(a.b, t, lane);
+        if (t < seq.q0 || t >= seq.q1) continue;
+        if (MODE != kRuns) {
+            blocks = 1;  // up to the last one that is named
+            for (int i = 0; i < a.top; i += 64) {
+                const int e = i ? list[min(i + lane, a.top - 1)] : entry;
+                const uint64_t some = __ballot(i + lane < a.top && e >= 0);
+                if (some) blocks = i + 64 - __clzll((long long)some);
+            }
+            const int mine = MODE == kItem ? (blocks + kWaves - 1) / kWaves : blocks;
+            b0 = MODE == kItem ? wave * mine : 0;
+            b1 = min(b0 + mine, blocks);
+            if (b0 >= b1) continue;
+        }
+        const int place = seq.len - seq.q1 + t;
+        const Rows r = {seq.s, t, head, tile, min(kRows, group - tile * kRows), place, (int)(seq.len < cap ? seq.len : cap), place};
+        const int from = MODE == kRuns ? b0 : 0;  // entry is list[from + lane]
+        walk<D, MODE != kWave1, true>(a, r, 0, b0, b1, b0 == 0, b1 == blocks, ln, lane, wave, sh, [&](int i) {
+            if (b1 - from <= 64) return __shfl(entry, i - from);
+            return (int)list[min(i, a.top - 1)];
+        });
     }
+    if (MODE == kWave1) return;
     __syncthreads();
-    join_pieces<D>(a, parts, tags, sh, blockIdx.x);
+    join_pieces<D>(a, parts, tags, *sh, me);
 }
 
 template <int D>
@@ -752,9 +773,14 @@ bool whole(int64_t tiles, int groups, int64_t room) {
     return tiles <= groups && room <= (4 * tiles < groups ? kWholeTokens : 4 * kWholeTokens);
 }
 
-// The same of selected blocks: their number is known.
+// The same of selected blocks: their number is known.  A wave to each item where there are items for all of them, or a workgroup, or, where
+// that would leave many blocks to few, equal runs and a second launch.
 int64_t selected_items(int64_t T, int heads, int n_kv) { return T * n_kv * ((heads / n_kv + kRows - 1) / kRows); }
-bool selected_whole(int64_t items, int groups, int top) { return 2 * items >= groups || top <= 2 * kWaves; }
+int selected_mode(int64_t items, int groups, int top) {
+    if (items >= groups) return kWave1;
+    const int64_t whole = (top + kWaves - 1) / kWaves, runs = (items * top + groups * kWaves - 1) / (groups * kWaves);
+    return whole <= runs + kJoinBlocks ? kItem : kRuns;
+}
 
 template <int D>
 hipError_t launch(Kv8Attention a, int64_t max_q, void *ws, hipStream_t st) {
@@ -765,9 +791,16 @@ hipError_t launch(Kv8Attention a, int64_t max_q, void *ws, hipStream_t st) {
     // Without a workspace (kv8_attention_workspace) nothing may be split between workgroups.
     if (a.selected) {
         const int64_t items = selected_items(a.b.T, a.heads, a.b.f.n_kv);
-        a.whole = selected_whole(items, groups, a.top);
-        kv8_selected_kernel<D><<<(unsigned)(a.whole ? items : groups), kWaves * kWave, 0, st>>>(a, parts, tags);
-        if (!a.whole) kv8_join_kernel<D><<<groups, 256, 0, st>>>(a, parts, tags);
+        const int mode = selected_mode(items, groups, a.top);
+        a.whole = mode != kRuns;
+        if (mode == kWave1) {
+            kv8_selected_kernel<D, kWave1><<<(unsigned)((items + kWaves - 1) / kWaves), kWaves * kWave, 0, st>>>(a, parts, tags);
+        } else if (mode == kItem) {
+            kv8_selected_kernel<D, kItem><<<(unsigned)items, kWaves * kWave, 0, st>>>(a, parts, tags);
+        } else {
+            kv8_selected_kernel<D, kRuns><<<groups, kWaves * kWave, 0, st>>>(a, parts, tags);
+            kv8_join_kernel<D><<<groups, 256, 0, st>>>(a, parts, tags);
+        }
         return hipGetLastError();
     }
     const int64_t row_tiles = whole_tiles(a.b.T, a.b.S, a.heads, a.b.f.n_kv);
@@ -795,7 +828,7 @@ hipError_t launch(Kv8Attention a, int64_t max_q, void *ws, hipStream_t st) {
 
 size_t kv8_attention_workspace(int64_t T, int64_t S, int heads, int n_kv, int dim, int64_t room, int top) {
     const int groups = device_cus() * kGroupsPerCu;
-    if (top > 0 ? selected_whole(selected_items(T, heads, n_kv), groups, top) : whole(whole_tiles(T, S, heads, n_kv), groups, room)) return 0;
+    if (top > 0 ? selected_mode(selected_items(T, heads, n_kv), groups, top) != kRuns : whole(whole_tiles(T, S, heads, n_kv), groups, room)) return 0;
     return dim == 128 ? decode_workspace<128>(groups) : decode_workspace<64>(groups);
 }
 

@@ -41,6 +41,28 @@ __device__ __forceinline__ int seq_of_row(const int32_t *q_start, int S, int s, 
     return s;
 }
 
+// Row t's sequence, called by a whole wave with one t: up to 64 sequences are read at once, with what is wanted of them.
+struct RowSeq {
+    int s, q0, q1, len;
+    template <class B>
+    __device__ __forceinline__ RowSeq(const B &b, int t, int lane) {
+        if (b.S <= kWave) {
+            const int i = min(lane, b.S - 1);
+            const int from = b.q_start[i], to = b.q_start[i + 1], n = b.kv_len[i];
+            const uint64_t m = __ballot(lane < b.S && from <= t);
+            s = m ? 63 - __clzll((long long)m) : 0;
+            q0 = __builtin_amdgcn_readlane(from, s);
+            q1 = __builtin_amdgcn_readlane(to, s);
+            len = __builtin_amdgcn_readlane(n, s);
+        } else {
+            s = __builtin_amdgcn_readfirstlane(find_seq(b.q_start, b.S, t, lane));
+            q0 = b.q_start[s];
+            q1 = b.q_start[s + 1];
+            len = b.kv_len[s];
+        }
+    }
+};
+
 // Where row t is kept: the head-0 block of its page and its token within the page; null
 // where the sequence has no place or no valid page for it.
 template <class B>
