@@ -86,16 +86,29 @@ struct Unit {
 
 template <class B>
 __device__ __forceinline__ bool find_unit(const B &b, int slot, int lane, Unit &u) {
-    int s = 0;
-    for (int n = b.S; n > 1;) {  // the last s whose first block is at or before the slot, 64 looks at a time
-        const int step = (n + 63) >> 6, at = s + lane * step;
-        const bool yes = lane * step < n && (b.q_start[at] >> 6) + 2 * at <= slot;
-        const uint64_t m = __ballot(yes);
-        s += (m ? 63 - __clzll((long long)m) : 0) * step;
-        n = min(step, b.S - s);
+    int s = 0, q0, n, len;
+    if (b.S <= kWave) {  // all of them read at once
+        const int i = min(lane, b.S - 1);
+        const int from = b.q_start[i], to = b.q_start[i + 1], l = b.kv_len[i];
+        const uint64_t m = __ballot(lane < b.S && (from >> 6) + 2 * lane <= slot);
+        s = m ? 63 - __clzll((long long)m) : 0;
+        q0 = __builtin_amdgcn_readlane(from, s);
+        n = __builtin_amdgcn_readlane(to, s) - q0;
+        len = __builtin_amdgcn_readlane(l, s);
+    } else {
+        for (int left = b.S; left > 1;) {  // the last s whose first block is at or before the slot, 64 looks at a time
+            const int step = (left + 63) >> 6, at = s + lane * step;
+            const bool yes = lane * step < left && (b.q_start[at] >> 6) + 2 * at <= slot;
+            const uint64_t m = __ballot(yes);
+            s += (m ? 63 - __clzll((long long)m) : 0) * step;
+            left = min(step, b.S - s);
+        }
+        s = __builtin_amdgcn_readfirstlane(s);
+        q0 = b.q_start[s];
+        n = b.q_start[s + 1] - q0;
+        len = b.kv_len[s];
     }
-    s = __builtin_amdgcn_readfirstlane(s);
-    const int q0 = b.q_start[s], n = b.q_start[s + 1] - q0, len = b.kv_len[s], begin = len - n;
+    const int begin = len - n;
     if (n <= 0) return false;
     u.s = s;
     u.block = (begin >> 6) + slot - (q0 >> 6) - 2 * s;  // rounded down, also below 0
@@ -158,15 +171,192 @@ struct AppendShared {
     float most[4][D], least[4][D];
 };
 
+// What a block's new tokens need, and what its earlier ones are multiplied with: 1 unless the scale grows.
+struct Scales {
+    int kbyte, vbyte, kwas;
+    float kdown, vdown, kmore, vmore;
+    template <int D>
+    __device__ __forceinline__ Scales(const AppendShared<D> &sh, bool had, uint32_t was) {
+        const uint32_t ktop = max(max(sh.top[0][0], sh.top[0][1]), max(sh.top[0][2], sh.top[0][3]));
+        const uint32_t vtop = max(max(sh.top[1][0], sh.top[1][1]), max(sh.top[1][2], sh.top[1][3]));
+        kwas = min((int)(was & 255u), kHigh);
+        const int vwas = min((int)(was >> 8 & 255u), kHigh);
+        kbyte = had ? max(scale_byte(ktop), kwas) : scale_byte(ktop);
+        vbyte = had ? max(scale_byte(vtop), vwas) : scale_byte(vtop);
+        kdown = pow2_byte(254 - kbyte);
+        vdown = pow2_byte(254 - vbyte);
+        kmore = had ? pow2_byte(max(127 + kwas - kbyte, 0)) : 1.f;
+        vmore = had ? pow2_byte(max(127 + vwas - vbyte, 0)) : 1.f;
+    }
+};
+
+// Tokens before `lo` of the block's keys, times `more`: a unit of 16 channels a thread.
 template <int D>
-__device__ __forceinline__ void append(const Kv8Batch &b, const KvRows &k, const KvRows &v, const KvRotation &r, int slot, int head,
+__device__ __forceinline__ void earlier_keys(uint8_t *block, int lo, float more) {
+    for (int i = threadIdx.x; i < D / 16 * lo; i += kThreads) {
+        u32x4 *p = reinterpret_cast<u32x4 *>(block + ((i / lo) * 64 + i % lo) * 16);
+        u32x4 w = *p;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = again(w[e], more);
+        *p = w;
+    }
+}
+
+// Of the four tokens from `tok` on, a byte each, those before `lo` times `more`.
+__device__ __forceinline__ uint32_t earlier_values(uint32_t w, int tok, int lo, float more) {
+    const int n = min(max(lo - tok, 0), 4);
+    const uint32_t early = n == 4 ? ~0u : (1u << (8 * n)) - 1;
+    return (again(w, more) & early) | (w & ~early);
+}
+
+// Bounds of a block: of the new tokens (in LDS, by wave) and, if there were some, what it has.
+template <int D>
+__device__ __forceinline__ void store_bounds(const AppendShared<D> &sh, const Scales &sc, bool had, uint8_t *bounds, uint8_t *scales) {
+    if (threadIdx.x < D) {  // two bounds of a channel
+        const int c = threadIdx.x;
+        float a = fmaxf(fmaxf(sh.most[0][c], sh.most[1][c]), fmaxf(sh.most[2][c], sh.most[3][c]));
+        float d = fminf(fminf(sh.least[0][c], sh.least[1][c]), fminf(sh.least[2][c], sh.least[3][c]));
+        if (had) {
+            const float scale = pow2_byte((uint32_t)sc.kwas);
+            a = fmaxf(a, __builtin_amdgcn_cvt_f32_fp8((int)bounds[c], 0) * scale);
+            d = fminf(d, __builtin_amdgcn_cvt_f32_fp8((int)bounds[D + c], 0) * scale);
+        }
+        const uint32_t w = codes<false>(a, d, sc.kdown, 0);
+        bounds[c] = (uint8_t)w;
+        bounds[D + c] = (uint8_t)(w >> 8);
+    }
+    if (threadIdx.x == 0) *reinterpret_cast<uint32_t *>(scales) = (uint32_t)sc.kbyte | (uint32_t)sc.vbyte << 8;
+}
+
+// Up to kFewTokens new tokens of a block and head: a lane has two channels of a token.  Little code, which is run once and read from
+// memory (48 sequences, a token each: 13.0 us by the code for many tokens, 6.7 by this).
+constexpr int kFewTokens = 8;
+template <int D>
+__device__ __forceinline__ void append_few(const Kv8Batch &b, const KvRows &k, const KvRows &v, const KvRotation &r, const Unit &u, int head,
+                                           AppendShared<D> &sh) {
+    constexpr int kLanes = D / 2, kAtOnce = 4 * kWave / kLanes, kPasses = kFewTokens / kAtOnce;  // lanes to a token, tokens of the workgroup
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int at = head * b.f.blocks() + u.in_page;
+    uint8_t *block = u.page + at * b.f.block_bytes();
+    uint8_t *bounds = u.page + b.f.bounds_at() + at * 2 * D, *scales = u.page + b.f.scales_at() + at * 4;
+    const bool had = u.lo > 0;
+    const uint32_t was = had ? *reinterpret_cast<const uint32_t *>(scales) : 0u;
+    const int c = 2 * (lane % kLanes), first = u.lo + (int)(threadIdx.x / kLanes);
+    // the channels that mine are turned with, the pair of the first and whether mine are the second of theirs
+    const bool turned = c < r.dim, second = !r.interleaved && c >= r.dim / 2;
+    const int other = !turned || r.interleaved ? c : second ? c - r.dim / 2 : c + r.dim / 2;
+    const int pair = r.interleaved ? c / 2 : second ? c - r.dim / 2 : c;
+
+    uint32_t kx[kPasses], ko[kPasses], vx[kPasses];
+    f32x2 t0[kPasses], t1[kPasses];
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+        const int tok = first + p * kAtOnce;
+        kx[p] = ko[p] = vx[p] = 0;
+        t0[p] = t1[p] = (f32x2){1.f, 0.f};
+        if (tok < u.hi) {
+            const int64_t t = u.t + tok - u.lo;
+            const uint16_t *from = k.p + t * k.ld + head * k.hd;
+            kx[p] = *reinterpret_cast<const uint32_t *>(from + c);
+            ko[p] = *reinterpret_cast<const uint32_t *>(from + other);
+            vx[p] = *reinterpret_cast<const uint32_t *>(v.p + t * v.ld + head * v.hd + c);
+            if (turned) {
+                const f32x2 *turn = reinterpret_cast<const f32x2 *>(r.cos_sin + ((int64_t)u.block * 64 + tok) * r.ld);
+                t0[p] = turn[pair];
+                t1[p] = r.interleaved ? t0[p] : turn[pair + 1];
+            }
+        }
+    }
+    float y[kPasses][2];
+    uint32_t ktop = 0, vtop = 0;
+    bool lost[kPasses];
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+        const float x0 = bf16_lo(kx[p]), x1 = bf16_hi(kx[p]);
+        y[p][0] = x0;
+        y[p][1] = x1;
+        if (turned) {
+            const float o0 = r.interleaved ? x1 : bf16_lo(ko[p]), o1 = r.interleaved ? x0 : bf16_hi(ko[p]);
+            const double s0 = second ? (double)t0[p][1] : -(double)t0[p][1], s1 = second || r.interleaved ? (double)t1[p][1] : -(double)t1[p][1];
+            y[p][0] = narrowed(__builtin_fma((double)x0, (double)t0[p][0], (double)o0 * s0));
+            y[p][1] = narrowed(__builtin_fma((double)x1, (double)t1[p][0], (double)o1 * s1));
+        }
+        if (first + p * kAtOnce >= u.hi) y[p][0] = y[p][1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t m = __float_as_uint(y[p][i]) & 0x7FFFFFFFu;
+            ktop = max(ktop, m < 0x7F800000u ? m : 0u);
+        }
+        const uint32_t lo = vx[p] << 16 & 0x7FFFFFFFu, hi = vx[p] & 0x7FFF0000u;
+        vx[p] &= (lo >= 0x7F800000u ? 0xFFFF0000u : ~0u) & (hi >= 0x7F800000u ? 0xFFFFu : ~0u);
+        const uint64_t m = __ballot(lo >= 0x7F800000u || hi >= 0x7F800000u);
+        lost[p] = D == 128 ? m != 0 : (lane < 32 ? (uint32_t)m : (uint32_t)(m >> 32)) != 0;
+        vtop = max(vtop, max(vx[p] << 16 & 0x7FFFFFFFu, vx[p] & 0x7FFF0000u));
+    }
+    ktop = wave_max(ktop);
+    vtop = wave_max(vtop);
+    if (lane == 0) {
+        sh.top[0][wave] = ktop;
+        sh.top[1][wave] = vtop;
+    }
+    __syncthreads();
+    const Scales sc(sh, had, was);
+    if (sc.kmore != 1.f) earlier_keys<D>(block, u.lo, sc.kmore);
+    if (sc.vmore != 1.f) {
+        for (int i = threadIdx.x; i < 4 * D; i += kThreads) {
+            u32x4 *p = reinterpret_cast<u32x4 *>(block + 64 * D + i * 16);
+            u32x4 w = *p;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = earlier_values(w[j], 16 * j + 4 * (i / D), u.lo, sc.vmore);
+            *p = w;
+        }
+        __syncthreads();  // new tokens have bytes in the same units
+    }
+    float most[2] = {-INFINITY, -INFINITY}, least[2] = {INFINITY, INFINITY};
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+        const int tok = first + p * kAtOnce;
+        if (tok >= u.hi) break;
+        uint32_t w = codes<false>(y[p][0], y[p][1], sc.kdown, 0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if ((__float_as_uint(y[p][i]) & 0x7FFFFFFFu) >= 0x7F800000u) {
+                w = (w & ~(255u << (8 * i))) | kNaN8 << (8 * i);
+                y[p][i] = 0.f;
+            }
+            most[i] = fmaxf(most[i], y[p][i]);
+            least[i] = fminf(least[i], y[p][i]);
+        }
+        if (c == 0 && lost[p]) w = (w & ~255u) | kNaN8;
+        *reinterpret_cast<uint16_t *>(block + b.f.k_byte(tok, c)) = (uint16_t)w;
+        const uint32_t x = codes<false>(bf16_lo(vx[p]), bf16_hi(vx[p]), sc.vdown, 0);
+        uint8_t *to = block + b.f.v_byte(tok, c);
+        to[0] = (uint8_t)x;
+        to[16] = (uint8_t)(x >> 8);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (D == 64) {  // two tokens a wave
+            const uint32_t a = __float_as_uint(most[i]), d = __float_as_uint(least[i]);
+            const auto p = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+            const auto q = __builtin_amdgcn_permlane32_swap(d, d, false, false);
+            most[i] = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+            least[i] = fminf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+        }
+        sh.most[wave][c + i] = most[i];
+        sh.least[wave][c + i] = least[i];
+    }
+    __syncthreads();
+    store_bounds(sh, sc, had, bounds, scales);
+}
+
+template <int D>
+__device__ __forceinline__ void append(const Kv8Batch &b, const KvRows &k, const KvRows &v, const KvRotation &r, const Unit &u, int head,
                                        AppendShared<D> &sh) {
     constexpr int kSlots = D / 16, kTokens = kThreads / kSlots, kPasses = 64 / kTokens;  // D 128: 32 tokens in 2 passes
     constexpr int kJ = D / 32;  // of the four j of a V unit, those that a thread has
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    Unit u;
-    if (!find_unit(b, slot, lane, u) || !u.page) return;  // the whole workgroup
-    const int per = b.f.blocks(), at = head * per + u.in_page;
+    const int at = head * b.f.blocks() + u.in_page;
     uint8_t *block = u.page + at * b.f.block_bytes();
     uint8_t *bounds = u.page + b.f.bounds_at() + at * 2 * D, *scales = u.page + b.f.scales_at() + at * 4;
     const bool had = u.lo > 0;
@@ -251,23 +441,9 @@ __device__ __forceinline__ void append(const Kv8Batch &b, const KvRows &k, const
         sh.bad[wave] = bad;
     }
     __syncthreads();
-    ktop = max(max(sh.top[0][0], sh.top[0][1]), max(sh.top[0][2], sh.top[0][3]));
-    vtop = max(max(sh.top[1][0], sh.top[1][1]), max(sh.top[1][2], sh.top[1][3]));
-    const int kwas = min((int)(was & 255u), kHigh), vwas = min((int)(was >> 8 & 255u), kHigh);
-    const int kbyte = had ? max(scale_byte(ktop), kwas) : scale_byte(ktop), vbyte = had ? max(scale_byte(vtop), vwas) : scale_byte(vtop);
-    const float kdown = pow2_byte(254 - kbyte), vdown = pow2_byte(254 - vbyte);
-    // what earlier tokens are multiplied with, 1 unless the scale grows
-    const float kmore = had ? pow2_byte(max(127 + kwas - kbyte, 0)) : 1.f, vmore = had ? pow2_byte(max(127 + vwas - vbyte, 0)) : 1.f;
-
-    if (kmore != 1.f) {  // earlier keys, a unit of 16 channels a thread
-        for (int i = threadIdx.x; i < kSlots * u.lo; i += kThreads) {
-            u32x4 *p = reinterpret_cast<u32x4 *>(block + ((i / u.lo) * 64 + i % u.lo) * 16);
-            u32x4 w = *p;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = again(w[e], kmore);
-            *p = w;
-        }
-    }
+    const Scales sc(sh, had, was);
+    const float kdown = sc.kdown, vdown = sc.vdown, vmore = sc.vmore;
+    if (sc.kmore != 1.f) earlier_keys<D>(block, u.lo, sc.kmore);
     float most[16], least[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -329,12 +505,7 @@ __device__ __forceinline__ void append(const Kv8Batch &b, const KvRows &k, const
                     const uint32_t m = mine >> (4 * j) & 15u;
                     const uint32_t keep = (m & 1 ? 0u : 255u) | (m & 2 ? 0u : 255u << 8) | (m & 4 ? 0u : 255u << 16) | (m & 8 ? 0u : 255u << 24);
                     uint32_t old = p[j];
-                    if (vmore != 1.f) {
-                        const int tok = 16 * (vj + j) + 4 * wave;  // those before the new ones
-                        const int n = min(max(u.lo - tok, 0), 4);
-                        const uint32_t early = n == 4 ? ~0u : (1u << (8 * n)) - 1;
-                        old = (again(old, vmore) & early) | (old & ~early);
-                    }
+                    if (vmore != 1.f) old = earlier_values(old, 16 * (vj + j) + 4 * wave, u.lo, vmore);
                     w[j] = (w[j] & ~keep) | (old & keep);
                 }
             }
@@ -346,20 +517,7 @@ __device__ __forceinline__ void append(const Kv8Batch &b, const KvRows &k, const
         }
     }
     __syncthreads();
-    if (threadIdx.x < D) {  // two bounds of a channel
-        const int c = threadIdx.x;
-        float a = fmaxf(fmaxf(sh.most[0][c], sh.most[1][c]), fmaxf(sh.most[2][c], sh.most[3][c]));
-        float d = fminf(fminf(sh.least[0][c], sh.least[1][c]), fminf(sh.least[2][c], sh.least[3][c]));
-        if (had) {
-            const float scale = pow2_byte((uint32_t)kwas);
-            a = fmaxf(a, __builtin_amdgcn_cvt_f32_fp8((int)bounds[c], 0) * scale);
-            d = fminf(d, __builtin_amdgcn_cvt_f32_fp8((int)bounds[D + c], 0) * scale);
-        }
-        const uint32_t w = codes<false>(a, d, kdown, 0);
-        bounds[c] = (uint8_t)w;
-        bounds[D + c] = (uint8_t)(w >> 8);
-    }
-    if (threadIdx.x == 0) *reinterpret_cast<uint32_t *>(scales) = (uint32_t)kbyte | (uint32_t)vbyte << 8;
+    store_bounds(sh, sc, had, bounds, scales);
 }
 
 // Queries: a wave takes a token, its lanes 16 channels each of several heads at once.
@@ -407,7 +565,12 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Batch b, KvRows
     b.f.dim = D;
     const int i = blockIdx.x;
     if (i < blocks) {
-        append<D>(b, k, v, r, i / b.f.n_kv, i % b.f.n_kv, sh);
+        Unit u;
+        if (!find_unit(b, i / b.f.n_kv, threadIdx.x & 63, u) || !u.page) return;  // the whole workgroup
+        if (u.hi - u.lo <= kFewTokens)
+            append_few<D>(b, k, v, r, u, i % b.f.n_kv, sh);
+        else
+            append<D>(b, k, v, r, u, i % b.f.n_kv, sh);
     } else {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         turn_queries<D>(b, r, q, out, heads, (i - blocks) * 4 + wave);

@@ -763,7 +763,7 @@ __global__ __launch_bounds__(kMaxWaves *kWave) void kv8_select_kernel(Kv8Select 
 
 // ---- sixteen rows of a sequence and a head ----
 
-constexpr int kTileWaves = 4;
+constexpr int kTileWaves = 8;
 
 // What the rows of a tile keep in LDS before their keys.
 template <int D>
@@ -805,7 +805,7 @@ __global__ __launch_bounds__(kTileWaves *kWave) void kv8_select_tile_kernel(Kv8S
 
     // sums of queries: 16 threads (or 8) a row, 8 channels each, positive parts and negative ones
     const int row = threadIdx.x >> 4, c8 = threadIdx.x & 15;
-    {
+    if (row < kTileRows) {  // whole waves
         double sum[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) sum[i] = 0.0;
@@ -906,7 +906,9 @@ __global__ __launch_bounds__(kTileWaves *kWave) void kv8_select_tile_kernel(Kv8S
     largest = wave_max(largest);
     if (lane == 0) sh.scales[wave] = largest;
     __syncthreads();
-    largest = max(max(sh.scales[0], sh.scales[1]), max(sh.scales[2], sh.scales[3]));
+    largest = 0;
+#pragma unroll
+    for (int w = 0; w < kTileWaves; ++w) largest = max(largest, sh.scales[w]);
     for (int r = wave; r < rows; r += kTileWaves) {
         const Ask ask(a, place0 + r);
         rb.q = a.q.p + (int64_t)(t0 + r) * a.q.ld + (int64_t)head * group * a.q.hd;
