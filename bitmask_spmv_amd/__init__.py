@@ -34,7 +34,7 @@ __all__ = [
     "nm_spmv_noalloc", "nm_kv4_page_bytes", "nm_kv4_append", "nm_kv4_unpack", "nm_kv4_attention",
     "nm_kv4_attention_workspace_bytes", "nm_kv_pages_workspace_bytes", "nm_kv_resize", "nm_kv_fork",
     "nm_kv_compact", "nm_kv_copy_pages", "nm_kv8_page_bytes", "nm_kv8_append", "nm_kv8_unpack", "nm_kv8_select",
-    "nm_kv8_attention", "nm_kv8_attention_workspace_bytes",
+    "nm_kv8_select_workspace_bytes", "nm_kv8_attention", "nm_kv8_attention_workspace_bytes",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnmspmv.so")
@@ -131,7 +131,8 @@ def _load() -> ctypes.CDLL:
     L.nm_kv8_page_bytes.argtypes, L.nm_kv8_page_bytes.restype = [i32, i32, i32], i64
     L.nm_kv8_append.argtypes = [d, d, d, d, d, i32, d, p]
     L.nm_kv8_unpack.argtypes = [d, d, d, p]
-    L.nm_kv8_select.argtypes = [d, d, i32, i32, i32, i32, p, i64, p]
+    L.nm_kv8_select.argtypes = [d, d, i32, i32, i32, i32, p, i64, p, sz, p]
+    L.nm_kv8_select_workspace_bytes.argtypes, L.nm_kv8_select_workspace_bytes.restype = [i64, i64, i32, i64], sz
     L.nm_kv8_attention_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i64, i64, i32]
     L.nm_kv8_attention_workspace_bytes.restype = sz
     L.nm_kv8_attention.argtypes = [d, d, i32, i64, f32, i64, p, i64, i32, d, p, i64, p, sz, p]
@@ -873,22 +874,33 @@ def _kv8_selected(t: torch.Tensor, T: int, H: int, dev: int):
     return t.data_ptr(), stride[0] if T > 1 else H * shape[2], shape[2]
 
 
+def nm_kv8_select_workspace_bytes(T: int, S: int, n_kv: int, room: int) -> int:
+    """room: tokens that a row of the page table has room for (columns * page_size)."""
+    return int(lib.nm_kv8_select_workspace_bytes(T, S, n_kv, room))
+
+
+@functools.lru_cache(maxsize=4096)
+def _kv8_select_workspace(dev: int, *sizes) -> int:
+    return int(lib.nm_kv8_select_workspace_bytes(*sizes))
+
+
 def nm_kv8_select(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
                   q_start: torch.Tensor, n_kv: int, page_size: int, top: int, first: int = 1, last: int = 1,
-                  out: torch.Tensor | None = None) -> torch.Tensor:
+                  out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """For each row of q bf16 [T, heads, D] and key/value head the `top` blocks of 64 places whose bound on the heads' sum of
     scores is largest, the `first` and the `last` blocks of the row's keys in any case -> int32 [T, n_kv, top] in increasing
     order, -1 behind the last (rows behind the last sequence are left as they are)."""
     dev, shape = _where(q, "q"), q.shape
     qr = _kv_rows(q, "q", dev, shape)
     T, Hq, D = shape
-    b, _, _ = _kv_batch(dev, cache, page_table, kv_len, q_start, page_size, n_kv, T, D, _kv8_page)
+    b, S, room = _kv_batch(dev, cache, page_table, kv_len, q_start, page_size, n_kv, T, D, _kv8_page)
     if out is None:
         out = torch.empty((T, n_kv, top), dtype=torch.int32, device=q.device)
     elif out.dim() == 3 and out.shape[2] != top:
         raise ValueError(f"out must have room for {top} blocks (got {list(out.shape)})")
     ptr, ld, _ = _kv8_selected(out, T, n_kv, dev)
-    _call(dev, lib.nm_kv8_select, b, qr, Hq, top, first, last, ptr, ld)
+    ws, wp, wn = _kv_workspace(_kv8_select_workspace, dev, (T, S, n_kv, room), workspace)
+    _call(dev, lib.nm_kv8_select, b, qr, Hq, top, first, last, ptr, ld, wp, wn)
     return out
 
 

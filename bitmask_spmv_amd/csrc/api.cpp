@@ -1025,8 +1025,16 @@ nm_status nm_kv8_unpack(const nm_kv8_batch *batch, const nm_kv8_rows *k, const n
     }
 }
 
+size_t nm_kv8_select_workspace_bytes(int64_t T, int64_t S, int n_kv, int64_t room) {
+    if (T < 0 || T > (1 << 24) || S < 0 || S > (1 << 20) || n_kv < 1 || n_kv > 256 || room < 1 ||
+        room > (int64_t)nmk::kMaxSelectBlocks * 64)
+        return 0;
+    return nmk::kv8_select_workspace(T, S, n_kv, (room + 63) / 64);
+}
+
 nm_status nm_kv8_select(const nm_kv8_batch *batch, const nm_kv8_rows *q, int n_heads, int top, int first, int last,
-                        int32_t *selected, int64_t ld_selected, void *hip_stream) {
+                        int32_t *selected, int64_t ld_selected, void *workspace, size_t workspace_bytes,
+                        void *hip_stream) {
     try {
         g_err[0] = 0;
         const char *who = "nm_kv8_select";
@@ -1050,13 +1058,17 @@ nm_status nm_kv8_select(const nm_kv8_batch *batch, const nm_kv8_rows *q, int n_h
         if (!aligned(selected, 4)) return fail(NM_ERR_ALIGN, "%s: selected needs 4-byte alignment", who);
         if (ld_selected < (int64_t)a.b.f.n_kv * top)
             return fail(NM_ERR_SHAPE, "%s: ld_selected=%lld", who, (long long)ld_selected);
+        const size_t need = nmk::kv8_select_workspace(a.b.T, a.b.S, a.b.f.n_kv, blocks);
+        if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+            return fail(NM_ERR_WORKSPACE, "%s: 16-byte aligned workspace of %zu bytes required, %zu given", who, need,
+                        workspace ? workspace_bytes : (size_t)0);
         a.heads = n_heads;
         a.top = top;
         a.first = first;
         a.last = last;
         a.out = selected;
         a.ld_out = ld_selected;
-        hipError_t e = nmk::launch_kv8_select(a, (hipStream_t)hip_stream);
+        hipError_t e = nmk::launch_kv8_select(a, workspace, (hipStream_t)hip_stream);
         return e == hipSuccess ? NM_OK : hip_fail(who, e);
     } catch (...) {
         return fail(NM_ERR_HIP, "nm_kv8_select: internal error");

@@ -145,7 +145,8 @@ hipError_t launch_kv8_append(const Kv8Batch &b, const KvRows &k, const KvRows &v
 hipError_t launch_kv8_unpack(const Kv8Batch &b, const KvRows &k, const KvRows &v, hipStream_t st);
 size_t kv8_attention_workspace(int64_t T, int64_t S, int heads, int n_kv, int dim, int64_t room, int top);
 hipError_t launch_kv8_attention(const Kv8Attention &a, int64_t max_q, void *ws, hipStream_t st);
-hipError_t launch_kv8_select(const Kv8Select &a, hipStream_t st);
+size_t kv8_select_workspace(int64_t T, int64_t S, int n_kv, int64_t blocks);
+hipError_t launch_kv8_select(const Kv8Select &a, void *ws, hipStream_t st);
 
 hipError_t launch_kv4_append(const Kv4Batch &b, const Kv4Rows &k, const Kv4Rows &v, hipStream_t st);
 hipError_t launch_kv4_unpack(const Kv4Batch &b, const Kv4Rows &k, const Kv4Rows &v, hipStream_t st);

@@ -69,6 +69,17 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     return __builtin_amdgcn_readfirstlane((int)op((uint32_t)q[0], (uint32_t)q[1]));
 }
 
+__device__ __forceinline__ uint32_t wave_total(uint32_t v) {
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false);
+    const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = (uint32_t)p[0] + (uint32_t)p[1];
+    const auto q = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return __builtin_amdgcn_readfirstlane((int)((uint32_t)q[0] + (uint32_t)q[1]));
+}
+
 // A score as a whole number with the same order; 0 is none, kAsked a block that is taken in any case.  First scores
 // are the upper half of a key, the lower half is 1.
 constexpr uint64_t kAsked = ~0ull;
@@ -235,15 +246,14 @@ struct Exact {
     }
 };
 
-// One wave: first scores of n <= 64 R blocks in `key`, `off` how far they may be off.
+// One wave: first scores of n <= 64 R blocks, 64 r + lane a lane's, 0 behind the last, `off` how far they may be off.  `key`: room for n.
 template <int D, int R>
-__device__ __forceinline__ void choose_first(uint64_t *key, int n, int top, float off, const RowBlocks &rb, Doubts &few, int32_t *out, int lane) {
-    uint32_t k[R], most = 0, least = ~0u;
+__device__ __forceinline__ void choose_first(const uint32_t (&k)[R], uint64_t *key, int n, int top, float off, const RowBlocks &rb, Doubts &few,
+                                             int32_t *out, int lane) {
+    uint32_t most = 0, least = ~0u;
     int forced = 0, count = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int i = r * 64 + lane;
-        k[r] = i < n ? (uint32_t)(key[i] >> 32) : 0u;
         const bool asked = k[r] == ~0u, free = !asked && k[r] != 0;
         most = free ? max(most, k[r]) : most;
         least = free ? min(least, k[r]) : least;
@@ -263,7 +273,7 @@ __device__ __forceinline__ void choose_first(uint64_t *key, int n, int top, floa
         near = sure = ~0u;
     } else if (count > left) {
         // a key with as many at or above it as are left: between two with more and fewer, in turn by where it should lie
-        // if scores were spread evenly, and halfway
+        // if scores were spread evenly, and halfway (three tries at once took longer)
         uint32_t lo = ~wave_max(~least), hi = wave_max(most) + 1;
         int above_lo = count, above_hi = 0;
         for (bool half = false; above_lo != left && hi - lo > 1; half = !half) {
@@ -360,17 +370,25 @@ __device__ __forceinline__ void choose_first(uint64_t *key, int n, int top, floa
     for (int i = over + lane; i < top; i += 64) out[i] = -1;
 }
 
+template <int D, int R>
+__device__ __forceinline__ void choose_from(uint64_t *key, int n, int top, float off, const RowBlocks &rb, Doubts &few, int32_t *out, int lane) {
+    uint32_t k[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) k[r] = r * 64 + lane < n ? (uint32_t)(key[r * 64 + lane] >> 32) : 0u;
+    choose_first<D>(k, key, n, top, off, rb, few, out, lane);
+}
+
 template <int D>
 __device__ __forceinline__ void choose_up_to_1024(uint64_t *key, int n, int top, float off, bool none, const RowBlocks &rb, Doubts &few,
                                                   int32_t *out, int lane) {
     if (none)
         choose<kOneWave / 64>(key, n, top, out, lane);
     else if (n <= 256)
-        choose_first<D, 4>(key, n, top, off, rb, few, out, lane);
+        choose_from<D, 4>(key, n, top, off, rb, few, out, lane);
     else if (n <= 512)
-        choose_first<D, 8>(key, n, top, off, rb, few, out, lane);
+        choose_from<D, 8>(key, n, top, off, rb, few, out, lane);
     else
-        choose_first<D, kOneWave / 64>(key, n, top, off, rb, few, out, lane);
+        choose_from<D, kOneWave / 64>(key, n, top, off, rb, few, out, lane);
 }
 
 // ---- more blocks than one wave holds ----
@@ -380,7 +398,8 @@ struct Board {
     int count[kMaxWaves], forced[kMaxWaves];
     int bins[256];
     int bin, above, inside;  // what the scan of the bins found
-    int listed;
+    int listed, sum[8];
+    uint32_t least;
     uint64_t list[kFew];
     int at[kFew];
 };
@@ -546,54 +565,175 @@ __device__ __forceinline__ void choose_among_many(uint64_t *key, int n, int top,
     for (int i = over + min(on, left) + threadIdx.x; i < top; i += blockDim.x) out[i] = -1;
 }
 
-// First scores of more blocks than one wave holds: those that decide, and keys in 64 bits for the others.
+// The whole workgroup: first scores in `key`, `off` how far they may be off.  As choose_first, a key a thread and round; counts meet in LDS.
 template <int D>
-__device__ __forceinline__ void choose_many(uint64_t *key, int n, int top, float off, bool none, const RowBlocks &rb, int32_t *out, Board &sh) {
+__device__ __forceinline__ void choose_together(uint64_t *key, int n, int top, float off, bool none, const RowBlocks &rb, Doubts &few, int32_t *out,
+                                                Board &sh) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-    const Survey v(key, n, sh);
-    int left = top - v.forced;
-    if (!none && left > 0 && v.count > left) {
-        uint64_t last = v.any >> 32;  // the left-th largest
-        if (v.any != v.all) {
-            Digits g;
-            g.d = 63 - __clzll((long long)(v.any ^ v.all));
-            g.pre = g.d == 63 ? 0 : v.any >> (g.d + 1);
-            for (;;) {
-                g.lo = max(g.d - 7, 32);
-                count_digits(key, n, left, g, sh);
-                left -= sh.above;
-                g.pre = (g.d == 63 ? 0 : g.pre << (g.d - g.lo + 1)) | (uint64_t)sh.bin;
-                if (g.lo == 32) break;
-                g.d = g.lo - 1;
-                __syncthreads();  // bins and what the scan found are used again
-            }
-            last = g.pre;
+    const bool one = n <= (int)blockDim.x;  // a round
+    uint32_t most = 0, least = ~0u, own = 0;
+    int forced = 0, count = 0;
+    for (int i0 = 0; i0 < n; i0 += blockDim.x) {
+        own = i0 + threadIdx.x < n ? (uint32_t)(key[i0 + threadIdx.x] >> 32) : 0u;
+        const bool asked = own == ~0u, free = !asked && own != 0;
+        most = free ? max(most, own) : most;
+        least = free ? min(least, own) : least;
+        forced += __popcll(__ballot(asked));
+        count += __popcll(__ballot(free));
+    }
+    most = wave_max(most);
+    least = ~wave_max(~least);
+    if (lane == 0) {
+        sh.any[wave] = (uint64_t)most << 32 | least;
+        sh.all[wave] = (uint64_t)(uint32_t)forced << 32 | (uint32_t)count;
+    }
+    if (threadIdx.x < 8) sh.sum[threadIdx.x] = 0;
+    if (threadIdx.x == 0) sh.least = ~0u;
+    __syncthreads();
+    {
+        const uint64_t x = lane < waves ? sh.any[lane] : 0xFFFFFFFFull, y = lane < waves ? sh.all[lane] : 0ull;
+        most = wave_max((uint32_t)(x >> 32));
+        least = ~wave_max(~(uint32_t)x);
+        forced = (int)wave_total((uint32_t)(y >> 32));
+        count = (int)wave_total((uint32_t)y);
+    }
+    int turn = 0;
+    auto round = [&](auto &&f) {  // of all keys
+        if (one) {
+            f(own);
+        } else {
+            for (int i0 = 0; i0 < n; i0 += blockDim.x) f(i0 + threadIdx.x < n ? (uint32_t)(key[i0 + threadIdx.x] >> 32) : 0u);
         }
-        const float t = number((uint32_t)last);
-        const uint32_t sure = ordered(t + 2.f * off), near = ordered(t - 2.f * off);
-        const Exact<D> exact(rb, lane);
+    };
+    auto from_on = [&](uint32_t c) {  // free blocks of key c and above
+        int m = 0;
+        round([&](uint32_t k) { m += __popcll(__ballot(k >= c)); });
+        if (lane == 0) atomicAdd(&sh.sum[turn & 3], m);
+        if (threadIdx.x == 0) sh.sum[(turn + 2) & 3] = 0;  // the one after the next, which everyone has read
+        __syncthreads();
+        return sh.sum[turn++ & 3] - forced;
+    };
+    const int left = top - forced;
+    if (!none && left > 0 && count > left) {
+        uint32_t lo = least, hi = most + 1;
+        int above_lo = count, above_hi = 0;
+        for (bool half = false; above_lo != left && hi - lo > 1; half = !half) {
+            uint32_t c = lo + (hi - lo) / 2;
+            if (!half) {
+                const float a = number(lo), b = number(hi);
+                const float at = a + (b - a) * (((float)(above_lo - left) + 0.5f) * __builtin_amdgcn_rcpf((float)(above_lo - above_hi)));
+                c = min(max((uint32_t)__builtin_amdgcn_readfirstlane((int)ordered(at)), lo + 1), hi - 1);
+            }
+            const int m = __builtin_amdgcn_readfirstlane(from_on(c));
+            if (m >= left) {
+                lo = c;
+                above_lo = m;
+            } else {
+                hi = c;
+                above_hi = m;
+            }
+        }
+        if (above_lo == left) {  // the smallest of them: the left-th largest
+            uint32_t x = ~0u;
+            round([&](uint32_t k) { x = k >= lo ? min(x, k) : x; });
+            x = ~wave_max(~x);
+            if (lane == 0) atomicMin(&sh.least, x);
+            __syncthreads();
+            lo = sh.least;
+        }
+        const float t = number(lo);
+        const uint32_t near = ordered(t - 2.f * off), sure = ordered(t + 2.f * off);  // above `sure`: taken; below `near`: not
+        const int some = __builtin_amdgcn_readfirstlane(from_on(near)), sures = __builtin_amdgcn_readfirstlane(from_on(sure + 1));
+        const int doubts = some - sures;
+        const bool all = some == left, rank = !all && doubts <= kFew;
+        if (threadIdx.x == 0) sh.listed = 0;
+        __syncthreads();
         for (int i0 = wave * 64; i0 < n; i0 += waves * 64) {
             const int i = i0 + lane;
-            const uint32_t k = i < n ? (uint32_t)(key[i] >> 32) : 0u;
+            const uint32_t k = one ? own : i < n ? (uint32_t)(key[i] >> 32) : 0u;
             const bool doubt = k >= near && k <= sure && k != 0u && k != ~0u;
             if (i < n && !doubt) key[i] = k > sure ? kAsked : 0ull;
-            const uint64_t all = __ballot(doubt);
-            uint64_t m = all;
-            while (m) {  // kAtOnce of them
-                int mine = -1;
-#pragma unroll
-                for (int s = 0; s < Exact<D>::kAtOnce; ++s) {
-                    const int at = m ? __builtin_ctzll(m) : -1;
-                    if (s == exact.sub) mine = at;
-                    m &= m - 1;
+            if (doubt && all) key[i] = kAsked;
+            if (doubt && rank) few.at[atomicAdd(&sh.listed, 1)] = i;
+        }
+        if (rank) {  // each wave's share in 64 bits, ranked by one
+            __syncthreads();
+            const int own = wave * Exact<D>::kAtOnce;
+            if (own < doubts) {
+                const Exact<D> exact(rb, lane);
+                for (int i = own; i < doubts; i += waves * Exact<D>::kAtOnce) {
+                    const uint64_t x = exact.key(rb, few.at[min(i + exact.sub, doubts - 1)]);
+                    if (exact.part == 0 && i + exact.sub < doubts) few.key[i + exact.sub] = x;
                 }
-                const uint64_t x = exact.key(rb, i0 + (mine >= 0 ? mine : __builtin_ctzll(all)));
-                if (mine >= 0 && exact.part == 0) key[i0 + mine] = x;
             }
+            __syncthreads();
+            if (wave == 0) {
+                const uint64_t x = lane < doubts ? few.key[lane] : 0ull;
+                const int i = lane < doubts ? few.at[lane] : 0;
+                int ahead = 0;
+                for (int j = 0; j < doubts; ++j) {
+                    const uint64_t y = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(x >> 32), j) << 32 |
+                                       (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, j);
+                    ahead += y > x || (y == x && __builtin_amdgcn_readlane(i, j) < i);
+                }
+                if (lane < doubts) key[i] = ahead < left - sures ? kAsked : 0ull;
+            }
+        } else if (!all) {  // many, alike for instance: keys in 64 bits take their place
+            const Exact<D> exact(rb, lane);
+            for (int i0 = wave * 64; i0 < n; i0 += waves * 64) {
+                const uint64_t kept = i0 + lane < n ? key[i0 + lane] : 0ull;
+                const uint64_t every = __ballot(kept != 0 && kept != kAsked);
+                uint64_t m = every;
+                while (m) {  // kAtOnce of them
+                    int mine = -1;
+#pragma unroll
+                    for (int s = 0; s < Exact<D>::kAtOnce; ++s) {
+                        const int at = m ? __builtin_ctzll(m) : -1;
+                        if (s == exact.sub) mine = at;
+                        m &= m - 1;
+                    }
+                    const uint64_t x = exact.key(rb, i0 + (mine >= 0 ? mine : __builtin_ctzll(every)));
+                    if (mine >= 0 && exact.part == 0) key[i0 + mine] = x;
+                }
+            }
+            __syncthreads();
+            choose_among_many(key, n, top, out, sh);
+            return;
         }
         __syncthreads();
+    } else if (none) {
+        __syncthreads();  // what was found above is read
+        choose_among_many(key, n, top, out, sh);
+        return;
     }
-    choose_among_many(key, n, top, out, sh);
+    // out in the order of the blocks: what is asked for by now, or all there are
+    const bool every = count <= left;
+    int before = 0;
+    for (int i0 = 0; i0 < n; i0 += blockDim.x) {
+        const int i = i0 + threadIdx.x;
+        const uint64_t k = i < n ? key[i] : 0ull;
+        const bool is = k == kAsked || (every && k != 0);
+        const uint64_t m = __ballot(is);
+        if (i0) __syncthreads();  // counts are read before they are used again
+        if (lane == 0) sh.count[wave] = __popcll(m);
+        __syncthreads();
+        const int c = lane < waves ? sh.count[lane] : 0;
+        const int to = before + (int)wave_total(lane < wave ? (uint32_t)c : 0u) + __popcll(m & ((1ull << lane) - 1));
+        before += (int)wave_total((uint32_t)c);
+        if (is && to < top) out[to] = i;
+    }
+    for (int i = before + threadIdx.x; i < top; i += blockDim.x) out[i] = -1;
+}
+
+// Up to 1024 blocks one wave is faster than all of them (512 blocks, 8 rows and heads: 13.4 us a call against 17.6).
+template <int D, int CAP>
+__device__ __forceinline__ void choose_any(uint64_t *key, int n, int top, float off, bool none, const RowBlocks &rb, Doubts &few, int32_t *out) {
+    if (n <= kOneWave) {
+        if (threadIdx.x < kWave) choose_up_to_1024<D>(key, n, top, off, none, rb, few, out, (int)threadIdx.x);
+    } else if constexpr (CAP > kOneWave) {
+        __shared__ Board board;
+        choose_together<D>(key, n, top, off, none, rb, few, out, board);
+    }
 }
 
 // ---- first scores ----
@@ -630,8 +770,19 @@ __device__ __forceinline__ void split(double x, uint32_t (&piece)[3]) {
 __device__ __forceinline__ int to_one(uint32_t top) { return 1023 - (int)(top >> 20); }
 constexpr uint32_t kNotFinite = 0x7FF00000u;  // upper word of what is not
 
-template <int D, int CAP>
-__global__ __launch_bounds__(kMaxWaves *kWave) void kv8_select_kernel(Kv8Select a) {
+// What the first of two launches leaves for the second: a row's first scores, 0 for none and ~0 for a block that is taken in any
+// case, the largest scale byte of each of its parts and how large its query sums are (NaN: not finite).
+struct Left {
+    uint32_t *key;      // [items][parts * kPart]
+    uint32_t *largest;  // [items][parts]
+    float *size;        // [items]
+    int parts;
+};
+constexpr int kPart = 256;
+
+// SPLIT: a workgroup takes kPart of a row's blocks and leaves their scores.
+template <int D, int CAP, bool SPLIT>
+__global__ __launch_bounds__(SPLIT ? kPart : kMaxWaves *kWave) void kv8_select_kernel(Kv8Select a, Left to) {
     __shared__ uint64_t key[CAP];
     __shared__ uint16_t pieces[4][2 * D];  // the last of zeros: for the columns behind the third
     __shared__ uint32_t tops[kMaxWaves], scales[kMaxWaves];
@@ -643,7 +794,8 @@ __global__ __launch_bounds__(kMaxWaves *kWave) void kv8_select_kernel(Kv8Select 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int col = lane & 15, g = lane >> 4;
     const int n_kv = b.f.n_kv, group = a.heads / n_kv;
-    const int t = blockIdx.x / n_kv, head = blockIdx.x - t * n_kv;
+    const int item = SPLIT ? blockIdx.x / to.parts : blockIdx.x, part = SPLIT ? blockIdx.x - item * to.parts : 0;
+    const int t = item / n_kv, head = item - t * n_kv;
 
     // sums of the positive and of the negative parts of a channel's queries, a thread each
     const uint16_t *queries = a.q.p + (int64_t)t * a.q.ld + (int64_t)head * group * a.q.hd;
@@ -669,13 +821,14 @@ __global__ __launch_bounds__(kMaxWaves *kWave) void kv8_select_kernel(Kv8Select 
     const RowSeq seq(b, t, lane);
     if (t < seq.q0 || t >= seq.q1) return;
     const Ask ask(a, seq.len - seq.q1 + t);
-    const int per = b.f.blocks(), n = ask.n;
+    const int per = b.f.blocks(), n = SPLIT ? min(ask.n, (part + 1) * kPart) : ask.n, begin = part * (kPart / 16);  // blocks, tiles
+    if (SPLIT && part > 0 && n <= part * kPart) return;
     const RowBlocks rb = {queries, a.q.hd, group, head, per, b.table + (int64_t)seq.s * b.ld_table, &b, sums};
 
     // the first 64 blocks of a wave, 16 a tile: tile wave + waves * i is i's 16 lanes'
     auto block_of = [&](int tile0) { return (tile0 + g * waves) * 16 + col; };
     auto look = [&](int tile0) { return n > 0 ? rb.table[min(block_of(tile0), n - 1) / per] : -1; };
-    int page = look(wave);
+    int page = look(begin + wave);
     top = wave_max(top);
     if (lane == 0) tops[wave] = top;
     __syncthreads();
@@ -702,7 +855,7 @@ __global__ __launch_bounds__(kMaxWaves *kWave) void kv8_select_kernel(Kv8Select 
     for (int i = 0; i < D / 16; ++i) q[i].u = *reinterpret_cast<const u32x4 *>(&pieces[min(col, 3)][64 * (i >> 1) + 16 * g + 8 * (i & 1)]);
 
     uint32_t largest = 0;
-    for (int tile0 = wave; tile0 * 16 < n; tile0 += 4 * waves) {
+    for (int tile0 = begin + wave; tile0 * 16 < n; tile0 += 4 * waves) {
         const int own = block_of(tile0), k = min(own, n - 1);
         const bool ok = page >= 0 && page < b.num_pages;
         const int at = head * per + (k & (per - 1));
@@ -741,24 +894,57 @@ __global__ __launch_bounds__(kMaxWaves *kWave) void kv8_select_kernel(Kv8Select 
             score = g == i ? (col & 1 ? odd : even) : score;
         }
         if (own < n) {
-            key[own] = !ok ? 0ull : ask.asked(own) ? kAsked : none ? kAlike : (uint64_t)ordered(__builtin_ldexpf(score, scale - 127)) << 32 | 1;
+            const uint32_t first = ordered(__builtin_ldexpf(score, scale - 127));
+            if (SPLIT)
+                to.key[((int64_t)item * to.parts * kPart) + own] = !ok ? 0u : ask.asked(own) ? ~0u : first;
+            else
+                key[own] = !ok ? 0ull : ask.asked(own) ? kAsked : none ? kAlike : (uint64_t)first << 32 | 1;
             if (ok) largest = max(largest, (uint32_t)scale);
         }
     }
     largest = wave_max(largest);
     if (lane == 0) scales[wave] = largest;
     __syncthreads();
-    if (n <= kOneWave && wave != 0) return;
-    largest = 0;
-    for (int w = 0; w < waves; ++w) largest = max(largest, scales[w]);
-    const float off = slack(size, (int)largest);
-    int32_t *out = a.out + (int64_t)t * a.ld_out + (int64_t)head * a.top;
-    if (n <= kOneWave) {
-        choose_up_to_1024<D>(key, n, a.top, off, none, rb, few, out, lane);
-    } else if constexpr (CAP > kOneWave) {
-        __shared__ Board board;
-        choose_many<D>(key, n, a.top, off, none, rb, out, board);
+    largest = wave_max(lane < waves ? scales[lane] : 0u);
+    if constexpr (SPLIT) {
+        if (threadIdx.x == 0) {
+            to.largest[(int64_t)item * to.parts + part] = largest;
+            if (part == 0) to.size[item] = none ? NAN : size;
+        }
+    } else {
+        int32_t *out = a.out + (int64_t)t * a.ld_out + (int64_t)head * a.top;
+        choose_any<D, CAP>(key, n, a.top, slack(size, (int)largest), none, rb, few, out);
     }
+}
+
+// The second of two launches: a workgroup to each row and head.
+template <int D, int CAP>
+__global__ __launch_bounds__(kMaxWaves *kWave) void kv8_choose_kernel(Kv8Select a, Left from) {
+    __shared__ uint64_t key[CAP];
+    __shared__ Doubts few;
+    a.b.f.dim = D;
+    const Kv8Batch &b = a.b;
+    const int lane = threadIdx.x & 63;
+    const int n_kv = b.f.n_kv, group = a.heads / n_kv;
+    const int item = blockIdx.x, t = item / n_kv, head = item - t * n_kv;
+    const float size = from.size[item];
+    uint32_t largest = lane < from.parts ? from.largest[(int64_t)item * from.parts + lane] : 0u;  // at most 64 parts
+    const RowSeq seq(b, t, lane);
+    if (t < seq.q0 || t >= seq.q1) return;
+    const Ask ask(a, seq.len - seq.q1 + t);
+    const int n = ask.n;
+    const bool none = size != size;
+    if (lane * kPart >= n) largest = 0;
+    const float off = slack(size, (int)wave_max(largest));
+    const uint32_t *scores = from.key + (int64_t)item * from.parts * kPart;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const uint32_t x = scores[i];
+        key[i] = x == 0 ? 0ull : x == ~0u ? kAsked : none ? kAlike : (uint64_t)x << 32 | 1;
+    }
+    __syncthreads();
+    const RowBlocks rb = {a.q.p + (int64_t)t * a.q.ld + (int64_t)head * group * a.q.hd, a.q.hd, group, head, b.f.blocks(),
+                          b.table + (int64_t)seq.s * b.ld_table, &b, nullptr};
+    choose_any<D, CAP>(key, n, a.top, off, none, rb, few, a.out + (int64_t)t * a.ld_out + (int64_t)head * a.top);
 }
 
 // ---- sixteen rows of a sequence and a head ----
@@ -917,8 +1103,12 @@ __global__ __launch_bounds__(kTileWaves *kWave) void kv8_select_tile_kernel(Kv8S
     }
 }
 
+// Few rows behind long contexts: one compute unit reads bounds at about 30 GB/s, so their blocks go to many and the choice to a second launch.
+constexpr int kFewItems = 512, kSplitBlocks = 2048;
+bool split(int64_t items, int64_t room) { return items <= kFewItems && room > kSplitBlocks; }
+
 template <int D>
-hipError_t launch(const Kv8Select &a, hipStream_t st) {
+hipError_t launch(const Kv8Select &a, void *ws, hipStream_t st) {
     const int64_t room = (int64_t)a.b.cols * a.b.f.blocks();
     if (room <= kOneWave && (int64_t)a.b.T >= 4 * (int64_t)a.b.S) {
         const int64_t tiles = a.b.T / kTileRows + a.b.S;
@@ -932,20 +1122,37 @@ hipError_t launch(const Kv8Select &a, hipStream_t st) {
         return hipGetLastError();
     }
     const int64_t items = (int64_t)a.b.T * a.b.f.n_kv;
-    const dim3 block((items <= 512 ? kMaxWaves : 4) * kWave);  // more waves to a row where there are few of them
+    Left left = {};
+    if (split(items, room)) {
+        left.parts = (int)((room + kPart - 1) / kPart);
+        left.key = (uint32_t *)ws;
+        left.largest = left.key + items * left.parts * kPart;
+        left.size = (float *)(left.largest + items * left.parts);
+        kv8_select_kernel<D, 1, true><<<(unsigned)(items * left.parts), kPart, 0, st>>>(a, left);
+        kv8_choose_kernel<D, kMaxSelectBlocks><<<(unsigned)items, kMaxWaves * kWave, 0, st>>>(a, left);
+        return hipGetLastError();
+    }
+    // more waves to a row where there are few rows and blocks enough (48 rows and 8 heads of up to 128 blocks: 24.8 us with 16 waves, 9.7 with 4)
+    const dim3 block((items <= kFewItems && room > 256 ? kMaxWaves : 4) * kWave);
     if (room <= kOneWave)
-        kv8_select_kernel<D, kOneWave><<<(unsigned)items, block, 0, st>>>(a);
+        kv8_select_kernel<D, kOneWave, false><<<(unsigned)items, block, 0, st>>>(a, left);
     else if (room <= 4 * kOneWave)
-        kv8_select_kernel<D, 4 * kOneWave><<<(unsigned)items, block, 0, st>>>(a);
+        kv8_select_kernel<D, 4 * kOneWave, false><<<(unsigned)items, block, 0, st>>>(a, left);
     else
-        kv8_select_kernel<D, kMaxSelectBlocks><<<(unsigned)items, block, 0, st>>>(a);
+        kv8_select_kernel<D, kMaxSelectBlocks, false><<<(unsigned)items, block, 0, st>>>(a, left);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_kv8_select(const Kv8Select &a, hipStream_t st) {
-    return a.b.f.dim == 128 ? launch<128>(a, st) : launch<64>(a, st);
+size_t kv8_select_workspace(int64_t T, int64_t S, int n_kv, int64_t blocks) {
+    const int64_t items = T * n_kv, parts = (blocks + kPart - 1) / kPart;
+    if ((blocks <= kOneWave && T >= 4 * S) || !split(items, blocks)) return 0;
+    return (size_t)(items * (parts * kPart + parts + 1)) * sizeof(uint32_t);
+}
+
+hipError_t launch_kv8_select(const Kv8Select &a, void *ws, hipStream_t st) {
+    return a.b.f.dim == 128 ? launch<128>(a, ws, st) : launch<64>(a, ws, st);
 }
 
 }  // namespace nmk

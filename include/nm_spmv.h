@@ -522,7 +522,9 @@ nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int 
  *     score_b = sum_g sum_c max(q_gc most_bc, q_gc least_bc)
  * over the query heads g of the key/value head h, most and least the block's bounds, a bound on its keys' sum of scores; of equal ones
  * the lowest; `top` in all, in increasing order, -1 behind the last.  Scores are formed in fp64.  A row with an infinity or NaN among the
- * queries of h takes the lowest.  first + last <= top <= 2^14, table_cols * page_size <= 2^20, T * n_kv <= 2^21.
+ * queries of h takes the lowest.  first + last <= top <= 2^14, table_cols * page_size <= 2^20, T * n_kv <= 2^21.  Workspace:
+ * nm_kv8_select_workspace_bytes (room = table_cols * page_size), 16-byte aligned; many calls need none; calls that may overlap in time
+ * need workspaces of their own.
  */
 typedef nm_kv4_batch nm_kv8_batch;
 typedef nm_kv4_rows nm_kv8_rows;
@@ -536,8 +538,9 @@ nm_status nm_kv8_append(const nm_kv8_batch *batch, const nm_kv8_rows *k, const n
                         const nm_kv8_rotation *rotation, const nm_kv8_rows *q, int n_heads, const nm_kv8_rows *q_out,
                         void *hip_stream);
 nm_status nm_kv8_unpack(const nm_kv8_batch *batch, const nm_kv8_rows *k, const nm_kv8_rows *v, void *hip_stream);
+size_t nm_kv8_select_workspace_bytes(int64_t T, int64_t S, int n_kv, int64_t room);
 nm_status nm_kv8_select(const nm_kv8_batch *batch, const nm_kv8_rows *q, int n_heads, int top, int first, int last,
-                        int32_t *selected, int64_t ld_selected, void *hip_stream);
+                        int32_t *selected, int64_t ld_selected, void *workspace, size_t workspace_bytes, void *hip_stream);
 size_t nm_kv8_attention_workspace_bytes(int64_t T, int64_t S, int n_heads, int n_kv, int head_dim, int64_t max_q_len,
                                         int64_t room, int top);
 nm_status nm_kv8_attention(const nm_kv8_batch *batch, const nm_kv8_rows *q, int n_heads, int64_t max_q_len, float scale,

@@ -15,7 +15,7 @@ CALLS = {
                       ("stream", p, None)],
     "nm_kv8_unpack": [("batch", BATCH), rows("k"), rows("v"), ("stream", p, None)],
     "nm_kv8_select": [("batch", BATCH), rows("q"), ("n_heads", i32, 8), ("top", i32, 12), ("first", i32, 1), ("last", i32, 2),
-                      ("selected", p, A), ("ld_selected", i64, 24), ("stream", p, None)],
+                      ("selected", p, A), ("ld_selected", i64, 24), *WS],
     "nm_kv8_attention": [("batch", BATCH), rows("q"), ("n_heads", i32, 8), ("max_q_len", i64, 1), ("scale", f32, 0.1),
                          ("window", i64, 0), ("selected", p, A), ("ld_selected", i64, 24), ("top", i32, 12), rows("o"), ("lse", p, A),
                          ("ld_lse", i64, 8), *WS],
@@ -35,6 +35,7 @@ def L():
     lib.nm_kv8_page_bytes.argtypes, lib.nm_kv8_page_bytes.restype = [i32] * 3, i64
     lib.nm_kv8_attention_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i64, i64, i32]
     lib.nm_kv8_attention_workspace_bytes.restype = sz
+    lib.nm_kv8_select_workspace_bytes.argtypes, lib.nm_kv8_select_workspace_bytes.restype = [i64, i64, i32, i64], sz
     return lib
 
 
@@ -70,8 +71,12 @@ def test_null_pointers_and_odd_addresses(L, name):
     for arg, kind, _ in fields(name):
         if kind is not p or (arg in OPTIONAL and (name, arg) != ("nm_kv8_select", "selected")):
             continue
-        if arg == "workspace":
-            assert call(L, name, workspace=None) == WORKSPACE and call(L, name, workspace=HALF) == WORKSPACE
+        if arg == "workspace":  # asked of calls that need one
+            long = dict(table_cols=8000, ld_table=8000)
+            if name == "nm_kv8_attention":
+                long["selected"] = None
+            assert call(L, name, workspace=None, **long) == WORKSPACE and call(L, name, workspace=HALF, **long) == WORKSPACE
+            assert call(L, name, workspace_bytes=8, **long) == WORKSPACE
             continue
         assert call(L, name, **{arg: None}) == NULL, arg
         assert name.encode() in L.nm_last_error()
@@ -120,6 +125,12 @@ def test_nothing_to_do_is_not_an_error(L):
 
 
 def test_size_queries(L):
+    assert L.nm_kv8_select_workspace_bytes(16, 16, 8, 1 << 18) == 16 * 8 * (4096 + 16 + 1) * 4
+    assert L.nm_kv8_select_workspace_bytes(16, 16, 8, 65536) == 0  # short contexts
+    assert L.nm_kv8_select_workspace_bytes(512, 1, 8, 65536) == 0  # rows of a sequence go by sixteen
+    assert L.nm_kv8_select_workspace_bytes(2000, 2000, 8, 1 << 20) == 0  # rows enough for the machine
+    for bad in ((-1, 1, 8, 65536), (16, 16, 0, 65536), (16, 16, 8, 0), (16, 16, 8, (1 << 20) + 1)):
+        assert L.nm_kv8_select_workspace_bytes(*bad) == 0
     assert L.nm_kv8_page_bytes(64, 8, 128) == 133248  # 8 blocks of 16384 + 256 + 4, to a multiple of 128
     assert L.nm_kv8_page_bytes(512, 1, 64) == 66688
     for bad in ((0, 8, 128), (48, 8, 128), (64, 0, 128), (64, 8, 80), (64, 300, 128)):
