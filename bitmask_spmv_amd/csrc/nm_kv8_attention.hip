@@ -441,8 +441,7 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Attention a, const Par
 // Many rows of a sequence: a workgroup takes kPromptRows rows of one key/value head, 32 a wave, and walks the blocks of 64 tokens that
 // the last of them sees, in 32 x 32 tiles.  Values are converted once for the 128 rows: a thread has the 16 + 16 tokens of one
 // channel that one lane half of a score tile has, and leaves them in LDS in the operand order of the product (two buffers, one
-// barrier a block).  Keys, which would need as much LDS bandwidth again, go from the page to each wave, which converts
-// its own.  The walk is a pipeline over tiles of 32 tokens, one step of which has the products of three of them, so that
+// barrier a block).  Keys go the same way, a block further ahead.  The walk is a pipeline over tiles of 32 tokens, one step of which has the products of three of them, so that
 // matrix and vector instructions alternate within a wave: see `step`.
 constexpr int kPromptTile = 32;                       // rows of a wave
 constexpr int kPromptRows = kWaves * kPromptTile;     // rows of a workgroup
@@ -450,11 +449,14 @@ constexpr int kPromptRows = kWaves * kPromptTile;     // rows of a workgroup
 // Lane (col, hh) = (lane % 32, lane / 32): column col is a query row, token rows of the scores are
 // 8 (i / 4) + 4 hh + i % 4 of a tile of 32, channel rows of O 32 mt + 8 (i / 4) + 4 hh + i % 4.
 template <int D>
-using Values = u32x4[2][4][D / 32][kWave];
+struct Staged {  // two blocks' bf16 operands
+    u32x4 k[2][2][D / 16][kWave];  // of a tile of 32 tokens: channels 32 (i / 2) + 16 hh + 8 (i % 2) ..
+    u32x4 v[2][4][D / 32][kWave];
+};
 
 // Workgroup `block` of tiles * n_kv.
 template <int D>
-__device__ __forceinline__ void prompt(Kv8Attention &a, int tiles, Values<D> &values, int block) {
+__device__ __forceinline__ void prompt(Kv8Attention &a, int tiles, Staged<D> &staged, int block) {
     constexpr int MT = D / 32, KU = D / 32;  // channel tiles of the values, K units of a lane
     a.b.f.dim = D;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -520,15 +522,21 @@ __device__ __forceinline__ void prompt(Kv8Attention &a, int tiles, Values<D> &va
     int held = b_first;  // first of the blocks whose places are held
     lies.load(a.b, row, head, held + lane);
 
-    // keys: token 32 tt + col, units 2 i + hh
-    const uint32_t k_off = (hh * 64 + col) * 16;
-    u32x4 kx[2][KU];
-    float kscale[2];
-    auto load_keys = [&](int b, int tt) {
-        const uint8_t *kp = lies.at(b - held);
-        kscale[tt] = lies.k_scale(b - held);
+    // this thread's share of a block's keys: token `lane`, units kUnits wave ..
+    constexpr int kUnits = D / 64;
+    const uint32_t k_off = (wave * kUnits * 64 + lane) * 16;
+    u32x4 kx[kUnits];
+    float kscale = 1.f;
+    auto load_keys = [&](int b) {
+        const uint8_t *kp = lies.at(b - held) + k_off;
+        kscale = lies.k_scale(b - held);
 #pragma unroll
-        for (int i = 0; i < KU; ++i) kx[tt][i] = load_cache<false, u32x4>(kp + k_off + (tt * 512 + i * 2048));
+        for (int i = 0; i < kUnits; ++i) kx[i] = load_cache<false, u32x4>(kp + i * 1024);
+    };
+    auto put_keys = [&](int i, const Operand (&x)[2], int b) {  // unit 2 ku + half of the block
+        const int u = wave * kUnits + i;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) staged.k[b & 1][lane >> 5][(u >> 1) * 2 + e][(u & 1) * 32 + col] = x[e].u;
     };
 
     // this thread's share of a block's values: channel vc of the lane half vh, tokens 16 j + 4 vh + {0..3, 8..11} for kShare of
@@ -555,8 +563,7 @@ __device__ __forceinline__ void prompt(Kv8Attention &a, int tiles, Values<D> &va
             }
         }
     };
-    load_keys(b_first, 0);
-    load_keys(b_first, 1);
+    load_keys(b_first);
     load_values(b_first);
     // a weight of 0 times what an unseen place holds must be 0
     auto hide_values = [&](int b) {
@@ -576,13 +583,14 @@ __device__ __forceinline__ void prompt(Kv8Attention &a, int tiles, Values<D> &va
         for (int k = 0; k < 4; ++k) x.w[k] = fp8_pair(vx[k >> 1][j], vscale, k & 1);
         return x;
     };
-    auto put_values = [&](int j, const Operand &x, u32x4 (*to)[MT][kWave]) { to[vj + j][vc >> 5][vh * 32 + (vc & 31)] = x.u; };
+    auto put_values = [&](int j, const Operand &x, int b) { staged.v[b & 1][vj + j][vc >> 5][vh * 32 + (vc & 31)] = x.u; };
 
     // Products of the scores: number i of a 32-token tile's 2 KU.
-    auto dot = [&](int tt, int i, f32x16 &acc) {
+    auto dot = [&](int i, const u32x4 &w, f32x16 &acc) {
         const f32x16 zero = {};
-        const u32x4 &w = kx[tt][i >> 1];
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(eight(w[2 * (i & 1)], w[2 * (i & 1) + 1], kscale[tt]).h, q[i].h, i ? acc : zero, 0, 0, 0);
+        Operand x;
+        x.u = w;
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x.h, q[i].h, i ? acc : zero, 0, 0, 0);
     };
     constexpr int kDots = 2 * KU, kSums = 2 * MT;  // matrix products of a 32-token tile: scores, values
     auto sum = [&](int i, const u32x4 &v, const uint32_t (&w)[8]) {
@@ -648,37 +656,42 @@ __device__ __forceinline__ void prompt(Kv8Attention &a, int tiles, Values<D> &va
     };
 
     // Tile t = 2 b + tt: between them, product by product, the values of tile t (weights w are ready), the scores
-    // of tile t + 2 (into n), the softmax of tile t + 1 (scores sc to weights wn) and half of the conversion of
-    // block b + 1.
+    // of tile t + 2 (into n), the softmax of tile t + 1 (scores sc to weights wn) and half of the conversions: of
+    // block b + 1's values and block b + 2's keys.
     auto step = [&](int b, int tt, uint32_t (&w)[8], uint32_t (&wn)[8], f32x16 &sc, f32x16 &n) {
-        const u32x4 *from_lds = &values[b & 1][2 * tt][0][lane];
+        const u32x4 *values = &staged.v[b & 1][2 * tt][0][lane], *keys = &staged.k[(b + 1) & 1][tt][0][lane];
         hide(tt ? b + 1 : b, tt ^ 1, sc);
         raise(largest(sc), w);
         relative(sc);
         const float mc = less;
         if (tt == 0) hide_values(b + 1);
 
-        constexpr int kRead = 3;  // value operands read ahead
-        u32x4 v[kRead];
+        constexpr int kRead = 3;  // operands read ahead
+        u32x4 v[kRead], kk[kRead];
 #pragma unroll
-        for (int i = 0; i < kRead - 1; ++i) v[i] = from_lds[i * kWave];
-        constexpr int kMine = kShare / 2;  // operands converted in a step
-        Operand cv[kMine];
+        for (int i = 0; i < kRead - 1; ++i) {
+            v[i] = values[i * kWave];
+            kk[i] = keys[i * kWave];
+        }
+        constexpr int kMine = kShare / 2;  // operands of values converted in a step
+        Operand cv[kMine], ck[2];
         float part = 0.f;
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            if (k + kRead - 1 < kSums) v[(k + kRead - 1) % kRead] = from_lds[(k + kRead - 1) * kWave];
+            if (k + kRead - 1 < kSums) v[(k + kRead - 1) % kRead] = values[(k + kRead - 1) * kWave];
+            if (k + kRead - 1 < kDots) kk[(k + kRead - 1) % kRead] = keys[(k + kRead - 1) * kWave];
             if (k < kSums) sum(k, v[k % kRead], w);
-            if (k < kDots) dot(tt, k, n);
+            if (k < kDots) dot(k, kk[k % kRead], n);
             const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[2 * k], c, -mc));
             const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[2 * k + 1], c, -mc));
             wn[k] = pack_bf16(e0, e1);
             part += e0 + e1;
             if (k < 4 * kMine) cv[k / 4].w[k % 4] = fp8_pair(vx[k % 4 / 2][kMine * tt + k / 4], vscale, k & 1);
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            if (tt < kUnits) ck[k / 4].w[k % 4] = fp8_pair(kx[tt < kUnits ? tt : 0][k / 2], kscale, k & 1);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, 7, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
             __builtin_amdgcn_sched_group_barrier(0x002, 9, 0);
             __builtin_amdgcn_sched_barrier(0);
@@ -689,25 +702,36 @@ __device__ __forceinline__ void prompt(Kv8Attention &a, int tiles, Values<D> &va
         for (int k = 0; k < 8; ++k) asm volatile("" : "+v"(wn[k]));
         l += part;
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) put_values(kMine * tt + j, cv[j], values[(b + 1) & 1]);
+        for (int j = 0; j < kMine; ++j) put_values(kMine * tt + j, cv[j], b + 1);
+        if (tt < kUnits) put_keys(tt, ck, b + 2);
         if (tt == 1) load_values(b + 2);
-        load_keys(b + 2, tt);
+        if (tt == 1) load_keys(b + 3);
     };
 
     if (b_first < b_end) {
-        // fill the pipeline: values of the first block, scores of its two tiles, weights of the first
+        // fill the pipeline: values of the first block, keys of the first two, scores of the first's two tiles, weights of one
         uint32_t wa[8], wb[8];
         f32x16 sa, sb;
+        auto convert_keys = [&](int b) {
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+                const Operand x[2] = {eight(kx[i][0], kx[i][1], kscale), eight(kx[i][2], kx[i][3], kscale)};
+                put_keys(i, x, b);
+            }
+        };
         hide_values(b_first);
 #pragma unroll
-        for (int j = 0; j < kShare; ++j) put_values(j, operand(j), values[b_first & 1]);
+        for (int j = 0; j < kShare; ++j) put_values(j, operand(j), b_first);
         load_values(b_first + 1);
+        convert_keys(b_first);
+        load_keys(b_first + 1);
+        convert_keys(b_first + 1);
+        load_keys(b_first + 2);
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kDots; ++i) dot(0, i, sa);
+        for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-        for (int i = 0; i < kDots; ++i) dot(1, i, sb);
-        load_keys(b_first + 1, 0);
-        load_keys(b_first + 1, 1);
+            for (int i = 0; i < kDots; ++i) dot(i, staged.k[b_first & 1][tt][i][lane], tt ? sb : sa);
         hide(b_first, 0, sa);
         {
 #pragma unroll
@@ -758,12 +782,12 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv8_mixed_kernel(Kv8Attentio
                                                                      int groups, int tiles) {
     __shared__ union {
         Shared<D> sh;
-        Values<D> values;
+        Staged<D> staged;
     } lds;
     if ((int)blockIdx.x < groups)
         decode<D, false>(a, parts, tags, lds.sh, blockIdx.x, groups);
     else
-        prompt<D>(a, tiles, lds.values, (int)blockIdx.x - groups);
+        prompt<D>(a, tiles, lds.staged, (int)blockIdx.x - groups);
 }
 
 // Few and short: a workgroup to each row tile (sequence s has none but its own of
