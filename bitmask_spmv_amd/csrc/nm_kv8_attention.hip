@@ -362,12 +362,6 @@ __global__ __launch_bounds__(kWaves *kWave, 2) void kv8_decode_kernel(Kv8Attenti
 // workgroup's, each wave takes a quarter of the blocks that the row has.  kWave1: a wave's.  kRuns: units are cut into runs.
 // With kWave1 workgroups that go to one XCD take neighbouring items, tokens of few heads, whose blocks its L2 holds.
 enum : int { kItem = 0, kWave1 = 1, kRuns = 2 };
-constexpr int kXcds = 8;
-
-__device__ __forceinline__ int by_xcd(int block, int blocks) {
-    const int per = blocks / kXcds, rest = blocks % kXcds, xcd = block % kXcds;
-    return xcd * per + min(xcd, rest) + block / kXcds;
-}
 
 template <int D, int MODE>
 __global__ __launch_bounds__(kWaves *kWave, 2) void kv8_selected_kernel(Kv8Attention a, Part<D> *parts, PartTag *tags) {

@@ -794,7 +794,8 @@ __global__ __launch_bounds__(SPLIT ? kPart : kMaxWaves *kWave) void kv8_select_k
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int col = lane & 15, g = lane >> 4;
     const int n_kv = b.f.n_kv, group = a.heads / n_kv;
-    const int item = SPLIT ? blockIdx.x / to.parts : blockIdx.x, part = SPLIT ? blockIdx.x - item * to.parts : 0;
+    // the heads of a row to one XCD: their bounds lie side by side, and their scales in one cache line
+    const int item = SPLIT ? blockIdx.x / to.parts : by_xcd(blockIdx.x, gridDim.x), part = SPLIT ? blockIdx.x - item * to.parts : 0;
     const int t = item / n_kv, head = item - t * n_kv;
 
     // sums of the positive and of the negative parts of a channel's queries, a thread each

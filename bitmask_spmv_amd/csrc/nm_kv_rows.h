@@ -41,6 +41,13 @@ __device__ __forceinline__ int seq_of_row(const int32_t *q_start, int S, int s, 
     return s;
 }
 
+// Workgroups go to the XCDs in turn: a number for each by which those of an XCD, which share its L2, are neighbours.
+constexpr int kXcds = 8;
+__device__ __forceinline__ int by_xcd(int block, int blocks) {
+    const int per = blocks / kXcds, rest = blocks % kXcds, xcd = block % kXcds;
+    return xcd * per + min(xcd, rest) + block / kXcds;
+}
+
 // Row t's sequence, called by a whole wave with one t: up to 64 sequences are read at once, with what is wanted of them.
 struct RowSeq {
     int s, q0, q1, len;

@@ -379,6 +379,26 @@ def test_scores_and_values_at_the_ends_of_the_range(rows):
         held_to(out[t : t + 1, ~bad], lse[t : t + 1, ~bad], {k: v[:, ~bad] for k, v in r.items()}, f"row {t}")
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_key_that_is_no_number_in_a_prompt(D):
+    """Rows before it, in the same tiles, are what they are without it."""
+    say("NaN in a prompt", D)
+    g = np.random.default_rng(D)
+    H, Hq, ps, rows = 2, 64, 64, 1100
+    table, kv_len, q_start, N = batch(g, [rows], [rows], ps)
+    cache = filled_cache(g, N, ps, H, D)
+    q = bf16(g.standard_normal((rows, Hq, D)))
+    out, lse = run_attention(q, cache, table, kv_len, q_start, H, ps, rows)
+    at = 517
+    v = sections(cache, ps, H, D)[0]
+    v[table[0, at // 64], 0, 0, kv8.places(D)[0][at % 64, 7]] = 255
+    out2, lse2 = run_attention(q, cache, table, kv_len, q_start, H, ps, rows)
+    first = np.arange(Hq) < Hq // H
+    assert np.isnan(out2[at:, first]).all() and np.isnan(lse2[at:, first]).all()
+    for a, b in ((out, out2), (lse, lse2)):
+        assert (a[:at] == b[:at]).all() and (a[:, ~first] == b[:, ~first]).all()
+
+
 def test_strided_rows_of_one_projection():
     """q, k and v as slices of one [T, (Hq + 2 H) D] tensor; out and lse with strides of their own."""
     say("strides")
