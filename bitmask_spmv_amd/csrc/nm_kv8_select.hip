@@ -26,6 +26,7 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kMaxWaves = 16;
 constexpr int kFew = 64;          // candidates that one wave ranks
@@ -96,8 +97,10 @@ constexpr uint64_t kAlike = 1ull << 63;  // every score of a row with queries th
 
 // How far a first score may be off.  The sum of the magnitudes of its products is at most 448 times `size`, the sum of the magnitudes of the query
 // sums; each of eight instructions is taken to cut its sum four times by a unit in the last place (2^-23): 2^-18 in all (2^-20.9 is the
-// most that 80 million random sums were off); and whatever is below 2^-126.
-__device__ __forceinline__ float slack(float size, int scale) { return __builtin_ldexpf(__builtin_fmaf(size, 448.f * 0x1p-18f, 0x1p-100f), scale - 127); }
+// most that 80 million random sums were off); query sums of `group` heads may be off by group 2^-24; and whatever is below 2^-126.
+__device__ __forceinline__ float slack(float size, int group, int scale) {
+    return __builtin_ldexpf(__builtin_fmaf(size, 448.f * __builtin_fmaf((float)group, 0x1p-24f, 0x1p-18f), 0x1p-100f), scale - 127);
+}
 
 __device__ __forceinline__ float channel(const u32x4 &w, int i) { return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); }
 
@@ -272,15 +275,17 @@ __device__ __forceinline__ void choose_first(const uint32_t (&k)[R], uint64_t *k
     if (left <= 0) {
         near = sure = ~0u;
     } else if (count > left) {
-        // a key with as many at or above it as are left: between two with more and fewer, in turn by where it should lie
-        // if scores were spread evenly, and halfway (three tries at once took longer)
+        // a key with as many at or above it as are left: between two with more and fewer, where it should lie if the logarithm of the
+        // number above fell evenly, as it does at the upper end of most distributions; each fourth time halfway
         uint32_t lo = ~wave_max(~least), hi = wave_max(most) + 1;
         int above_lo = count, above_hi = 0;
-        for (bool half = false; above_lo != left && hi - lo > 1; half = !half) {
+        const float want = __builtin_amdgcn_logf((float)left + 0.25f);
+        for (int turns = 1; above_lo != left && hi - lo > 1; ++turns) {
             uint32_t c = lo + (hi - lo) / 2;
-            if (!half) {
+            if (turns & 3) {
                 const float a = number(lo), b = number(hi);
-                const float at = a + (b - a) * (((float)(above_lo - left) + 0.5f) * __builtin_amdgcn_rcpf((float)(above_lo - above_hi)));
+                const float la = __builtin_amdgcn_logf((float)above_lo + 0.5f), lb = __builtin_amdgcn_logf((float)above_hi + 0.5f);
+                const float at = a + (b - a) * ((la - want) * __builtin_amdgcn_rcpf(la - lb));
                 c = min(max((uint32_t)__builtin_amdgcn_readfirstlane((int)ordered(at)), lo + 1), hi - 1);
             }
             const int m = from_on(c);
@@ -617,11 +622,13 @@ __device__ __forceinline__ void choose_together(uint64_t *key, int n, int top, f
     if (!none && left > 0 && count > left) {
         uint32_t lo = least, hi = most + 1;
         int above_lo = count, above_hi = 0;
-        for (bool half = false; above_lo != left && hi - lo > 1; half = !half) {
+        const float want = __builtin_amdgcn_logf((float)left + 0.25f);
+        for (int turns = 1; above_lo != left && hi - lo > 1; ++turns) {
             uint32_t c = lo + (hi - lo) / 2;
-            if (!half) {
+            if (turns & 3) {
                 const float a = number(lo), b = number(hi);
-                const float at = a + (b - a) * (((float)(above_lo - left) + 0.5f) * __builtin_amdgcn_rcpf((float)(above_lo - above_hi)));
+                const float la = __builtin_amdgcn_logf((float)above_lo + 0.5f), lb = __builtin_amdgcn_logf((float)above_hi + 0.5f);
+                const float at = a + (b - a) * ((la - want) * __builtin_amdgcn_rcpf(la - lb));
                 c = min(max((uint32_t)__builtin_amdgcn_readfirstlane((int)ordered(at)), lo + 1), hi - 1);
             }
             const int m = __builtin_amdgcn_readfirstlane(from_on(c));
@@ -914,7 +921,7 @@ __global__ __launch_bounds__(SPLIT ? kPart : kMaxWaves *kWave) void kv8_select_k
         }
     } else {
         int32_t *out = a.out + (int64_t)t * a.ld_out + (int64_t)head * a.top;
-        choose_any<D, CAP>(key, n, a.top, slack(size, (int)largest), none, rb, few, out);
+        choose_any<D, CAP>(key, n, a.top, slack(size, group, (int)largest), none, rb, few, out);
     }
 }
 
@@ -936,7 +943,7 @@ __global__ __launch_bounds__(kMaxWaves *kWave) void kv8_choose_kernel(Kv8Select 
     const int n = ask.n;
     const bool none = size != size;
     if (lane * kPart >= n) largest = 0;
-    const float off = slack(size, (int)wave_max(largest));
+    const float off = slack(size, group, (int)wave_max(largest));
     const uint32_t *scores = from.key + (int64_t)item * from.parts * kPart;
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
         const uint32_t x = scores[i];
@@ -950,7 +957,7 @@ __global__ __launch_bounds__(kMaxWaves *kWave) void kv8_choose_kernel(Kv8Select 
 
 // ---- sixteen rows of a sequence and a head ----
 
-constexpr int kTileWaves = 8;
+constexpr int kTileWaves = 8;  // two rows' choices a wave (with 16 waves registers spill: 512 rows behind 16K tokens 29 us, not 25)
 
 // What the rows of a tile keep in LDS before their keys.
 template <int D>
@@ -990,62 +997,71 @@ __global__ __launch_bounds__(kTileWaves *kWave) void kv8_select_tile_kernel(Kv8S
     const int per = b.f.blocks();
     RowBlocks rb = {a.q.p + (int64_t)t0 * a.q.ld + (int64_t)head * group * a.q.hd, a.q.hd, group, head, per, b.table + (int64_t)s * b.ld_table, &b, nullptr};
 
-    // sums of queries: 16 threads (or 8) a row, 8 channels each, positive parts and negative ones
+    // Sums of queries, 16 threads (or 8) a row, 8 channels each, positive parts and negative ones: in fp32, of the power of two of the
+    // row's largest query, which costs first scores group 2^-24 more (in 64 bits this took 3.9 us of a tile's 17).
     const int row = threadIdx.x >> 4, c8 = threadIdx.x & 15;
     if (row < kTileRows) {  // whole waves
-        double sum[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum[i] = 0.0;
-        uint32_t top = 0;
-        if (c8 < D / 8 && row < rows) {
-            const uint16_t *p = rb.q + (int64_t)row * a.q.ld + c8 * 8;
+        const bool mine = c8 < D / 8 && row < rows;
+        const uint16_t *p = rb.q + (int64_t)min(row, rows - 1) * a.q.ld + min(c8, D / 8 - 1) * 8;
+        auto heads = [&](auto &&f) {  // four loads at once
             for (int h0 = 0; h0 < group; h0 += 4) {
                 u32x4 w[4];
 #pragma unroll
                 for (int h = 0; h < 4; ++h) w[h] = *reinterpret_cast<const u32x4 *>(p + (int64_t)min(h0 + h, group - 1) * a.q.hd);
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    if (h0 + h >= group) break;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float x = i & 1 ? bf16_hi(w[h][i >> 1]) : bf16_lo(w[h][i >> 1]);
-                        if ((__float_as_uint(x) & 0x7F800000u) == 0x7F800000u) top = kNotFinite;
-                        sum[i] += (double)fmaxf(x, 0.f);
-                        sum[8 + i] += (double)fminf(x, 0.f);
-                    }
-                }
+                for (int h = 0; h < 4; ++h)
+                    if (h0 + h < group) f(w[h]);
             }
-        }
+        };
+        u16x2 most = {0, 0};
+        heads([&](const u32x4 &w) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = max(top, (uint32_t)__double2hiint(sum[i]) & 0x7FFFFFFFu);
+            for (int i = 0; i < 4; ++i) {
+                union { uint32_t u; u16x2 h; } x;
+                x.u = w[i] & 0x7FFF7FFFu;
+                most = __builtin_elementwise_max(most, x.h);
+            }
+        });
+        uint32_t top = mine ? max(most[0], most[1]) : 0;
 #define NM_KV8_ROW_MAX(C) top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, C, 0xF, 0xF, false))
         NM_KV8_ROW_MAX(0xB1);
         NM_KV8_ROW_MAX(0x4E);
         NM_KV8_ROW_MAX(0x141);
         NM_KV8_ROW_MAX(0x140);
 #undef NM_KV8_ROW_MAX
-        const bool none = top >= kNotFinite;
-        float size = 0.f;
-        uint32_t word[3][2][4];
+        const bool none = top >= 0x7F80u;
+        const int down = none || !mine ? -1000 : 127 - (int)(top >> 7);  // zeros for what is not finite or not there
+        float sum[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const double x = none ? 0.0 : __builtin_ldexp(sum[i], to_one(top));
-            uint32_t piece[3];
-            split(x, piece);
-            size += (float)(x < 0.0 ? -x : x);
+        for (int i = 0; i < 16; ++i) sum[i] = 0.f;
+        heads([&](const u32x4 &w) {
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                uint32_t &to = word[k][i >> 3][i >> 1 & 3];
-                to = i & 1 ? to | piece[k] << 16 : piece[k];
+            for (int i = 0; i < 8; ++i) {
+                const float x = none ? 0.f : __builtin_ldexpf(channel(w, i), down);
+                sum[i] += fmaxf(x, 0.f);
+                sum[8 + i] += fminf(x, 0.f);
             }
-        }
+        });
+        float size = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) size += fabsf(sum[i]);
         size = dpp_add<0x140>(dpp_add<0x141>(dpp_add<0x4E>(dpp_add<0xB1>(size))));
-        if (c8 < D / 8)
 #pragma unroll
-            for (int k = 0; k < 3; ++k)
+        for (int k = 0; k < 3; ++k)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    *reinterpret_cast<u32x4 *>(&sh.pieces[k][row][i * D + c8 * 8]) = (u32x4){word[k][i][0], word[k][i][1], word[k][i][2], word[k][i][3]};
+            for (int i = 0; i < 2; ++i) {
+                u32x4 w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float &lo = sum[8 * i + 2 * e], &hi = sum[8 * i + 2 * e + 1];
+                    union { bf16x2 h; uint32_t u; } x;
+                    x.h = __builtin_convertvector((f32x2){lo, hi}, bf16x2);
+                    w[e] = x.u;
+                    lo -= bf16_lo(x.u);
+                    hi -= bf16_hi(x.u);
+                }
+                if (c8 < D / 8) *reinterpret_cast<u32x4 *>(&sh.pieces[k][row][i * D + c8 * 8]) = w;
+            }
         if (c8 == 0) {
             sh.size[row] = size;
             sh.none[row] = none;
@@ -1093,13 +1109,11 @@ __global__ __launch_bounds__(kTileWaves *kWave) void kv8_select_tile_kernel(Kv8S
     largest = wave_max(largest);
     if (lane == 0) sh.scales[wave] = largest;
     __syncthreads();
-    largest = 0;
-#pragma unroll
-    for (int w = 0; w < kTileWaves; ++w) largest = max(largest, sh.scales[w]);
+    largest = wave_max(lane < kTileWaves ? sh.scales[lane] : 0u);
     for (int r = wave; r < rows; r += kTileWaves) {
         const Ask ask(a, place0 + r);
         rb.q = a.q.p + (int64_t)(t0 + r) * a.q.ld + (int64_t)head * group * a.q.hd;
-        choose_up_to_1024<D>(keys + r * room, ask.n, a.top, slack(sh.size[r], (int)largest), sh.none[r], rb, sh.few[wave],
+        choose_up_to_1024<D>(keys + r * room, ask.n, a.top, slack(sh.size[r], group, (int)largest), sh.none[r], rb, sh.few[wave],
                              a.out + (int64_t)(t0 + r) * a.ld_out + (int64_t)head * a.top, lane);
     }
 }

@@ -56,6 +56,14 @@ def test_long_rows_and_many_rows():
     select_case(3, [400, 300], [900, 1800], 4, 1, 64, 256, 6, 1, 1)  # more rows than workgroups of sixteen waves are for
 
 
+def test_sixteen_rows_a_workgroup_at_the_largest_table():
+    """A table of 1024 blocks, as many as such rows' scores have room for."""
+    say("1024 blocks")
+    for D in (64, 128):
+        select_case(4, [21], [65000], 2, 1, D, 512, 30, 1, 1)
+        select_case(5, [9, 7, 3], [40000, 500, 64], 2, 1, D, 512, 300, 2, 2)
+
+
 def test_scores_that_are_alike():
     """Blocks with the same bytes, in groups larger and smaller than what one wave ranks: the lowest of them."""
     say("alike")
