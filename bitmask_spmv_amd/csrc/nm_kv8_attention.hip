@@ -670,6 +670,7 @@ __device__ __forceinline__ void prompt(Kv8Attention &a, int tiles, Staged<D> &st
         constexpr int kMine = kShare / 2;  // operands of values converted in a step
         Operand cv[kMine], ck[2];
         float part = 0.f;
+        __builtin_amdgcn_s_setprio(1);  // ahead of the wave that loads or rescales (499 -> 495 us)
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -690,6 +691,7 @@ __device__ __forceinline__ void prompt(Kv8Attention &a, int tiles, Staged<D> &st
             __builtin_amdgcn_sched_group_barrier(0x002, 9, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
+        __builtin_amdgcn_s_setprio(0);
         // this step's work: not to be put off to where it is used
         asm volatile("" : "+v"(n));
 #pragma unroll
