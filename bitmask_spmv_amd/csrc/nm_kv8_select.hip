@@ -304,8 +304,8 @@ __device__ __forceinline__ void choose_first(const uint32_t (&k)[R], uint64_t *k
             lo = ~wave_max(~least);
         }
         const float t = number(lo);
-        near = ordered(t - 2.f * off);
-        sure = ordered(t + 2.f * off);
+        near = max(ordered(t - 2.f * off), 1u);  // in pages that were never written scores may be NaN: blocks without one stay out
+        sure = min(ordered(t + 2.f * off), ~1u);
         const int some = from_on(near), sures = from_on(sure + 1), doubts = some - sures;
         if (some > left && doubts <= kFew) {  // one wave ranks them by scores in 64 bits
             int at = 0;
@@ -649,7 +649,7 @@ __device__ __forceinline__ void choose_together(uint64_t *key, int n, int top, f
             lo = sh.least;
         }
         const float t = number(lo);
-        const uint32_t near = ordered(t - 2.f * off), sure = ordered(t + 2.f * off);  // above `sure`: taken; below `near`: not
+        const uint32_t near = max(ordered(t - 2.f * off), 1u), sure = min(ordered(t + 2.f * off), ~1u);  // above `sure`: taken; below `near`: not
         const int some = __builtin_amdgcn_readfirstlane(from_on(near)), sures = __builtin_amdgcn_readfirstlane(from_on(sure + 1));
         const int doubts = some - sures;
         const bool all = some == left, rank = !all && doubts <= kFew;

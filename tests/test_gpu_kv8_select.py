@@ -187,3 +187,30 @@ def test_choice_and_attention_together(seqs):
     assert (sel == kv8.select(q, cache, table, kv_len, q_start, ps, H, top, 1, 2)).all()
     r = kv8.attention(q, cache, table, kv_len, q_start, ps, H, D**-0.5, 0, sel)
     held_to(*run_attention(q, cache, table, kv_len, q_start, H, ps, 1, selected=sel), r, f"{seqs} sequences")
+
+
+@pytest.mark.parametrize("rows,lens", [([1, 1], [900, 40000]), ([21], [30000]), ([1], [200000]), ([600], [140000])])
+def test_pages_that_were_never_written(rows, lens):
+    """Any bytes as bounds and scales, NaN among them: blocks that the row has, each once, none without a page."""
+    say("never written", rows, lens)
+    g = np.random.default_rng(77)
+    ps, H, D, Hq = 512, 1, 64, 2
+    table, kv_len, q_start, N = batch(g, rows, lens, ps)
+    cache = g.integers(0, 256, size=(N, kv8.page_bytes(ps, H, D)), dtype=np.uint8)
+    b, s = sections(cache, ps, H, D)[1:]
+    b[::3] = 127
+    s[1::4] = 255
+    bad = g.random(table.shape) < 0.2
+    table[bad] = np.where(g.random(table.shape) < 0.5, -1, N)[bad]
+    q = bf16(g.standard_normal((int(q_start[-1]), Hq, D)))
+    for top in (2, 7, 90):
+        got = run_select(q, cache, table, kv_len, q_start, H, ps, top, 1, 1)
+        for i, n in enumerate(rows):
+            for t in range(q_start[i], q_start[i + 1]):
+                own = (kv_len[i] - q_start[i + 1] + t) // 64
+                x = got[t, 0]
+                x = x[x != -1]
+                assert (got[t, 0, : len(x)] == x).all() and (np.diff(x) > 0).all()
+                assert (x >= 0).all() and (x <= own).all()
+                pages = table[i, x * 64 // ps]
+                assert ((pages >= 0) & (pages < N)).all()
