@@ -321,16 +321,14 @@ __device__ __forceinline__ void join_groups(const A &a, const Part<D> *parts, co
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, m[i]);
         const float keep = weight_of(j.m, top);
-        j.l *= keep;
-#pragma unroll
-        for (int e = 0; e < N; ++e) j.o[e] *= keep;
         j.m = top;
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
             const float its = k0 + i <= n ? weight_of(m[i], top) : 0.f;
-            j.l += l[i] * its;
+            // Which of the first two products is rounded is said here: else it is the compiler's choice, and differs between kernels.
+            j.l = __builtin_fmaf(l[i], its, i ? j.l : j.l * keep);
 #pragma unroll
-            for (int e = 0; e < N; ++e) j.o[e] += o[i][e] * its;
+            for (int e = 0; e < N; ++e) j.o[e] = i ? __builtin_fmaf(o[i][e], its, j.o[e]) : __builtin_fmaf(j.o[e], keep, o[0][e] * its);
         }
     }
     j.finish(a, tag, a.heads / a.b.f.n_kv, row, cc);
