@@ -47,7 +47,8 @@ __device__ __forceinline__ uint32_t codes(float a, float b, float s, uint32_t ol
 __device__ __forceinline__ uint32_t again(uint32_t w, float s) {
     const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
     uint32_t r = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a[0] * s, a[1] * s, 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(b[0] * s, b[1] * s, (int)r, true);
+    r = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(b[0] * s, b[1] * s, (int)r, true);
+    return r & ~(((r & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u);  // the conversions may give a NaN either sign: kept as 0x7F
 }
 
 __device__ __forceinline__ uint32_t wave_max(uint32_t m) {
