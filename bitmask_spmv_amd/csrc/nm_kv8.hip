@@ -229,13 +229,15 @@ __device__ __forceinline__ void store_bounds(const AppendShared<D> &sh, const Sc
     if (threadIdx.x == 0) *reinterpret_cast<uint32_t *>(scales) = (uint32_t)sc.kbyte | (uint32_t)sc.vbyte << 8;
 }
 
-// Up to kFewTokens new tokens of a block and head: a lane has two channels of a token.  Little code, which is run once and read from
-// memory (48 sequences, a token each: 13.0 us by the code for many tokens, 6.7 by this).
-constexpr int kFewTokens = 8;
-template <int D>
+// Few new tokens of a block and head: a lane has two channels of a token, the workgroup few_at_once of them, PASSES times.  Little code,
+// which is run once and read from memory.  Calls of 48 sequences, 32 / 8 heads of 128, by the code for many tokens and by 2, 4 and 8
+// passes of this: 1 token each 13.2 us and 7.0 (2), 7.5 (4); 16 tokens 14.6 and 10.3 (4), 10.9 (8); 32 tokens 16.5 and 14.3 (8);
+// 512 sequences of 32 tokens 121 and 123 (8).
+constexpr int few_at_once(int dim) { return kThreads / (dim / 2); }
+template <int D, int PASSES>
 __device__ __forceinline__ void append_few(const Kv8Batch &b, const KvRows &k, const KvRows &v, const KvRotation &r, const Unit &u, int head,
                                            AppendShared<D> &sh) {
-    constexpr int kLanes = D / 2, kAtOnce = 4 * kWave / kLanes, kPasses = kFewTokens / kAtOnce;  // lanes to a token, tokens of the workgroup
+    constexpr int kLanes = D / 2, kAtOnce = few_at_once(D), kPasses = PASSES;  // lanes to a token, tokens of the workgroup
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int at = head * b.f.blocks() + u.in_page;
     uint8_t *block = u.page + at * b.f.block_bytes();
@@ -568,8 +570,12 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Batch b, KvRows
     if (i < blocks) {
         Unit u;
         if (!find_unit(b, i / b.f.n_kv, threadIdx.x & 63, u) || !u.page) return;  // the whole workgroup
-        if (u.hi - u.lo <= kFewTokens)
-            append_few<D>(b, k, v, r, u, i % b.f.n_kv, sh);
+        if (u.hi - u.lo <= 2 * few_at_once(D))
+            append_few<D, 2>(b, k, v, r, u, i % b.f.n_kv, sh);
+        else if (u.hi - u.lo <= 4 * few_at_once(D))
+            append_few<D, 4>(b, k, v, r, u, i % b.f.n_kv, sh);
+        else if (u.hi - u.lo <= 8 * few_at_once(D) && u.hi - u.lo < 64)
+            append_few<D, 8>(b, k, v, r, u, i % b.f.n_kv, sh);
         else
             append<D>(b, k, v, r, u, i % b.f.n_kv, sh);
     } else {
