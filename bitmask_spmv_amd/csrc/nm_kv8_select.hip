@@ -1122,10 +1122,17 @@ __global__ __launch_bounds__(kTileWaves *kWave) void kv8_select_tile_kernel(Kv8S
 constexpr int kFewItems = 512, kSplitBlocks = 2048;
 bool split(int64_t items, int64_t room) { return items <= kFewItems && room > kSplitBlocks; }
 
+// Sixteen rows a workgroup where there are that many of a sequence and more choices than the machine makes side by side.  By single rows
+// and by tiles, 8 heads: 16 sequences of 5 rows behind 16K tokens 13.1 and 16.6 us, of 16 (2048 choices) 19.6 and 20.4, of 24 26.9 and
+// 21.2; a lone one's 128 rows 16.6 and 20.8, 512 rows 44.1 and 22.5; 64 sequences of 12 rows behind 8K 34.0 and 37.1, of 16 43.7 and 40.8.
+constexpr int kTileItems = 2048;
+bool by_tiles(int64_t T, int64_t S, int64_t items, int64_t room) { return room <= kOneWave && T >= kTileRows * S && items > kTileItems; }
+
 template <int D>
 hipError_t launch(const Kv8Select &a, void *ws, hipStream_t st) {
     const int64_t room = (int64_t)a.b.cols * a.b.f.blocks();
-    if (room <= kOneWave && (int64_t)a.b.T >= 4 * (int64_t)a.b.S) {
+    const int64_t items = (int64_t)a.b.T * a.b.f.n_kv;
+    if (by_tiles(a.b.T, a.b.S, items, room)) {
         const int64_t tiles = a.b.T / kTileRows + a.b.S;
         const size_t lds = (size_t)kTileRows * room * sizeof(uint64_t);
         if (lds + sizeof(TileShared<D>) > (64 << 10)) {
@@ -1136,7 +1143,6 @@ hipError_t launch(const Kv8Select &a, void *ws, hipStream_t st) {
         kv8_select_tile_kernel<D><<<(unsigned)(tiles * a.b.f.n_kv), kTileWaves * kWave, lds, st>>>(a, (int)room);
         return hipGetLastError();
     }
-    const int64_t items = (int64_t)a.b.T * a.b.f.n_kv;
     Left left = {};
     if (split(items, room)) {
         left.parts = (int)((room + kPart - 1) / kPart);
@@ -1162,7 +1168,7 @@ hipError_t launch(const Kv8Select &a, void *ws, hipStream_t st) {
 
 size_t kv8_select_workspace(int64_t T, int64_t S, int n_kv, int64_t blocks) {
     const int64_t items = T * n_kv, parts = (blocks + kPart - 1) / kPart;
-    if ((blocks <= kOneWave && T >= 4 * S) || !split(items, blocks)) return 0;
+    if (!split(items, blocks)) return 0;
     return (size_t)(items * (parts * kPart + parts + 1)) * sizeof(uint32_t);
 }
 

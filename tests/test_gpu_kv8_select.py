@@ -214,3 +214,41 @@ def test_pages_that_were_never_written(rows, lens):
                 assert (x >= 0).all() and (x <= own).all()
                 pages = table[i, x * 64 // ps]
                 assert ((pages >= 0) & (pages < N)).all()
+
+
+@pytest.mark.parametrize("kind", ["plain", "alike", "not finite", "pages", "loud"])
+@pytest.mark.parametrize("rows,lens,Hq,H,D,ps,top,first,last", [
+    ([129], [5000], 32, 16, 128, 64, 9, 1, 1), ([260], [64000], 8, 8, 64, 512, 40, 0, 2), ([130, 3], [700, 9000], 16, 16, 128, 512, 100, 2, 3),
+    ([40, 17, 0, 31, 9], [40, 900, 64, 31, 300], 32, 32, 64, 128, 3, 0, 0)])
+def test_sixteen_rows_a_workgroup(rows, lens, Hq, H, D, ps, top, first, last, kind):
+    """More than 2048 choices, of sequences of 16 rows and more on average."""
+    say("sixteen rows", rows, lens, Hq, H, D, ps, top, kind)
+    assert sum(rows) * H > 2048 and sum(rows) >= 16 * len(rows)
+
+    def change(g, cache, table, q):
+        _, b, s = sections(cache, ps, H, D)
+        if kind == "alike":
+            b[:], s[:] = b[:1, :, :1], 120
+        if kind == "not finite":
+            q[3, 0, 1], q[7, -1, 5], q[20] = np.inf, np.nan, 0
+        if kind == "pages":
+            bad = g.random(table.shape) < 0.3
+            table[bad] = np.where(g.random(table.shape) < 0.5, -1, len(cache))[bad]
+        if kind == "loud":
+            s[g.random(s.shape) < 0.2] = 182  # among quiet ones: first scores decide about few blocks
+    select_case(len(rows) * D, rows, lens, Hq, H, D, ps, top, first, last, change=change, extra=1)
+
+
+def test_sixteen_rows_a_workgroup_behind_a_wide_table():
+    """A table of 1024 blocks, the most that such rows' scores have room for, at the larger dimension."""
+    say("sixteen rows, wide")
+    g = np.random.default_rng(9)
+    ps, Hq, H, D, rows, lens = 512, 16, 8, 128, [300], [20000]
+    table, kv_len, q_start, N = batch(g, rows, lens, ps)
+    wide = np.full((1, 1024 * 64 // ps), -1, dtype=np.int32)
+    wide[:, : table.shape[1]] = table
+    cache = filled_cache(g, N, ps, H, D)
+    poison(cache, table, kv_len, ps, H, D)
+    q = bf16(g.standard_normal((rows[0], Hq, D)))
+    want = kv8.select(q, cache, wide, kv_len, q_start, ps, H, 20, 1, 1)
+    assert (run_select(q, cache, wide, kv_len, q_start, H, ps, 20, 1, 1) == want).all()
