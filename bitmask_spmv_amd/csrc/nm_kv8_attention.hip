@@ -77,23 +77,24 @@ __device__ __forceinline__ Operand read_query(const uint16_t *from, bool real, c
 }
 
 // Where the blocks of one head lie: lane i holds the address and the scales of a block and its number, so that a walk reads the page table
-// once for kAhead blocks.  Without a valid page the address is that of page 0, so that loads need no branch, and
-// the block's bit in `valid` is clear.
+// once for kAhead blocks.  Without a valid page, and without a place in [from, upto], those that some row sees, the address is that of
+// page 0, so that loads need no branch, the scales are 1 (what was never written may be scales that are no numbers, and values of 0 times
+// one are none either), and the block's bit in `valid` is clear.
 struct Blocks {
     static constexpr int kAhead = 60;  // of 64: a walk looks up to three blocks ahead
     uint32_t lo, hi, scales;
     int block;
     uint64_t valid;
-    __device__ void load(const Kv8Batch &b, const int32_t *row, int head, int mine) {
+    __device__ void load(const Kv8Batch &b, const int32_t *row, int head, int mine, int from, int upto) {
         block = mine;
         const int per = b.f.blocks(), col = block >= 0 ? block / per : 0;
         int page = block >= 0 && col < b.cols ? row[col] : -1;
-        const bool ok = page >= 0 && page < b.num_pages;
+        const bool ok = page >= 0 && page < b.num_pages && block >= from >> 6 && block <= upto >> 6;
         if (!ok) page = 0;
         valid = __ballot(ok);
         const uint32_t at = (uint32_t)(head * per + (ok ? block & (per - 1) : 0));
         const uint8_t *p = b.cache + (uint64_t)page * (uint64_t)b.f.page_bytes();
-        scales = *reinterpret_cast<const uint32_t *>(p + b.f.scales_at() + at * 4);
+        scales = ok ? *reinterpret_cast<const uint32_t *>(p + b.f.scales_at() + at * 4) : 0x7F7Fu;
         const uint64_t k = (uint64_t)(uintptr_t)p + (uint64_t)at * (uint32_t)b.f.block_bytes();
         lo = (uint32_t)k;
         hi = (uint32_t)(k >> 32);
@@ -214,14 +215,17 @@ __device__ __forceinline__ void walk(const Kv8Attention &a, const Rows &r, int f
                                      int lane, int wave, Shared<D> *sh, L &&listed) {
     const int group = a.heads / a.b.f.n_kv;
     const int32_t *row = a.b.table + (int64_t)r.s * a.b.ld_table;
+    // keys that any of the rows sees
+    auto first_of = [&](int p) { return a.window > 0 && p >= a.window ? (int)(p - a.window + 1) : 0; };
+    const int any_first = first_of(r.place), any_last = min(r.last, r.see_end - 1);
     Blocks lies;
     int held = b0;
     auto look = [&] {
         if constexpr (SEL) {
             const int b = listed(held + lane);
-            lies.load(a.b, row, r.head, held + lane < b1 && b <= r.place >> 6 ? b : -1);  // behind its own: none
+            lies.load(a.b, row, r.head, held + lane < b1 ? b : -1, any_first, any_last);
         } else {
-            lies.load(a.b, row, r.head, first + held + lane);
+            lies.load(a.b, row, r.head, first + held + lane, any_first, any_last);
         }
     };
     look();
@@ -236,12 +240,10 @@ __device__ __forceinline__ void walk(const Kv8Attention &a, const Rows &r, int f
     const uint16_t *from = a.q.p + t * a.q.ld + h * a.q.hd;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) q[i] = read_query(from + 64 * (i >> 1) + 16 * ln.g + 8 * (i & 1), real, a);
-    // keys that my row sees: [see_first, see_last]; that every row sees, and that any of them sees
+    // keys that my row sees: [see_first, see_last]; that every row sees
     const int place = r.place + qi;
-    auto first_of = [&](int p) { return a.window > 0 && p >= a.window ? (int)(p - a.window + 1) : 0; };
     const int see_last = real ? min(place, r.see_end - 1) : -1, see_first = first_of(place);
     const int all_first = first_of(r.last), all_last = min(r.place, r.see_end - 1);
-    const int any_first = first_of(r.place), any_last = min(r.last, r.see_end - 1);
 
     Tile<D> tl;
     clear(tl);
@@ -523,7 +525,7 @@ __device__ __forceinline__ void prompt(Kv8Attention &a, int tiles, Staged<D> &st
     const int32_t *row = a.b.table + (int64_t)s * a.b.ld_table;
     Blocks lies;
     int held = b_first;  // first of the blocks whose places are held
-    lies.load(a.b, row, head, held + lane);
+    lies.load(a.b, row, head, held + lane, any_from, any_upto);
 
     // this thread's share of a block's keys: token `lane`, units kUnits wave ..
     constexpr int kUnits = D / 64;
@@ -757,7 +759,7 @@ __device__ __forceinline__ void prompt(Kv8Attention &a, int tiles, Staged<D> &st
         do {
             if (b - held == Blocks::kAhead) {
                 held = b;
-                lies.load(a.b, row, head, held + lane);
+                lies.load(a.b, row, head, held + lane, any_from, any_upto);
             }
             step(b, 0, wa, wb, sb, sa);
             step(b, 1, wb, wa, sa, sb);
