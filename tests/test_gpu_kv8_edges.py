@@ -95,3 +95,28 @@ def test_pages_of_a_prompt_that_are_not_there(ps, window, D):
     table, kv_len, q_start, cache = without_page_zero(g, rows, [1300, 900, 400], ps, H, D)
     table[0, 2], table[0, 3], table[1, 0], table[0, table.shape[1] - 2], table[2, 0] = -1, len(cache), 2**31 - 1, -5, -(2**31)
     prompt_rows(g, rows, kv_len, table, cache, q_start, Hq, H, D, ps, window)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 1, 63, 64, 700])
+@pytest.mark.parametrize("rows,lens,longer", [([1100], [1200], 300), ([1100, 5], [700, 3], 0), ([600, 500, 2], [1000, 900, 70], 600)])
+def test_prompts_at_the_ends_of_table_and_sequence(rows, lens, longer, window, D):
+    """Lengths behind the table's last column (`longer` tokens), more rows than places, windows shorter than a block."""
+    say("prompt, ends", rows, lens, longer, window, D)
+    g = np.random.default_rng(len(rows) + window)
+    H, Hq, ps = 2, 64, 64
+    table, kv_len, q_start, cache = without_page_zero(g, rows, lens, ps, H, D, extra_cols=0)
+    kv_len = kv_len + np.array([longer] + [0] * (len(rows) - 1), dtype=np.int32)
+    if longer:  # what poison left behind the old end is looked at now
+        cache[1:] = filled_cache(g, len(cache) - 1, ps, H, D)
+    prompt_rows(g, rows, kv_len, table, cache, q_start, Hq, H, D, ps, window, drawn=2)
+
+
+def test_prompts_of_one_token_and_many():
+    """Single tokens, drafts and prompts in one call, over pages of every size."""
+    say("prompt, mixed")
+    for ps in (64, 128, 256, 512):
+        g = np.random.default_rng(ps)
+        rows, lens = [1, 600, 4, 0, 33, 500], [2000, 600, 90, 5, 33, 1100]
+        table, kv_len, q_start, cache = without_page_zero(g, rows, lens, ps, 4, 128)
+        prompt_rows(g, rows, kv_len, table, cache, q_start, 20, 4, 128, ps, 0, drawn=3)
