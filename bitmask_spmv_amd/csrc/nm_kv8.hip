@@ -5,7 +5,7 @@
 // E the biased exponent of the largest magnitude, which lands in (224, 448], 448 the largest E4M3 number.  A scale never
 // shrinks while tokens of the block are there: new tokens that need a larger one have the earlier ones
 // rounded again to it, which is exact but for numbers that become subnormal.  The ends 63 and 182 keep magnitudes below 2^64, so that
-// sums over any number of keys and values stay in range.  Rotated keys are products and one sum in 64 bits, rounded once.
+// sums over any number of keys and values stay in range.  Rotated keys and queries are products and one sum in 64 bits, rounded once.
 //
 // A workgroup takes one block and head: the block's largest magnitude has to be known before any of it is stored, and
 // then everything it stores is in its registers.  Keys: a thread has 16 channels of one token (two runs of 8 where the pairs
@@ -22,6 +22,7 @@ constexpr int kLow = 63, kHigh = 182;  // scale bytes
 constexpr uint32_t kNaN8 = 0x7F;
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ float pow2_byte(uint32_t byte) { return __uint_as_float(byte << 23); }
 
@@ -30,6 +31,12 @@ __device__ __forceinline__ float pow2_byte(uint32_t byte) { return __uint_as_flo
 __device__ __forceinline__ float narrowed(double d) {
     const uint32_t lo = (uint32_t)__double2loint(d), hi = (uint32_t)__double2hiint(d);
     return (float)__hiloint2double((int)(hi | (lo != 0u)), 0);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    union { bf16x2 h; uint32_t u; } c;
+    c.h = __builtin_convertvector((f32x2){a, b}, bf16x2);
+    return c.u;
 }
 
 __device__ __forceinline__ int scale_byte(uint32_t top) {  // bits of the largest magnitude, fp32
@@ -153,14 +160,14 @@ struct Runs {
 
 __device__ __forceinline__ float channel(const u32x4 &w, int i) { return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); }
 
-// x[0..7] of run a, x[8..15] of run b -> rotated; T the arithmetic's type.
-template <class T, class F>
+// x[0..7] of run a, x[8..15] of run b -> rotated.
+template <class F>
 __device__ __forceinline__ void rotate(const u32x4 &a, const u32x4 &b, const Turn &t, bool interleaved, F &&put) {
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
         const int i = interleaved ? 2 * p : p, j = interleaved ? 2 * p + 1 : p + 8;
-        const T x = (T)(i < 8 ? channel(a, i & 7) : channel(b, i & 7)), y = (T)(j < 8 ? channel(a, j & 7) : channel(b, j & 7));
-        const T c = (T)t.x[p >> 1][2 * (p & 1)], s = (T)t.x[p >> 1][2 * (p & 1) + 1];
+        const double x = i < 8 ? channel(a, i & 7) : channel(b, i & 7), y = j < 8 ? channel(a, j & 7) : channel(b, j & 7);
+        const double c = t.x[p >> 1][2 * (p & 1)], s = t.x[p >> 1][2 * (p & 1) + 1];
         put(i, __builtin_elementwise_fma(x, c, -(y * s)));
         put(j, __builtin_elementwise_fma(y, c, x * s));
     }
@@ -403,9 +410,9 @@ __device__ __forceinline__ void append(const Kv8Batch &b, const KvRows &k, const
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
         if (run.turned && r.interleaved) {
-            rotate<double>(ka[p], kb[p], turn[p], true, [&](int i, double d) { y[p][i] = narrowed(d); });
+            rotate(ka[p], kb[p], turn[p], true, [&](int i, double d) { y[p][i] = narrowed(d); });
         } else if (run.turned) {
-            rotate<double>(ka[p], kb[p], turn[p], false, [&](int i, double d) { y[p][i] = narrowed(d); });
+            rotate(ka[p], kb[p], turn[p], false, [&](int i, double d) { y[p][i] = narrowed(d); });
         } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i) y[p][i] = channel(i < 8 ? ka[p] : kb[p], i & 7);
@@ -544,16 +551,16 @@ __device__ __forceinline__ void turn_queries(const Kv8Batch &b, const KvRotation
     for (int h = lane / kSlots; h < heads; h += kAtOnce) {
         u32x4 a = *reinterpret_cast<const u32x4 *>(from + h * q.hd + run.a), c = *reinterpret_cast<const u32x4 *>(from + h * q.hd + run.b);
         if (run.turned) {
-            uint32_t w[16];
-            auto put = [&](int i, float f) { w[i] = f32_to_bf16_rne(f); };
+            float w[16];
+            auto put = [&](int i, double d) { w[i] = narrowed(d); };
             if (r.interleaved)
-                rotate<float>(a, c, turn, true, put);
+                rotate(a, c, turn, true, put);
             else
-                rotate<float>(a, c, turn, false, put);
+                rotate(a, c, turn, false, put);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                a[i] = w[2 * i] | w[2 * i + 1] << 16;
-                c[i] = w[8 + 2 * i] | w[9 + 2 * i] << 16;
+                a[i] = pack_bf16(w[2 * i], w[2 * i + 1]);
+                c[i] = pack_bf16(w[8 + 2 * i], w[9 + 2 * i]);
             }
         }
         *reinterpret_cast<u32x4 *>(to + h * out.hd + run.a) = a;

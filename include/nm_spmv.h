@@ -492,8 +492,8 @@ nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int 
  * written, read as zeros, left out.
  *
  * nm_kv8_append -- stores rows of k and v, after a rotation if there is one.  With (c, s) the cosine and sine of a row's place and
- * pair of channels (x, y): (x c - y s, y c + x s), in fp64 for keys and rounded to E4M3 from there, in fp32 for queries and
- * rounded to bf16.  Pair i is channels (i, i + rotary_dim / 2), or (2i, 2i + 1) where interleaved; channels from rotary_dim on stay.
+ * pair of channels (x, y): (x c - y s, y c + x s), in fp64, rounded from there to E4M3 for keys and to bf16 for queries.  Pair i is
+ * channels (i, i + rotary_dim / 2), or (2i, 2i + 1) where interleaved; channels from rotary_dim on stay.
  * cos_sin: fp32 [positions][ld] of cosine and sine in turn, 16-byte aligned, ld a multiple of 4, positions >= table_cols *
  * page_size; rotary_dim a multiple of 16.  q (n_heads heads) is rotated into q_out (q itself, or memory that does not
  * overlap it); both NULL: keys alone.  A row of q whose place is below 0 or behind the table's last column is left as it is in q_out.
