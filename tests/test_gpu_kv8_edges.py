@@ -9,7 +9,7 @@ import torch
 from oracle import kv8
 from tests.gpu_util import say
 from tests.kv4_util import batch, bf16
-from tests.kv8_util import filled_cache, poison
+from tests.kv8_util import filled_cache, poison, sections
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +120,33 @@ def test_prompts_of_one_token_and_many():
         rows, lens = [1, 600, 4, 0, 33, 500], [2000, 600, 90, 5, 33, 1100]
         table, kv_len, q_start, cache = without_page_zero(g, rows, lens, ps, 4, 128)
         prompt_rows(g, rows, kv_len, table, cache, q_start, 20, 4, 128, ps, 0, drawn=3)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("far", [False, True])
+def test_the_rounding_of_a_dominant_key_cancels_in_prompts(far, D):
+    """Values are all 1, and so is their mean.  One key of each row has nearly all the weight: first place 0, from place 500 on that, with 2^q
+    times the weight, 4 <= q < 8, from place 900 on that, with 2^2q times; the others 2^-9q.  The largest weight is as large in the divisor as it was
+    multiplied; of the rest, at most 2^-4 of it, roundings are 2^-12 of the result, and fp32 sums 1300 x 2^-23: less than half a step
+    of bf16 below 1, 2^-9.  far: scores behind 28672 q0 in fp32, for all keys of a row alike."""
+    say("dominant key", far, D)
+    g = np.random.default_rng(D)
+    rows, lens, H, Hq, ps = [1100, 200], [1100, 900], 2, 32, 64
+    table, kv_len, q_start, cache = without_page_zero(g, rows, lens, ps, H, D)
+    v, _, s = sections(cache, ps, H, D)
+    kat, vat = kv8.places(D)
+    v[...], s[...] = 0, 127
+    v[:, :, :, vat.reshape(-1)] = 0x38
+    v[:, :, :, kat[:, 0]] = kv8.encode(np.array(-8.0))
+    v[:, :, :, kat[:, 1]] = kv8.encode(np.array(448.0))
+    for place, x in ((0, 1.0), (500, 2.0), (900, 4.0)):
+        for row in table[:, place // ps]:
+            if row >= 0:
+                v[row, :, 0, kat[place % ps, 0]] = kv8.encode(np.array(x))
+    q = np.zeros((int(q_start[-1]) + 1, Hq, D))
+    q[..., 0] = bf16(g.uniform(4, 7.96, q.shape[:2]))
+    if far:
+        q[..., 1] = bf16(g.uniform(-64, 64, q.shape[:2]))
+    assert len(q) * Hq > 64 * torch.cuda.get_device_properties(0).multi_processor_count
+    out, _ = run_attention(q, cache, table, kv_len, q_start, H, ps, 1100, scale=float(np.float32(np.log(2))))
+    assert (out[:-1] == 1).all()
