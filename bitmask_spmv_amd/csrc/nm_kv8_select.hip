@@ -18,6 +18,8 @@
 // Bound by the chain of reads (lengths, page, bounds) and of the choice's steps; by the bytes of the bounds, 2 D + 4 for every 128 D of keys
 // and values, where there are rows enough for all compute units.  16 rows to 64K tokens, 8 heads: 20.9 us for 17 MB; one row of 32K 12.0;
 // 512 rows behind 16K by sixteens 25.
+#include <atomic>
+
 #include "nm_kv_rows.h"
 
 namespace nmk {
@@ -1129,6 +1131,22 @@ bool split(int64_t items, int64_t room) { return items <= kFewItems && room > kS
 constexpr int kTileItems = 2048;
 bool by_tiles(int64_t T, int64_t S, int64_t items, int64_t room) { return room <= kOneWave && T >= kTileRows * S && items > kTileItems; }
 
+// Dynamic LDS beyond 64 KB has to be asked for, once a device: for the widest table, so that calls of other host threads need no less.
+template <int D>
+hipError_t allow_tile_lds(size_t bytes) {
+    static std::atomic<uint64_t> done{0};
+    if (bytes + sizeof(TileShared<D>) <= 64 * 1024) return hipSuccess;
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return hipSuccess;
+    e = hipFuncSetAttribute((const void *)kv8_select_tile_kernel<D>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                            kTileRows * kOneWave * (int)sizeof(uint64_t));
+    if (e == hipSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
+    return e;
+}
+
 template <int D>
 hipError_t launch(const Kv8Select &a, void *ws, hipStream_t st) {
     const int64_t room = (int64_t)a.b.cols * a.b.f.blocks();
@@ -1136,11 +1154,8 @@ hipError_t launch(const Kv8Select &a, void *ws, hipStream_t st) {
     if (by_tiles(a.b.T, a.b.S, items, room)) {
         const int64_t tiles = a.b.T / kTileRows + a.b.S;
         const size_t lds = (size_t)kTileRows * room * sizeof(uint64_t);
-        if (lds + sizeof(TileShared<D>) > (64 << 10)) {
-            const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kv8_select_tile_kernel<D>),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-            if (e != hipSuccess) return e;
-        }
+        const hipError_t e = allow_tile_lds<D>(lds);
+        if (e != hipSuccess) return e;
         kv8_select_tile_kernel<D><<<(unsigned)(tiles * a.b.f.n_kv), kTileWaves * kWave, lds, st>>>(a, (int)room);
         return hipGetLastError();
     }
