@@ -13,8 +13,10 @@
 //
 // Single rows: a workgroup takes a row and head, the three pieces are three columns of the instruction.  Many rows of a sequence: 16 rows a
 // workgroup are its columns, and a block's bounds are read once for them.  One wave has the scores of up to 1024 blocks in registers
-// and finds the last one taken bit by bit, from the first bit that differs until as many are above as are asked for, without a barrier;
-// for more blocks a workgroup counts 8 bits at a time in LDS.
+// and searches for the last one taken: it counts the scores at or above one after another that it interpolates between one with more above
+// it and one with fewer, until as many are above as are asked for, without a barrier; behind more blocks a workgroup does the same, its counts meet
+// in LDS.  What that leaves to scores in 64 bits is ranked directly, up to 64 blocks; more of them, as where many are alike, and rows whose queries
+// are not finite go by the bits that keys differ in: one at a time by one wave (choose), 8 at a time by a workgroup (choose_among_many).
 // Bound by the chain of reads (lengths, page, bounds) and of the choice's steps; by the bytes of the bounds, 2 D + 4 for every 128 D of keys
 // and values, where there are rows enough for all compute units.  16 rows to 64K tokens, 8 heads: 20.9 us for 17 MB; one row of 32K 12.0;
 // 512 rows behind 16K by sixteens 25.
@@ -99,10 +101,12 @@ __device__ __forceinline__ float number(uint32_t u) { return __uint_as_float(u ^
 constexpr uint64_t kAlike = 1ull << 63;  // every score of a row with queries that are not finite
 
 // How far a first score may be off.  The sum of the magnitudes of its products is at most 448 times `size`, the sum of the magnitudes of the query
-// sums; each of eight instructions is taken to cut its sum four times by a unit in the last place (2^-23): 2^-18 in all (2^-20.9 is the
-// most that 80 million random sums were off); query sums of `group` heads may be off by group 2^-24; and whatever is below 2^-126.
+// sums.  Each of the eight instructions (dim 64: four) that multiply the first pieces is taken to cut its sum four times by a unit in the last place
+// (2^-23): 2^-18.  Those of the second and the third pieces, 2^-8 and 2^-16 as large, cut as much of that less, whether they have columns of their own
+// or, in a tile, go into the same sum, the smallest first; adding the columns is off by 2^-23: with them less than 2^-18 (1 + 2^-4) (2^-20.9 is
+// the most that 80 million random sums were off).  Query sums of `group` heads may be off by group 2^-24; and whatever is below 2^-126.
 __device__ __forceinline__ float slack(float size, int group, int scale) {
-    return __builtin_ldexpf(__builtin_fmaf(size, 448.f * __builtin_fmaf((float)group, 0x1p-24f, 0x1p-18f), 0x1p-100f), scale - 127);
+    return __builtin_ldexpf(__builtin_fmaf(size, 448.f * __builtin_fmaf((float)group, 0x1p-24f, 0x1.1p-18f), 0x1p-100f), scale - 127);
 }
 
 __device__ __forceinline__ float channel(const u32x4 &w, int i) { return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); }
@@ -456,35 +460,35 @@ struct Survey {
 // Which bin of the pass the `left`-th largest of its keys is in, how many are in larger ones and in it.  The whole workgroup.
 __device__ __forceinline__ void count_digits(const uint64_t *key, int n, int left, const Digits &g, Board &sh) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-                for (int i = threadIdx.x; i < 256; i += blockDim.x) sh.bins[i] = 0;
-                __syncthreads();
-                for (int i = threadIdx.x; i < n; i += blockDim.x) {
-                    const uint64_t k = key[i];
-                    if (g.of(k)) atomicAdd(&sh.bins[(k >> g.lo) & ((2u << (g.d - g.lo)) - 1)], 1);
-                }
-                __syncthreads();
-                if (wave == 0) {  // lane l has bins 255 - 4 l and the three below
-                    int own[4], sum = 0;
-    #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        own[j] = sh.bins[255 - 4 * lane - j];
-                        sum += own[j];
-                    }
-                    int upto = sum;
-                    for (int m = 1; m < 64; m <<= 1) {
-                        const int o = __shfl_up(upto, m);
-                        if (lane >= m) upto += o;
-                    }
-                    int before = upto - sum;
-                    if (before < left && upto >= left) {
-                        int j = 0;
-                        while (before + own[j] < left) before += own[j++];
-                        sh.bin = 255 - 4 * lane - j;
-                        sh.above = before;
-                        sh.inside = own[j];
-                    }
-                }
-                __syncthreads();
+    for (int i = threadIdx.x; i < 256; i += blockDim.x) sh.bins[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const uint64_t k = key[i];
+        if (g.of(k)) atomicAdd(&sh.bins[(k >> g.lo) & ((2u << (g.d - g.lo)) - 1)], 1);
+    }
+    __syncthreads();
+    if (wave == 0) {  // lane l has bins 255 - 4 l and the three below
+        int own[4], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            own[j] = sh.bins[255 - 4 * lane - j];
+            sum += own[j];
+        }
+        int upto = sum;
+        for (int m = 1; m < 64; m <<= 1) {
+            const int o = __shfl_up(upto, m);
+            if (lane >= m) upto += o;
+        }
+        int before = upto - sum;
+        if (before < left && upto >= left) {
+            int j = 0;
+            while (before + own[j] < left) before += own[j++];
+            sh.bin = 255 - 4 * lane - j;
+            sh.above = before;
+            sh.inside = own[j];
+        }
+    }
+    __syncthreads();
 }
 
 // The whole workgroup.
@@ -578,14 +582,13 @@ template <int D>
 __device__ __forceinline__ void choose_together(uint64_t *key, int n, int top, float off, bool none, const RowBlocks &rb, Doubts &few, int32_t *out,
                                                 Board &sh) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-    const bool one = n <= (int)blockDim.x;  // a round
-    uint32_t most = 0, least = ~0u, own = 0;
+    uint32_t most = 0, least = ~0u;
     int forced = 0, count = 0;
     for (int i0 = 0; i0 < n; i0 += blockDim.x) {
-        own = i0 + threadIdx.x < n ? (uint32_t)(key[i0 + threadIdx.x] >> 32) : 0u;
-        const bool asked = own == ~0u, free = !asked && own != 0;
-        most = free ? max(most, own) : most;
-        least = free ? min(least, own) : least;
+        const uint32_t k = i0 + threadIdx.x < n ? (uint32_t)(key[i0 + threadIdx.x] >> 32) : 0u;
+        const bool asked = k == ~0u, free = !asked && k != 0;
+        most = free ? max(most, k) : most;
+        least = free ? min(least, k) : least;
         forced += __popcll(__ballot(asked));
         count += __popcll(__ballot(free));
     }
@@ -607,11 +610,7 @@ __device__ __forceinline__ void choose_together(uint64_t *key, int n, int top, f
     }
     int turn = 0;
     auto round = [&](auto &&f) {  // of all keys
-        if (one) {
-            f(own);
-        } else {
-            for (int i0 = 0; i0 < n; i0 += blockDim.x) f(i0 + threadIdx.x < n ? (uint32_t)(key[i0 + threadIdx.x] >> 32) : 0u);
-        }
+        for (int i0 = 0; i0 < n; i0 += blockDim.x) f(i0 + threadIdx.x < n ? (uint32_t)(key[i0 + threadIdx.x] >> 32) : 0u);
     };
     auto from_on = [&](uint32_t c) {  // free blocks of key c and above
         int m = 0;
@@ -660,7 +659,7 @@ __device__ __forceinline__ void choose_together(uint64_t *key, int n, int top, f
         __syncthreads();
         for (int i0 = wave * 64; i0 < n; i0 += waves * 64) {
             const int i = i0 + lane;
-            const uint32_t k = one ? own : i < n ? (uint32_t)(key[i] >> 32) : 0u;
+            const uint32_t k = i < n ? (uint32_t)(key[i] >> 32) : 0u;
             const bool doubt = k >= near && k <= sure && k != 0u && k != ~0u;
             if (i < n && !doubt) key[i] = k > sure ? kAsked : 0ull;
             if (doubt && all) key[i] = kAsked;
