@@ -888,8 +888,9 @@ def nm_kv8_select(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor
                   q_start: torch.Tensor, n_kv: int, page_size: int, top: int, first: int = 1, last: int = 1,
                   out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """For each row of q bf16 [T, heads, D] and key/value head the `top` blocks of 64 places whose bound on the heads' sum of
-    scores is largest, the `first` and the `last` blocks of the row's keys in any case -> int32 [T, n_kv, top] in increasing
-    order, -1 behind the last (rows behind the last sequence are left as they are)."""
+    scores is largest, the `first` and the `last` blocks of the row's places in any case (those with a page) -> int32 [T, n_kv, top] in
+    increasing order, -1 behind the last (rows behind the last sequence are left as they are).  page_table: as wide as the longest
+    sequence needs, page_table[:, :columns] of a wider one, is fastest."""
     dev, shape = _where(q, "q"), q.shape
     qr = _kv_rows(q, "q", dev, shape)
     T, Hq, D = shape
@@ -926,7 +927,8 @@ def nm_kv8_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Ten
     """Causal attention of rows q bf16 [T, heads, D] over the cached keys and values of their sequences ->
     (out bf16 [T, heads, D], lse fp32 [T, heads]).  scale: 1 / sqrt(D) unless given.  window: keys a row looks
     back over, itself among them (0: all).  selected int32 [T, n_kv, top]: blocks of 64 places that a row looks at
-    (nm_kv8_select; below 0: none), all unless given.  max_q_len: a hint, the most rows of one sequence."""
+    (nm_kv8_select; below 0: none), all unless given.  max_q_len: a hint, the most rows of one sequence.  page_table may be the
+    first columns of a wider one."""
     dev, shape = _where(q, "q"), q.shape
     qr = _kv_rows(q, "q", dev, shape)
     T, Hq, D = shape

@@ -10,7 +10,7 @@
 // A workgroup takes one block and head: the block's largest magnitude has to be known before any of it is stored, and
 // then everything it stores is in its registers.  Keys: a thread has 16 channels of one token (two runs of 8 where the pairs
 // of the rotation lie half the rotated channels apart); values: a thread has two channels of 16 tokens (D = 64: of 8), whole 16-byte
-// units of the cache.  Memory-bound for prompts (3 of 4K rows, 32 / 8 heads of 128: 277 MB past the L2s in 59 to 64 us), a chain of dependent reads
+// units of the cache.  Memory-bound for prompts (3 of 4K rows, 32 / 8 heads of 128: 275 MB past the L2s in 59 to 64 us), a chain of dependent reads
 // (lengths, page, scales) for single tokens (48 of them 7.0 us).
 #include "nm_kv_rows.h"
 

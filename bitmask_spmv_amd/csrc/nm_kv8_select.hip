@@ -18,8 +18,8 @@
 // in LDS.  What that leaves to scores in 64 bits is ranked directly, up to 64 blocks; more of them, as where many are alike, and rows whose queries
 // are not finite go by the bits that keys differ in: one at a time by one wave (choose), 8 at a time by a workgroup (choose_among_many).
 // Bound by the chain of reads (lengths, page, bounds) and of the choice's steps; by the bytes of the bounds, 2 D + 4 for every 128 D of keys
-// and values, where there are rows enough for all compute units.  16 rows to 64K tokens, 8 heads: 20.9 us for 17 MB; one row of 32K 12.0;
-// 512 rows behind 16K by sixteens 25.
+// and values, where there are rows enough for all compute units.  Traced, 8 heads: 16 rows to 64K tokens 20.7 us for 17 MB; one row of 32K 12.1;
+// 512 rows of up to 264 blocks by sixteens 26.9 (in a graph 24.9; up to 256 blocks, of which a lane holds four and not eight, 21.8).
 #include <atomic>
 
 #include "nm_kv_rows.h"
@@ -959,7 +959,7 @@ __global__ __launch_bounds__(kMaxWaves *kWave) void kv8_choose_kernel(Kv8Select 
 
 // ---- sixteen rows of a sequence and a head ----
 
-constexpr int kTileWaves = 8;  // two rows' choices a wave (with 16 waves registers spill: 512 rows behind 16K tokens 29 us, not 25)
+constexpr int kTileWaves = 8;  // two rows' choices a wave (with 16 waves registers spill: 512 rows behind 16K tokens 29 us in a graph, not 25)
 
 // What the rows of a tile keep in LDS before their keys.
 template <int D>
@@ -1125,7 +1125,7 @@ constexpr int kFewItems = 512, kSplitBlocks = 2048;
 bool split(int64_t items, int64_t room) { return items <= kFewItems && room > kSplitBlocks; }
 
 // Sixteen rows a workgroup where there are that many of a sequence and more choices than the machine makes side by side.  By single rows
-// and by tiles, 8 heads: 16 sequences of 5 rows behind 16K tokens 13.1 and 16.6 us, of 16 (2048 choices) 19.6 and 20.4, of 24 26.9 and
+// and by tiles in a graph, 8 heads: 16 sequences of 5 rows behind 16K tokens 13.1 and 16.6 us, of 16 (2048 choices) 19.6 and 20.4, of 24 26.9 and
 // 21.2; a lone one's 128 rows 16.6 and 20.8, 512 rows 44.1 and 22.5; 64 sequences of 12 rows behind 8K 34.0 and 37.1, of 16 43.7 and 40.8.
 constexpr int kTileItems = 2048;
 bool by_tiles(int64_t T, int64_t S, int64_t items, int64_t room) { return room <= kOneWave && T >= kTileRows * S && items > kTileItems; }

@@ -502,29 +502,33 @@ nm_status nm_kv4_attention(const nm_kv4_batch *batch, const nm_kv4_rows *q, int 
  * what it has, and where it grows, its earlier tokens and bounds are rounded again to the new scale.  Values are rounded to the nearest
  * E4M3 multiple, ties to the even code, magnitudes above 448 (of numbers above 448 * 2^55) to 448.  Bounds of a block without earlier
  * tokens are those of the new ones, else they widen.  (Tokens that a shorter length took back keep their part in scale and bounds until
- * the block begins anew.)  A key that is an infinity or NaN after the rotation is kept as NaN and counts as 0 for scale and
- * bounds; a value that is one is kept as 0, and the key of its token and head as NaN in channel 0: a row that sees the token gets NaN,
- * no other row does.  T * n_kv <= 2^28, S * n_kv <= 2^21.  Blocks are read and written whole: a page that two sequences of a batch
+ * the block begins anew.)  A key that is NaN, or 2^128 or more in magnitude, after the rotation is kept as NaN and counts as 0 for scale and
+ * bounds; a value that is an infinity or NaN is kept as 0, and the key of its token and head as NaN in channel 0: a row that sees the token
+ * gets NaN, no other row does.  T * n_kv <= 2^28, S * n_kv <= 2^21.  Blocks are read and written whole: a page that two sequences of a batch
  * share must not be written by both (nm_kv_resize gives each a page of its own first).
  *
  * nm_kv8_unpack -- the same rows of the cache as bf16 (exact).
  *
  * nm_kv8_attention -- as nm_kv4_attention, with these differences.  Scores are those of the bf16 queries and the cached keys, kept in
- * fp32; weights are rounded to bf16 for the product with the values.  Keys may be NaN (see above), values not.  scale is 0 or between
+ * fp32; weights are rounded to bf16 for the product with the values.  Keys may be NaN (see above), values not; blocks in which a call's rows see
+ * nothing may hold anything.  scale is 0 or between
  * 2^-60 and 2^60 in magnitude; sum_c |q_c K_jc| and |scale| times it < 2^125 for the keys a row sees.
  * selected (int32 [T][n_kv][top], ld_selected entries from a row to the next) may be NULL; else a row looks, for the heads of each
  * key/value head, at the keys of its `top` blocks selected[t][h][..] alone (block b: places 64 b .. 64 b + 63), as far as j <= p and the
- * window go.  Entries below 0, behind the row's own block or without a page are left out; one that is named twice counts
+ * window go.  Entries below 0, behind the row's own block, before its window or without a page are left out; one that is named twice counts
  * twice.  T * n_heads <= 2^23 then.  Workspace: nm_kv8_attention_workspace_bytes (top 0: no selected blocks).
  *
- * nm_kv8_select -- writes selected[t][h][..] for the rows of the sequences: of the blocks b <= p / 64 that have a page the first
- * `first` and the last `last`, and those with the largest
+ * nm_kv8_select -- writes selected[t][h][..] for the rows of the sequences: of the blocks b <= p / 64 that have a page those with b < first
+ * and those with b > p / 64 - last, and those with the largest
  *     score_b = sum_g sum_c max(q_gc most_bc, q_gc least_bc)
  * over the query heads g of the key/value head h, most and least the block's bounds, a bound on its keys' sum of scores; of equal ones
  * the lowest; `top` in all, in increasing order, -1 behind the last.  Scores are formed in fp64.  A row with an infinity or NaN among the
  * queries of h takes the lowest.  first + last <= top <= 2^14, table_cols * page_size <= 2^20, T * n_kv <= 2^21.  Workspace:
  * nm_kv8_select_workspace_bytes (room = table_cols * page_size), 16-byte aligned; many calls need none; calls that may overlap in time
  * need workspaces of their own.
+ *
+ * Which kernels attention and the choice take goes by the places that a row of the table has room for, as lengths are known on the device alone:
+ * a program with tables for far longer contexts than a batch has gives table_cols for the longest of these (ld_table stays what it is).
  */
 typedef nm_kv4_batch nm_kv8_batch;
 typedef nm_kv4_rows nm_kv8_rows;
